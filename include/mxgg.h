@@ -440,6 +440,143 @@ size_t mxgg_workspace_size(int32_t G);
  * 2^31 or more, other formats). */
 int64_t mxgg_segpad_rows(const int64_t* m_splits, int32_t G, mxgg_format fmt);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The block around the expert layer: the layer norm in front of it, the norm
+ * and clipping of its accumulated gradients, and the whole layer for a few
+ * tokens. Unless said otherwise the conventions above hold; where a pointer is
+ * called "element-aligned", any address that its element type allows is taken,
+ * and leading dimensions are any number of elements from the row length up.
+ * ---------------------------------------------------------------------------
+ */
+
+/* element types of plain (not block-scaled) tensors */
+typedef enum mxgg_dtype { MXGG_BF16 = 0, MXGG_F32 = 1 } mxgg_dtype;
+
+/*
+ * Layer norm, forward. Per row of x: mu = sum x / cols, var = sum (x - mu)^2 /
+ * cols, rstd = 1 / sqrt(var + eps), y = (x - mu) * rstd * weight + bias; fp32
+ * throughout, y rounded once (nearest even).
+ *   x, y        [rows, cols] of `dtype`, leading dimensions ldx, ldy;
+ *               element-aligned; y may be x.
+ *   weight, bias [cols] of `wdtype`, element-aligned; NULL: 1, 0.
+ *   mean, rstd  fp32 [rows], written: what the backward pass reads.
+ * rows in [0, 2^31), cols in [1, 16384], eps >= 0 and finite. rows == 0
+ * returns MXGG_OK. Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_layer_norm_fwd(const void* x, int64_t rows, int64_t cols, int64_t ldx, mxgg_dtype dtype,
+                                const void* weight, const void* bias, mxgg_dtype wdtype, float eps, void* y,
+                                int64_t ldy, float* mean, float* rstd, hipStream_t stream);
+
+/*
+ * Layer norm, backward: with xh = (x - mean) * rstd and g = dy * weight,
+ *   dx = rstd * (g - mean_cols(g) - xh * mean_cols(g * xh))
+ *   dweight = sum_rows dy * xh, dbias = sum_rows dy
+ *   dy, x, dx   [rows, cols] of `dtype`, leading dimensions lddy, ldx, lddx;
+ *               element-aligned; dx may be dy or x.
+ *   weight      [cols] of `wdtype` or NULL (1); mean, rstd from the forward.
+ *   dweight, dbias  fp32 [cols] each, or NULL (not computed).
+ *   accumulate  1: added to what dweight and dbias hold (a main_grad); 0:
+ *               written (zeros when rows == 0).
+ *   ws          mxgg_layer_norm_bwd_workspace(rows, cols) bytes, 16-byte
+ *               aligned, free again when the work on `stream` is done.
+ * The column sums have one fixed order: the same bits from run to run on the
+ * same GPU. Errors: NULL, SHAPE, FORMAT, ALIGN, WORKSPACE, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows,
+                                int64_t cols, mxgg_dtype dtype, const void* weight, mxgg_dtype wdtype,
+                                const float* mean, const float* rstd, void* dx, int64_t lddx, float* dweight,
+                                float* dbias, int32_t accumulate, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+/* 0 for sizes that the call refuses. */
+size_t mxgg_layer_norm_bwd_workspace(int64_t rows, int64_t cols);
+
+typedef enum mxgg_norm {
+  MXGG_NORM_L2 = 0,  /* square root of the sum of squares over all tensors */
+  MXGG_NORM_MAX = 1  /* largest magnitude                                  */
+} mxgg_norm;
+
+/*
+ * The norm of n gradients together.
+ *   grads   HOST array of n device pointers, element-aligned, dense; the
+ *           tensors do not overlap (MXGG_ERR_SHAPE).
+ *   numels  HOST array: elements of each (>= 0); dtypes HOST array: mxgg_dtype
+ *           of each, mixed as the caller likes. The arrays are read only
+ *           during the call.
+ *   total   fp32 [1] on the device, written: the norm (0 for no elements, NaN
+ *           if any element is NaN). Squares are summed in fp64, so it is
+ *           finite wherever fp32 holds it; the order is fixed (the same bits
+ *           from run to run).
+ *   ws      mxgg_grad_norm_workspace(n) bytes, 16-byte aligned.
+ * Errors: NULL, SHAPE, FORMAT, ALIGN, WORKSPACE, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_grad_norm(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n,
+                           mxgg_norm kind, float* total, void* ws, size_t ws_bytes, hipStream_t stream);
+size_t mxgg_grad_norm_workspace(int64_t n);
+
+/*
+ * mxgg_grad_norm, then every gradient scaled in place by
+ * min(1, max_norm / (total + 1e-6)), rounded to its type (nearest even). When
+ * the factor is 1 nothing is written. A NaN norm makes every gradient NaN, an
+ * infinite one 0 (and NaN where it was infinite): *total says so. max_norm >= 0
+ * and finite (MXGG_ERR_SHAPE).
+ */
+mxgg_status mxgg_clip_grad_norm(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n,
+                                mxgg_norm kind, float max_norm, float* total, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
+
+/*
+ * Only the scaling, by a norm that the caller holds on the device: the norm
+ * over several ranks' gradients, combined from each rank's mxgg_grad_norm.
+ */
+mxgg_status mxgg_clip_grads_with_norm(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n,
+                                      float max_norm, const float* total, hipStream_t stream);
+
+/* tokens and choices per token that mxgg_moe_layer takes */
+#define MXGG_MOE_MAX_TOKENS 64
+#define MXGG_MOE_MAX_TOP_K 16
+/* flags of mxgg_moe_layer */
+#define MXGG_MOE_RENORMALIZE 1u
+
+/*
+ * A whole expert layer for a few tokens (decoding): routing, gate and up
+ * projections, SiLU gating, down projection and the weighted sum, on weights
+ * quantized as for the grouped GEMMs; activations are bf16 and not quantized.
+ *   x         bf16 [tokens, hidden], leading dimension ldx (multiple of 8).
+ *   logits    [tokens, experts] of `ldtype`, leading dimension ldl: the gate's
+ *             output, element-aligned. Per token the top_k largest are chosen,
+ *             equal ones by the lowest index; -inf is never chosen; NaN ranks
+ *             above all (and makes the token's weights and output NaN).
+ *   weights of the choices: softmax over the chosen logits with
+ *             MXGG_MOE_RENORMALIZE, else over all of the token's logits.
+ *   w13_q/_s  [experts * 2 * inner, hidden] quantized along hidden: expert e's
+ *             `inner` gate rows, then its `inner` up rows.
+ *   w2_q/_s   [experts * hidden, inner] quantized along inner.
+ *   w_fmt     MXGG_MXFP4 or MXGG_MXFP8 (hidden, inner multiples of 32; scales
+ *             block-major), with MXGG_KBLOCK_ROWS for codes in 64-byte K
+ *             blocks (multiples of 128); MXGG_FP8_128x128 / _P2 (multiples of
+ *             128). As mxgg_quantize_rowwise writes them.
+ *   out       bf16 [tokens, hidden], dense: out[t] = sum over the token's
+ *             choices of weight * W2_e (silu(W1_e x[t]) * (W3_e x[t])); zeros
+ *             when nothing was chosen. Products and sums fp32; the inner
+ *             activation is rounded to bf16, as between two grouped products.
+ *   ids       int32 [tokens, top_k], written: the chosen experts in falling
+ *             order, -1 where fewer than top_k logits are above -inf.
+ *   weights   fp32 [tokens, top_k], written: 0 where ids is -1.
+ *   ws        mxgg_moe_layer_workspace(...) bytes, 16-byte aligned.
+ * tokens in [0, 64], top_k in [1, min(16, experts)], experts in [1, 512],
+ * hidden and inner at most 65536. tokens == 0 returns MXGG_OK. The sums have
+ * one fixed order (no atomics). Errors: NULL, SHAPE, FORMAT, ALIGN, WORKSPACE,
+ * DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64_t ldl, mxgg_dtype ldtype,
+                           int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k,
+                           const void* w13_q, const void* w13_s, const void* w2_q, const void* w2_s,
+                           mxgg_format w_fmt, uint32_t flags, void* out, int32_t* ids, float* weights, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+/* 0 for sizes that the call refuses. */
+size_t mxgg_moe_layer_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner);
+
 /* Static text for a status code. */
 const char* mxgg_status_string(mxgg_status status);
 

@@ -22,6 +22,10 @@ FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8, "fp8_1x128": FP8_1x128, "fp8_128x128"
            "fp8_1x128_p2": FP8_1x128_P2, "fp8_128x128_p2": FP8_128x128_P2}
 POW2_SCALES = 1
 MAX_EXPERTS = 512
+# mxgg_dtype, mxgg_norm and the limits and flags of mxgg_moe_layer
+BF16, F32 = 0, 1
+NORM_L2, NORM_MAX = 0, 1
+MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_RENORMALIZE = 64, 16, 1
 # mxgg_scale_layout: OR-ed into an MX format to state the layout of its scales
 LAYOUT_BLOCK_MAJOR, LAYOUT_ROW_MAJOR, LAYOUT_MFMA, LAYOUT_MASK = 0x000, 0x100, 0x200, 0xF00
 # MX code layouts: row-wise / column-wise codes in 64-byte K blocks
@@ -43,6 +47,7 @@ class MxggError(RuntimeError):
 
 _vp, _i64, _i32, _u32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
 _i64p = ctypes.POINTER(ctypes.c_int64)
+_f32, _i32p, _vpp = ctypes.c_float, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_void_p)
 
 _SIGS = {
     "mxgg_quantize_rowwise": [_vp, _i64, _i64, _i64, _i32, _u32, _vp, _vp, _vp],
@@ -54,6 +59,20 @@ _SIGS = {
     "mxgg_grouped_wgrad": [_vp, _vp, _vp, _vp, _i32, _i64p, _i32, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _sz,
                            _vp],
     "mxgg_mx_scales_relayout": [_vp, _i32, _i64, _i64, _vp, _i32, _vp],
+    "mxgg_layer_norm_fwd": [_vp, _i64, _i64, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _i64, _vp, _vp, _vp],
+    "mxgg_layer_norm_bwd": [_vp, _i64, _vp, _i64, _i64, _i64, _i32, _vp, _i32, _vp, _vp, _vp, _i64, _vp, _vp, _i32,
+                            _vp, _sz, _vp],
+    "mxgg_grad_norm": [_vpp, _i64p, _i32p, _i64, _i32, _vp, _vp, _sz, _vp],
+    "mxgg_clip_grad_norm": [_vpp, _i64p, _i32p, _i64, _i32, _f32, _vp, _vp, _sz, _vp],
+    "mxgg_clip_grads_with_norm": [_vpp, _i64p, _i32p, _i64, _f32, _vp, _vp],
+    "mxgg_moe_layer": [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _u32, _vp,
+                       _vp, _vp, _vp, _sz, _vp],
+}
+# functions that return a size
+_SIZES = {
+    "mxgg_layer_norm_bwd_workspace": [_i64, _i64],
+    "mxgg_grad_norm_workspace": [_i64],
+    "mxgg_moe_layer_workspace": [_i64, _i64, _i64, _i64],
 }
 
 
@@ -68,6 +87,10 @@ def _load():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
+    for name, args in _SIZES.items():
+        fn = getattr(lib, name)
+        fn.argtypes = args
+        fn.restype = _sz
     lib.mxgg_workspace_size.argtypes = [_i32]
     lib.mxgg_workspace_size.restype = _sz
     lib.mxgg_segpad_rows.argtypes = [_i64p, _i32, _i32]
@@ -423,6 +446,215 @@ def mxgg_grouped_wgrad(dycol_q, dycol_s, xcol_q, xcol_s, m_splits, N, K, mpad, m
     return main_grad
 
 
+def _dtype(t, name):
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float32:
+        return F32
+    raise ValueError(f"{name} must be bf16 or fp32, got {str(t.dtype).replace('torch.', '')}")
+
+
+def _rows2d(t, name, shape=None, dtype=None):
+    """Leading dimension of a 2-D tensor with unit inner stride, of the given
+    shape and dtype when they are given."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() and t.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit inner stride")
+    if (shape is not None and tuple(t.shape) != tuple(shape)) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor of shape {tuple(shape)}, got "
+                         f"{str(t.dtype).replace('torch.', '')} {tuple(t.shape)}")
+    return t.stride(0) if t.shape[0] > 1 and t.numel() else t.shape[1]
+
+
+def _cols_vector(t, name, cols):
+    if t is None:
+        return None
+    if tuple(t.shape) != (cols,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape ({cols},), got {tuple(t.shape)}")
+    return _dtype(t, name)
+
+
+def _same_device(like, **others):
+    for name, t in others.items():
+        if t is not None and t.device != like.device:
+            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+
+
+def _ws(ws, need, like):
+    """The caller's workspace, or one from torch's allocator on the current
+    stream (which keeps it from other streams until this one's work is done)."""
+    if ws is None:
+        ws = _torch().empty(need, dtype=_torch().uint8, device=like.device)
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws, ws.numel() * ws.element_size()
+
+
+def mxgg_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None):
+    """x: bf16 or fp32 [rows, cols] (any row stride); weight, bias: [cols], bf16
+    or fp32 alike, None for 1 and 0. Returns (y, mean, rstd): y like x, mean and
+    rstd fp32 [rows]."""
+    torch = _torch()
+    dt = _dtype(x, "x")
+    ldx = _rows2d(x, "x")
+    rows, cols = x.shape
+    wd, bd = _cols_vector(weight, "weight", cols), _cols_vector(bias, "bias", cols)
+    if wd is not None and bd is not None and wd != bd:
+        raise ValueError("weight and bias must have the same dtype")
+    if y is None:
+        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    ldy = _rows2d(y, "y", x.shape, x.dtype)
+    if mean is None:
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    _expect(mean, "mean", (rows,), torch.float32)
+    _expect(rstd, "rstd", (rows,), torch.float32)
+    _same_device(x, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
+    _check(lib.mxgg_layer_norm_fwd(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wd or bd or 0, eps, _ptr(y),
+                                   ldy, _ptr(mean), _ptr(rstd), _stream(x)))
+    return y, mean, rstd
+
+
+def mxgg_layer_norm_bwd(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None, accumulate=False, ws=None):
+    """dy, x: [rows, cols] alike (any row strides); mean, rstd from the forward.
+    Returns (dx, dweight, dbias): dx like x; dweight and dbias fp32 [cols],
+    added to the given ones with accumulate=True. False for dweight or dbias:
+    not computed (None comes back)."""
+    torch = _torch()
+    dt = _dtype(x, "x")
+    ldx = _rows2d(x, "x")
+    rows, cols = x.shape
+    lddy = _rows2d(dy, "dy", x.shape, x.dtype)
+    wd = _cols_vector(weight, "weight", cols)
+    if dx is None:
+        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
+    lddx = _rows2d(dx, "dx", x.shape, x.dtype)
+    grads = []
+    for name, g in (("dweight", dweight), ("dbias", dbias)):
+        if g is None:
+            if accumulate:
+                raise ValueError(f"accumulate=True needs {name} (or {name}=False)")
+            g = torch.empty(cols, dtype=torch.float32, device=x.device)
+        grads.append(None if g is False else _expect(g, name, (cols,), torch.float32))
+    dweight, dbias = grads
+    _expect(mean, "mean", (rows,), torch.float32)
+    _expect(rstd, "rstd", (rows,), torch.float32)
+    _same_device(x, dy=dy, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dweight, dbias=dbias, ws=ws)
+    ws, ws_bytes = _ws(ws, int(lib.mxgg_layer_norm_bwd_workspace(rows, cols)), x)
+    _check(lib.mxgg_layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, rows, cols, dt, _ptr(weight), wd or 0, _ptr(mean),
+                                   _ptr(rstd), _ptr(dx), lddx, _ptr(dweight), _ptr(dbias), 1 if accumulate else 0,
+                                   _ptr(ws), ws_bytes, _stream(x)))
+    return dx, dweight, dbias
+
+
+def _grad_list(grads, total):
+    """The host arrays of a gradient list, and a tensor of its device."""
+    torch = _torch()
+    grads = list(grads)
+    kinds = {torch.bfloat16: BF16, torch.float32: F32}
+    for i, g in enumerate(grads):
+        if g.dtype not in kinds or not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be a contiguous bf16 or fp32 tensor, got "
+                             f"{str(g.dtype).replace('torch.', '')} {tuple(g.shape)} with strides {g.stride()}")
+    n = len(grads)
+    ptrs = (ctypes.c_void_p * max(1, n))(*[g.data_ptr() for g in grads])
+    numels = (ctypes.c_int64 * max(1, n))(*[g.numel() for g in grads])
+    dtypes = (ctypes.c_int32 * max(1, n))(*[kinds[g.dtype] for g in grads])
+    like = grads[0] if grads else total
+    return n, ptrs, numels, dtypes, like
+
+
+def _norm_kind(norm_type):
+    if float(norm_type) == 2.0:
+        return NORM_L2
+    if float(norm_type) == float("inf"):
+        return NORM_MAX
+    raise ValueError(f"norm_type must be 2 or inf, got {norm_type}")
+
+
+def _total(total, like):
+    torch = _torch()
+    if total is None:
+        total = torch.empty((), dtype=torch.float32, device="cuda" if like is None else like.device)
+    if total.dtype != torch.float32 or total.numel() != 1:
+        raise ValueError("total must be one fp32 value")
+    return total
+
+
+def mxgg_grad_norm(grads, norm_type=2.0, total=None, ws=None):
+    """The norm (2 or inf) of all gradients together, an fp32 scalar on their
+    device. grads: contiguous bf16 / fp32 tensors, mixed; they must not
+    overlap."""
+    kind = _norm_kind(norm_type)
+    n, ptrs, numels, dtypes, like = _grad_list(grads, total)
+    total = _total(total, like)
+    ws, ws_bytes = _ws(ws, int(lib.mxgg_grad_norm_workspace(n)), total)
+    _check(lib.mxgg_grad_norm(ptrs, numels, dtypes, n, kind, _ptr(total), _ptr(ws), ws_bytes, _stream(total)))
+    return total
+
+
+def mxgg_clip_grad_norm(grads, max_norm, norm_type=2.0, total=None, ws=None):
+    """grad_norm, then every gradient *= min(1, max_norm / (norm + 1e-6)) in
+    place. Returns the norm (an fp32 scalar on the device; no host wait)."""
+    kind = _norm_kind(norm_type)
+    n, ptrs, numels, dtypes, like = _grad_list(grads, total)
+    total = _total(total, like)
+    ws, ws_bytes = _ws(ws, int(lib.mxgg_grad_norm_workspace(n)), total)
+    _check(lib.mxgg_clip_grad_norm(ptrs, numels, dtypes, n, kind, max_norm, _ptr(total), _ptr(ws), ws_bytes,
+                                   _stream(total)))
+    return total
+
+
+def mxgg_clip_grads_with_norm(grads, max_norm, total):
+    """Scale the gradients in place by min(1, max_norm / (total + 1e-6)); total:
+    fp32 scalar on the device, e.g. combined over ranks from grad_norm."""
+    n, ptrs, numels, dtypes, _ = _grad_list(grads, total)
+    total = _total(total, total)
+    _check(lib.mxgg_clip_grads_with_norm(ptrs, numels, dtypes, n, max_norm, _ptr(total), _stream(total)))
+    return total
+
+
+def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", renormalize=True, out=None, ids=None,
+                   weights=None, ws=None):
+    """The whole expert layer for at most 64 tokens. x: bf16 [tokens, hidden];
+    logits: the gate's output, bf16 or fp32 [tokens, experts]; w13: [experts *
+    2 * inner, hidden] (gate rows, then up rows of each expert) and w2: [experts
+    * hidden, inner] as quantize_rowwise(..., fmt) writes them, fmt "mxfp4",
+    "mxfp8" (also | KBLOCK_ROWS) or "fp8_128x128" (_p2). Returns (out, ids,
+    weights): bf16 [tokens, hidden], int32 and fp32 [tokens, top_k]."""
+    torch = _torch()
+    f = _fmt(fmt)
+    _check_bf16_2d(x)
+    T, H = x.shape
+    ldl = _rows2d(logits, "logits")
+    if logits.shape[0] != T:
+        raise ValueError(f"logits must have {T} rows, got {logits.shape[0]}")
+    E = logits.shape[1]
+    inner = _q_rows(w13_q, f) // (2 * E) if E else 0
+    if (f & 0xFF) not in (MXFP4, MXFP8, FP8_128x128, FP8_128x128_P2):
+        raise ValueError("fmt must be a weight format: mxfp4, mxfp8 or fp8_128x128(_p2)")
+    _expect(w13_q, "w13_q", _q_shape(f, E * 2 * inner, H), torch.uint8)
+    _expect(w13_s, "w13_s", _row_scale_shape(f, E * 2 * inner, H), _sdtype(f))
+    _expect(w2_q, "w2_q", _q_shape(f, E * H, inner), torch.uint8)
+    _expect(w2_s, "w2_s", _row_scale_shape(f, E * H, inner), _sdtype(f))
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
+    _expect(out, "out", (T, H), torch.bfloat16)
+    _expect(ids, "ids", (T, top_k), torch.int32)
+    _expect(weights, "weights", (T, top_k), torch.float32)
+    ws, ws_bytes = _ws(ws, int(lib.mxgg_moe_layer_workspace(T, E, top_k, inner)), x)
+    _check(lib.mxgg_moe_layer(_ptr(x), x.stride(0) if T > 1 else H, _ptr(logits), ldl, _dtype(logits, "logits"), T, H,
+                              inner, E, top_k, _ptr(w13_q), _ptr(w13_s), _ptr(w2_q), _ptr(w2_s), f,
+                              MOE_RENORMALIZE if renormalize else 0, _ptr(out), _ptr(ids), _ptr(weights), _ptr(ws),
+                              ws_bytes, _stream(x)))
+    return out, ids, weights
+
+
 # short names
 quantize_rowwise = mxgg_quantize_rowwise
 quantize_colwise_segpad = mxgg_quantize_colwise_segpad
@@ -435,3 +667,9 @@ workspace_size = mxgg_workspace_size
 segpad_rows = mxgg_segpad_rows
 mx_scale_stride = mxgg_mx_scale_stride
 mx_scales_relayout = mxgg_mx_scales_relayout
+layer_norm_fwd = mxgg_layer_norm_fwd
+layer_norm_bwd = mxgg_layer_norm_bwd
+grad_norm = mxgg_grad_norm
+clip_grad_norm = mxgg_clip_grad_norm
+clip_grads_with_norm = mxgg_clip_grads_with_norm
+moe_layer = mxgg_moe_layer

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxgg.so")
 
-SOURCES = ["api.cpp", "quant_mx.hip", "quant_blockwise.hip", "gemm_mx.hip"]
+SOURCES = ["api.cpp", "quant_mx.hip", "quant_blockwise.hip", "gemm_mx.hip", "layer_norm.hip", "grad_clip.hip",
+           "moe_layer.hip"]
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.
 HIP_FLAGS = [

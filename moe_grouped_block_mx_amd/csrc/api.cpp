@@ -16,10 +16,13 @@
 #include <mutex>
 #include <numeric>
 #include <string>
+#include <vector>
 
 #include "../../include/mxgg.h"
+#include "block_launch.hpp"
 #include "launch.hpp"
 #include "validate.hpp"
+#include "validate_block.hpp"
 
 namespace mxgg {
 namespace {
@@ -111,6 +114,77 @@ SplitArgs make_splits(const int64_t* m, int32_t G) {
   s.G = G;
   for (int32_t g = 0; g < G; ++g) s.m[g] = (int32_t)m[g];
   return s;
+}
+
+// Runs an entry point's body; nothing it throws (only allocations can) leaves
+// the C ABI.
+template <class F>
+mxgg_status guarded(F body) noexcept {
+  try {
+    const Check c = body();
+    return c.ok() ? ok() : finish(c);
+  } catch (...) {
+    g_last_error.clear();
+    return MXGG_ERR_HIP;
+  }
+}
+
+// The non-empty tensors of a gradient list, as many to a launch as its kernel
+// arguments hold.
+std::vector<ClipBatch> clip_batches(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n) {
+  std::vector<ClipBatch> out;
+  for (int64_t i = 0; i < n; ++i) {
+    if (numels[i] == 0) continue;
+    if (out.empty() || out.back().n == kClipTensors) {
+      out.emplace_back();
+      std::memset(&out.back(), 0, sizeof(ClipBatch));
+    }
+    ClipBatch& b = out.back();
+    b.data[b.n] = grads[i];
+    b.numel[b.n] = numels[i];
+    if (dtypes[i] == MXGG_F32) b.f32[b.n / 32] |= 1u << (b.n % 32);
+    b.chunks += (int32_t)((numels[i] + kClipChunk - 1) / kClipChunk);
+    b.first[++b.n] = b.chunks;
+  }
+  return out;
+}
+
+Check check_grads_on_device(void* const* grads, const int64_t* numels, int64_t n, int dev) {
+  for (int64_t i = 0; i < n; ++i)
+    if (numels[i] > 0) MXGG_TRY(check_on_device(grads[i], dev, "a gradient"));
+  return Check{};
+}
+
+// The norm into *total, and with `clip` the scaling by it.
+Check grad_norm_and_clip(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n, int kind,
+                         bool clip, float max_norm, float* total, void* ws, size_t ws_bytes, hipStream_t stream) {
+  MXGG_TRY(check_norm_kind(kind));
+  if (clip) MXGG_TRY(check_max_norm(max_norm));
+  MXGG_TRY(validate_grads(grads, numels, dtypes, n));
+  MXGG_TRY(check_elem_ptr(total, 4, "total"));
+  MXGG_TRY(check_workspace(ws, ws_bytes, mxgg_grad_norm_workspace(n)));
+  const std::vector<ClipBatch> batches = clip_batches(grads, numels, dtypes, n);
+  int cus = 0, dev = 0;
+  MXGG_TRY(stream_device(stream, &dev));
+  MXGG_TRY(device_checks(stream, {{total, "total"}, {ws, "ws"}}, &cus));
+  MXGG_TRY(check_grads_on_device(grads, numels, n, dev));
+  double* part = static_cast<double*>(ws);
+  const bool mx = kind == MXGG_NORM_MAX;
+  int parts = 0;
+  for (const ClipBatch& b : batches) {
+    MXGG_TRY(hip_status(launch_norm_partials(b, mx, part + parts, stream), "gradient norm launch"));
+    parts += clip_groups(b.chunks);
+  }
+  // With a few launches' partials every workgroup of the scaling adds them up
+  // itself, which saves a launch; with more, one workgroup does it first.
+  const bool few = batches.size() <= 2;
+  if (!clip || !few || batches.empty())
+    MXGG_TRY(hip_status(launch_norm_total(part, parts, mx, total, stream), "gradient norm launch"));
+  if (!clip) return Check{};
+  for (size_t i = batches.size(); i-- > 0;)   // backwards: the last read is the most cached
+    MXGG_TRY(hip_status(launch_clip(batches[i], part, few ? parts : 0, mx, max_norm, total, few && i == 0, stream),
+                        "gradient clipping launch"));
+  return Check{};
 }
 
 }  // namespace
@@ -420,6 +494,162 @@ mxgg_status mxgg_grouped_wgrad(const void* dycol_q, const void* dycol_s, const v
   c = hip_status(blk ? launch_grouped_wgrad_blk(p, p2, cus, stream) : launch_grouped_wgrad_mx(p, fp8, cus, stream),
                  "wgrad launch");
   return c.ok() ? ok() : finish(c);
+}
+
+mxgg_status mxgg_layer_norm_fwd(const void* x, int64_t rows, int64_t cols, int64_t ldx, mxgg_dtype dtype,
+                                const void* weight, const void* bias, mxgg_dtype wdtype, float eps, void* y,
+                                int64_t ldy, float* mean, float* rstd, hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_layer_norm_fwd(x, rows, cols, ldx, (int)dtype, weight, bias, (int)wdtype, eps, y, ldy, mean, rstd));
+    if (rows == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{x, "x"}, {weight, "weight"}, {bias, "bias"}, {y, "y"}, {mean, "mean"}, {rstd, "rstd"}},
+                           &cus));
+    NormFwdParams p;
+    p.x = x;
+    p.weight = weight;
+    p.bias = bias;
+    p.y = y;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.rows = rows;
+    p.ldx = ldx;
+    p.ldy = ldy;
+    p.cols = (int32_t)cols;
+    p.eps = eps;
+    return hip_status(launch_layer_norm_fwd(p, dtype == MXGG_F32, wdtype == MXGG_F32, stream), "layer norm launch");
+  });
+}
+
+size_t mxgg_layer_norm_bwd_workspace(int64_t rows, int64_t cols) {
+  if (!check_norm_dims(rows, cols).ok()) return 0;
+  return (size_t)norm_bwd_groups(rows, cols) * 2 * (size_t)cols * sizeof(float);
+}
+
+mxgg_status mxgg_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows, int64_t cols,
+                                mxgg_dtype dtype, const void* weight, mxgg_dtype wdtype, const float* mean,
+                                const float* rstd, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                int32_t accumulate, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_layer_norm_bwd(dy, lddy, x, ldx, rows, cols, (int)dtype, weight, (int)wdtype, mean, rstd, dx, lddx,
+                                     dweight, dbias, accumulate));
+    MXGG_TRY(check_workspace(ws, ws_bytes, mxgg_layer_norm_bwd_workspace(rows, cols)));
+    if (rows == 0 && (accumulate || (!dweight && !dbias))) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{dy, "dy"}, {x, "x"}, {weight, "weight"}, {mean, "mean"}, {rstd, "rstd"}, {dx, "dx"},
+                                    {dweight, "dweight"}, {dbias, "dbias"}, {ws, "ws"}}, &cus));
+    NormBwdParams p;
+    p.dy = dy;
+    p.x = x;
+    p.weight = weight;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dx = dx;
+    p.part = static_cast<float*>(ws);
+    p.rows = rows;
+    p.lddy = lddy;
+    p.ldx = ldx;
+    p.lddx = lddx;
+    p.cols = (int32_t)cols;
+    return hip_status(launch_layer_norm_bwd(p, dtype == MXGG_F32, wdtype == MXGG_F32, dweight, dbias, accumulate != 0,
+                                            stream), "layer norm backward launch");
+  });
+}
+
+size_t mxgg_grad_norm_workspace(int64_t n) {
+  if (n < 0 || n >= ((int64_t)1 << 24)) return 0;
+  return (size_t)((n + kClipTensors - 1) / kClipTensors) * kClipGroups * sizeof(double);
+}
+
+mxgg_status mxgg_grad_norm(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n, mxgg_norm kind,
+                           float* total, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return guarded([&]() -> Check {
+    return grad_norm_and_clip(grads, numels, dtypes, n, (int)kind, false, 0.f, total, ws, ws_bytes, stream);
+  });
+}
+
+mxgg_status mxgg_clip_grad_norm(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n,
+                                mxgg_norm kind, float max_norm, float* total, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  return guarded([&]() -> Check {
+    return grad_norm_and_clip(grads, numels, dtypes, n, (int)kind, true, max_norm, total, ws, ws_bytes, stream);
+  });
+}
+
+mxgg_status mxgg_clip_grads_with_norm(void* const* grads, const int64_t* numels, const int32_t* dtypes, int64_t n,
+                                      float max_norm, const float* total, hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(check_max_norm(max_norm));
+    MXGG_TRY(validate_grads(grads, numels, dtypes, n));
+    MXGG_TRY(check_elem_ptr(total, 4, "total"));
+    const std::vector<ClipBatch> batches = clip_batches(grads, numels, dtypes, n);
+    if (batches.empty()) return Check{};
+    int cus = 0, dev = 0;
+    MXGG_TRY(stream_device(stream, &dev));
+    MXGG_TRY(device_checks(stream, {{total, "total"}}, &cus));
+    MXGG_TRY(check_grads_on_device(grads, numels, n, dev));
+    for (const ClipBatch& b : batches)
+      MXGG_TRY(hip_status(launch_clip(b, nullptr, 0, false, max_norm, const_cast<float*>(total), false, stream),
+                          "gradient clipping launch"));
+    return Check{};
+  });
+}
+
+size_t mxgg_moe_layer_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner) {
+  if (!validate_moe_dims(tokens, 1, inner, experts, top_k).ok()) return 0;
+  return moe_workspace(tokens, experts, top_k, inner).bytes;
+}
+
+mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64_t ldl, mxgg_dtype ldtype,
+                           int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int64_t top_k,
+                           const void* w13_q, const void* w13_s, const void* w2_q, const void* w2_s,
+                           mxgg_format w_fmt, uint32_t flags, void* out, int32_t* ids, float* weights, void* ws,
+                           size_t ws_bytes, hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_moe_layer(x, ldx, logits, ldl, (int)ldtype, tokens, hidden, inner, experts, top_k, w13_q, w13_s,
+                                w2_q, w2_s, (int)w_fmt, flags, out, ids, weights));
+    const MoeWorkspace w = moe_workspace(tokens, experts, top_k, inner);
+    MXGG_TRY(check_workspace(ws, ws_bytes, w.bytes));
+    if (tokens == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{x, "x"}, {logits, "logits"}, {w13_q, "w13_q"}, {w13_s, "w13_s"}, {w2_q, "w2_q"},
+                                    {w2_s, "w2_s"}, {out, "out"}, {ids, "ids"}, {weights, "weights"}, {ws, "ws"}}, &cus));
+    const int f = base_format(format_bits((int)w_fmt));
+    const bool kb = f == MXGG_FP8_128x128 || kblock_bits((int)w_fmt) != 0;
+    uint8_t* at = static_cast<uint8_t*>(ws);
+    MoeParams p;
+    p.x = static_cast<const uint16_t*>(x);
+    p.logits = logits;
+    p.w13_q = static_cast<const uint8_t*>(w13_q);
+    p.w13_s = w13_s;
+    p.w2_q = static_cast<const uint8_t*>(w2_q);
+    p.w2_s = w2_s;
+    p.out = static_cast<uint16_t*>(out);
+    p.ids = ids;
+    p.weights = weights;
+    p.active = reinterpret_cast<int32_t*>(at);
+    p.table = reinterpret_cast<MoeExpert*>(at + w.table);
+    p.share = reinterpret_cast<float*>(at + w.share);
+    p.inner_x = reinterpret_cast<uint16_t*>(at + w.inner);
+    p.ldx = ldx;
+    p.ldl = ldl;
+    p.tokens = (int32_t)tokens;
+    p.experts = (int32_t)experts;
+    p.top_k = (int32_t)top_k;
+    p.hidden = (int32_t)hidden;
+    p.inner = (int32_t)inner;
+    const int64_t rows13 = experts * 2 * inner, rows2 = experts * hidden;
+    const int per_byte = f == MXGG_MXFP4 ? 2 : 1;
+    p.q13_row = kb ? 64 : hidden / per_byte;
+    p.q13_piece = kb ? rows13 * 64 : 64;
+    p.s13_block = mx_scale_stride(rows13);
+    p.q2_row = kb ? 64 : inner / per_byte;
+    p.q2_piece = kb ? rows2 * 64 : 64;
+    p.s2_block = mx_scale_stride(rows2);
+    const MoeFormat mf = f == MXGG_MXFP4 ? kMoeFp4 : f == MXGG_MXFP8 ? kMoeFp8 : kMoeBlock;
+    return hip_status(launch_moe_layer(p, mf, ldtype == MXGG_F32, (flags & MXGG_MOE_RENORMALIZE) != 0, stream),
+                      "expert layer launch");
+  });
 }
 
 }  // extern "C"
