@@ -553,15 +553,18 @@ def _grad_list(grads, total):
     torch = _torch()
     grads = list(grads)
     kinds = {torch.bfloat16: BF16, torch.float32: F32}
+    like = grads[0] if grads else total
+    dev = like.get_device() if like is not None else 0
     for i, g in enumerate(grads):
         if g.dtype not in kinds or not g.is_contiguous():
             raise ValueError(f"gradient {i} must be a contiguous bf16 or fp32 tensor, got "
                              f"{str(g.dtype).replace('torch.', '')} {tuple(g.shape)} with strides {g.stride()}")
+        if g.get_device() != dev or dev < 0:
+            raise ValueError(f"gradient {i} is on {g.device}: all gradients must be on one GPU")
     n = len(grads)
     ptrs = (ctypes.c_void_p * max(1, n))(*[g.data_ptr() for g in grads])
     numels = (ctypes.c_int64 * max(1, n))(*[g.numel() for g in grads])
     dtypes = (ctypes.c_int32 * max(1, n))(*[kinds[g.dtype] for g in grads])
-    like = grads[0] if grads else total
     return n, ptrs, numels, dtypes, like
 
 
@@ -609,8 +612,8 @@ def mxgg_clip_grad_norm(grads, max_norm, norm_type=2.0, total=None, ws=None):
 def mxgg_clip_grads_with_norm(grads, max_norm, total):
     """Scale the gradients in place by min(1, max_norm / (total + 1e-6)); total:
     fp32 scalar on the device, e.g. combined over ranks from grad_norm."""
-    n, ptrs, numels, dtypes, _ = _grad_list(grads, total)
     total = _total(total, total)
+    n, ptrs, numels, dtypes, _ = _grad_list(grads, total)
     _check(lib.mxgg_clip_grads_with_norm(ptrs, numels, dtypes, n, max_norm, _ptr(total), _stream(total)))
     return total
 

@@ -95,16 +95,19 @@ __global__ __launch_bounds__(THREADS) void layer_norm_fwd_kernel(NormFwdParams p
     for (int j = 0; j < N; ++j) s[0] += c[i].get(j);
   row_sum<L, THREADS, 1>(s, lds, 0);
   const float mean = s[0] / (float)p.cols;
+  // squares of (x - mu) / sqrt(C): their sum is the variance, and finite
+  // wherever that is
+  const float root = 1.f / sqrtf((float)p.cols);
   float q[1] = {0.f};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int j = 0; j < N; ++j) {
-      const float d = c[i].get(j) - mean;
+      const float d = (c[i].get(j) - mean) * root;
       q[0] += (i * L + lane) * N + j < p.cols ? d * d : 0.f;
     }
   row_sum<L, THREADS, 1>(q, lds, 1);
-  const float rstd = 1.f / sqrtf(q[0] / (float)p.cols + p.eps);
+  const float rstd = 1.f / sqrtf(q[0] + p.eps);
   if (!on) return;
   if (lane == 0) {
     p.mean[row] = mean;
