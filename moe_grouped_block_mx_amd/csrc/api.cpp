@@ -627,9 +627,10 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     p.out = static_cast<uint16_t*>(out);
     p.ids = ids;
     p.weights = weights;
-    p.active = reinterpret_cast<int32_t*>(at);
+    p.counts = reinterpret_cast<int32_t*>(at);
     p.table = reinterpret_cast<MoeExpert*>(at + w.table);
-    p.share = reinterpret_cast<float*>(at + w.share);
+    p.segments = reinterpret_cast<MoeSegment*>(at + w.segments);
+    p.row_list = reinterpret_cast<MoeRow*>(at + w.rows);
     p.inner_x = reinterpret_cast<uint16_t*>(at + w.inner);
     p.ldx = ldx;
     p.ldl = ldl;
@@ -638,6 +639,8 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     p.top_k = (int32_t)top_k;
     p.hidden = (int32_t)hidden;
     p.inner = (int32_t)inner;
+    p.rows = (int32_t)(tokens * top_k);
+    p.most_segments = (int32_t)moe_most_segments(tokens, experts, top_k);
     const int64_t rows13 = experts * 2 * inner, rows2 = experts * hidden;
     const int per_byte = f == MXGG_MXFP4 ? 2 : 1;
     p.q13_row = kb ? 64 : hidden / per_byte;

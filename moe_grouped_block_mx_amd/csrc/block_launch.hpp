@@ -72,18 +72,34 @@ struct MoeExpert {
   int32_t expert, base;
   uint64_t tokens;
 };
-// Workspace: the number of chosen experts, the table, the weight of each
-// (expert, token) row and the inner activation, bf16 [rows, inner].
+// At most 16 of its tokens (one column tile of the second product), and the
+// weight and token of one row.
+struct MoeSegment {
+  int32_t expert, base, tokens, unused;
+};
+struct MoeRow {
+  float weight;
+  int32_t token;
+};
+inline int64_t moe_most_segments(int64_t tokens, int64_t experts, int64_t top_k) {
+  const int64_t rows = tokens * top_k;
+  return rows / 16 + (rows < experts ? rows : experts);
+}
+// Workspace: how many experts and segments there are, their lists, the rows
+// and the inner activation, bf16 (laid out as its reader takes it: inner_at in
+// moe_layer.hip).
 struct MoeWorkspace {
-  size_t table, share, inner, bytes;
+  size_t table, segments, rows, inner, bytes;
 };
 inline MoeWorkspace moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner) {
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   MoeWorkspace w;
   w.table = 256;
-  w.share = w.table + up((size_t)experts * sizeof(MoeExpert));
-  w.inner = w.share + up((size_t)(tokens * top_k) * sizeof(float));
-  w.bytes = w.inner + up((size_t)(tokens * top_k) * (size_t)inner * 2);
+  w.segments = w.table + up((size_t)experts * sizeof(MoeExpert));
+  w.rows = w.segments + up((size_t)moe_most_segments(tokens, experts, top_k) * sizeof(MoeSegment));
+  w.inner = w.rows + up((size_t)(tokens * top_k) * sizeof(MoeRow));
+  // whole pieces of 128 elements: the second product reads whole ones
+  w.bytes = w.inner + up((size_t)(tokens * top_k) * (size_t)((inner + 127) / 128 * 128) * 2);
   return w;
 }
 struct MoeParams {
@@ -97,12 +113,15 @@ struct MoeParams {
   int32_t* ids;
   float* weights;
   // workspace
-  int32_t* active;
+  int32_t* counts;
   MoeExpert* table;
-  float* share;
+  MoeSegment* segments;
+  MoeRow* row_list;
   uint16_t* inner_x;
   int64_t ldx, ldl;
   int32_t tokens, experts, top_k, hidden, inner;
+  int32_t rows;                       // of the inner activation: tokens * top_k
+  int32_t most_segments;
   // byte strides of the codes: between rows, and between the 64-byte pieces of
   // a row; of the MX scales: between blocks of 32
   int64_t q13_row, q13_piece, s13_block, q2_row, q2_piece, s2_block;

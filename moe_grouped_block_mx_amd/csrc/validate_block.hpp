@@ -160,7 +160,8 @@ inline Check validate_moe_layer(const void* x, int64_t ldx, const void* logits, 
   const int unit = f == MXGG_FP8_128x128 || kblock_bits(w_fmt) ? 128 : 32;
   if (H % unit || I % unit)
     return fail(MXGG_ERR_SHAPE, "hidden=%lld and inner=%lld must be multiples of %lld", H, I, unit);
-  if (ldx < H || ldx >= ((int64_t)1 << 31)) return fail(MXGG_ERR_SHAPE, "ldx=%lld outside [hidden=%lld, 2^31)", ldx, H);
+  // 64 rows of x are addressed with 32-bit element offsets
+  if (ldx < H || ldx >= ((int64_t)1 << 25)) return fail(MXGG_ERR_SHAPE, "ldx=%lld outside [hidden=%lld, 2^25)", ldx, H);
   if (ldx % 8) return fail(MXGG_ERR_ALIGN, "ldx=%lld not a multiple of 8 elements", ldx);
   if (ldl < E || ldl >= ((int64_t)1 << 31)) return fail(MXGG_ERR_SHAPE, "ldl=%lld outside [experts=%lld, 2^31)", ldl, E);
   if (T == 0) return Check{};
