@@ -134,8 +134,13 @@ def _torch():
 
 
 def _stream(t):
-    torch = _torch()
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    """torch's current stream on the tensor's device, as the C ABI takes it
+    (the raw handle: building a torch.cuda.Stream around it takes longer than
+    a small launch)."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"expected a GPU tensor, got one on {t.device}")
+    return ctypes.c_void_p(_torch()._C._cuda_getCurrentRawStream(index))
 
 
 def _ptr(t):
@@ -159,7 +164,8 @@ def _expect(t, name, shape, dtypes):
     """The C ABI sees only pointers, so this is the one place where a buffer
     of the wrong shape, dtype or layout is caught before the GPU reads or
     writes past its end."""
-    torch = _torch()
+    if t is not None and t.dtype is dtypes and t.shape == shape and t.is_contiguous():
+        return t
     shape = tuple(int(v) for v in shape)
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if t is None:
@@ -446,71 +452,84 @@ def mxgg_grouped_wgrad(dycol_q, dycol_s, xcol_q, xcol_s, m_splits, N, K, mpad, m
     return main_grad
 
 
+_KINDS = {_torch().bfloat16: BF16, _torch().float32: F32}
+
+
 def _dtype(t, name):
     torch = _torch()
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return BF16
-    if t.dtype == torch.float32:
+    if t.dtype is torch.float32:
         return F32
     raise ValueError(f"{name} must be bf16 or fp32, got {str(t.dtype).replace('torch.', '')}")
 
 
-def _rows2d(t, name, shape=None, dtype=None):
-    """Leading dimension of a 2-D tensor with unit inner stride, of the given
-    shape and dtype when they are given."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.numel() and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit inner stride")
-    if (shape is not None and tuple(t.shape) != tuple(shape)) or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be a {str(dtype).replace('torch.', '')} tensor of shape {tuple(shape)}, got "
-                         f"{str(t.dtype).replace('torch.', '')} {tuple(t.shape)}")
-    return t.stride(0) if t.shape[0] > 1 and t.numel() else t.shape[1]
+def _rows2d(t, name):
+    """Leading dimension of a 2-D tensor with unit inner stride."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if rows == 0 or cols == 0:
+        return cols
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit inner stride")
+    return t.stride(0) if rows > 1 else cols
 
 
-def _cols_vector(t, name, cols):
+def _rows_like(t, x, name):
+    """The same, of a tensor with x's shape, dtype and device."""
+    if t.shape != x.shape or t.dtype is not x.dtype or t.get_device() != x.get_device():
+        raise ValueError(f"{name} must be a {str(x.dtype).replace('torch.', '')} tensor of shape {tuple(x.shape)} on "
+                         f"{x.device}, got {str(t.dtype).replace('torch.', '')} {tuple(t.shape)} on {t.device}")
+    return _rows2d(t, name)
+
+
+def _on(t, x, name):
+    if t.get_device() != x.get_device():
+        raise ValueError(f"{name} is on {t.device}, not on {x.device}")
+    return t
+
+
+def _cols_vector(t, name, x):
+    """dtype of a contiguous [cols] vector beside x, None for None."""
     if t is None:
         return None
-    if tuple(t.shape) != (cols,) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous tensor of shape ({cols},), got {tuple(t.shape)}")
-    return _dtype(t, name)
+    if t.shape != x.shape[1:] or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of shape ({x.shape[1]},), got {tuple(t.shape)}")
+    return _dtype(_on(t, x, name), name)
 
 
-def _same_device(like, **others):
-    for name, t in others.items():
-        if t is not None and t.device != like.device:
-            raise ValueError(f"{name} is on {t.device}, not on {like.device}")
+def _f32_out(t, name, n, x):
+    """fp32 [n] beside x: the caller's, or a new one."""
+    if t is None:
+        return x.new_empty(n, dtype=_torch().float32)
+    return _on(_expect(t, name, (n,), _torch().float32), x, name)
 
 
 def _ws(ws, need, like):
     """The caller's workspace, or one from torch's allocator on the current
     stream (which keeps it from other streams until this one's work is done)."""
     if ws is None:
-        ws = _torch().empty(need, dtype=_torch().uint8, device=like.device)
-    elif not ws.is_contiguous():
+        return like.new_empty(need, dtype=_torch().uint8), need
+    if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
-    return ws, ws.numel() * ws.element_size()
+    return _on(ws, like, "ws"), ws.numel() * ws.element_size()
 
 
 def mxgg_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, rstd=None):
     """x: bf16 or fp32 [rows, cols] (any row stride); weight, bias: [cols], bf16
     or fp32 alike, None for 1 and 0. Returns (y, mean, rstd): y like x, mean and
     rstd fp32 [rows]."""
-    torch = _torch()
-    dt = _dtype(x, "x")
-    ldx = _rows2d(x, "x")
+    dt, ldx = _dtype(x, "x"), _rows2d(x, "x")
     rows, cols = x.shape
-    wd, bd = _cols_vector(weight, "weight", cols), _cols_vector(bias, "bias", cols)
+    wd, bd = _cols_vector(weight, "weight", x), _cols_vector(bias, "bias", x)
     if wd is not None and bd is not None and wd != bd:
         raise ValueError("weight and bias must have the same dtype")
     if y is None:
-        y = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    ldy = _rows2d(y, "y", x.shape, x.dtype)
-    if mean is None:
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device)
-    if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    _expect(mean, "mean", (rows,), torch.float32)
-    _expect(rstd, "rstd", (rows,), torch.float32)
-    _same_device(x, weight=weight, bias=bias, y=y, mean=mean, rstd=rstd)
+        y, ldy = x.new_empty((rows, cols)), cols
+    else:
+        ldy = _rows_like(y, x, "y")
+    mean, rstd = _f32_out(mean, "mean", rows, x), _f32_out(rstd, "rstd", rows, x)
     _check(lib.mxgg_layer_norm_fwd(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wd or bd or 0, eps, _ptr(y),
                                    ldy, _ptr(mean), _ptr(rstd), _stream(x)))
     return y, mean, rstd
@@ -521,26 +540,21 @@ def mxgg_layer_norm_bwd(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=
     Returns (dx, dweight, dbias): dx like x; dweight and dbias fp32 [cols],
     added to the given ones with accumulate=True. False for dweight or dbias:
     not computed (None comes back)."""
-    torch = _torch()
-    dt = _dtype(x, "x")
-    ldx = _rows2d(x, "x")
+    dt, ldx = _dtype(x, "x"), _rows2d(x, "x")
     rows, cols = x.shape
-    lddy = _rows2d(dy, "dy", x.shape, x.dtype)
-    wd = _cols_vector(weight, "weight", cols)
+    lddy = _rows_like(dy, x, "dy")
+    wd = _cols_vector(weight, "weight", x)
     if dx is None:
-        dx = torch.empty((rows, cols), dtype=x.dtype, device=x.device)
-    lddx = _rows2d(dx, "dx", x.shape, x.dtype)
-    grads = []
-    for name, g in (("dweight", dweight), ("dbias", dbias)):
-        if g is None:
-            if accumulate:
-                raise ValueError(f"accumulate=True needs {name} (or {name}=False)")
-            g = torch.empty(cols, dtype=torch.float32, device=x.device)
-        grads.append(None if g is False else _expect(g, name, (cols,), torch.float32))
-    dweight, dbias = grads
-    _expect(mean, "mean", (rows,), torch.float32)
-    _expect(rstd, "rstd", (rows,), torch.float32)
-    _same_device(x, dy=dy, weight=weight, mean=mean, rstd=rstd, dx=dx, dweight=dweight, dbias=dbias, ws=ws)
+        dx, lddx = x.new_empty((rows, cols)), cols
+    else:
+        lddx = _rows_like(dx, x, "dx")
+    if accumulate and (dweight is None or dbias is None):
+        raise ValueError("accumulate=True needs dweight and dbias (or False for one that is not wanted)")
+    dweight = None if dweight is False else _f32_out(dweight, "dweight", cols, x)
+    dbias = None if dbias is False else _f32_out(dbias, "dbias", cols, x)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are required")
+    mean, rstd = _f32_out(mean, "mean", rows, x), _f32_out(rstd, "rstd", rows, x)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_layer_norm_bwd_workspace(rows, cols)), x)
     _check(lib.mxgg_layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, rows, cols, dt, _ptr(weight), wd or 0, _ptr(mean),
                                    _ptr(rstd), _ptr(dx), lddx, _ptr(dweight), _ptr(dbias), 1 if accumulate else 0,
@@ -552,20 +566,21 @@ def _grad_list(grads, total):
     """The host arrays of a gradient list, and a tensor of its device."""
     torch = _torch()
     grads = list(grads)
-    kinds = {torch.bfloat16: BF16, torch.float32: F32}
+    n, T = len(grads), torch.Tensor
     like = grads[0] if grads else total
-    dev = like.get_device() if like is not None else 0
-    for i, g in enumerate(grads):
-        if g.dtype not in kinds or not g.is_contiguous():
-            raise ValueError(f"gradient {i} must be a contiguous bf16 or fp32 tensor, got "
-                             f"{str(g.dtype).replace('torch.', '')} {tuple(g.shape)} with strides {g.stride()}")
-        if g.get_device() != dev or dev < 0:
-            raise ValueError(f"gradient {i} is on {g.device}: all gradients must be on one GPU")
-    n = len(grads)
-    ptrs = (ctypes.c_void_p * max(1, n))(*[g.data_ptr() for g in grads])
-    numels = (ctypes.c_int64 * max(1, n))(*[g.numel() for g in grads])
-    dtypes = (ctypes.c_int32 * max(1, n))(*[kinds[g.dtype] for g in grads])
-    return n, ptrs, numels, dtypes, like
+    # one pass in C for each property: a list of hundreds is the common case
+    dtypes = [_KINDS.get(g.dtype) for g in grads]
+    if None in dtypes or not all(map(T.is_contiguous, grads)):
+        for i, g in enumerate(grads):
+            if g.dtype not in _KINDS or not g.is_contiguous():
+                raise ValueError(f"gradient {i} must be a contiguous bf16 or fp32 tensor, got "
+                                 f"{str(g.dtype).replace('torch.', '')} {tuple(g.shape)} with strides {g.stride()}")
+    devices = set(map(T.get_device, grads))
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError(f"all gradients must be on one GPU, got {sorted({str(g.device) for g in grads})}")
+    ptrs = (ctypes.c_void_p * max(1, n))(*map(T.data_ptr, grads))
+    numels = (ctypes.c_int64 * max(1, n))(*map(T.numel, grads))
+    return n, ptrs, numels, (ctypes.c_int32 * max(1, n))(*dtypes), like
 
 
 def _norm_kind(norm_type):
@@ -579,10 +594,11 @@ def _norm_kind(norm_type):
 def _total(total, like):
     torch = _torch()
     if total is None:
-        total = torch.empty((), dtype=torch.float32, device="cuda" if like is None else like.device)
+        return torch.empty((), dtype=torch.float32, device="cuda") if like is None \
+            else like.new_empty((), dtype=torch.float32)
     if total.dtype != torch.float32 or total.numel() != 1:
         raise ValueError("total must be one fp32 value")
-    return total
+    return total if like is None else _on(total, like, "total")
 
 
 def mxgg_grad_norm(grads, norm_type=2.0, total=None, ws=None):
@@ -612,8 +628,9 @@ def mxgg_clip_grad_norm(grads, max_norm, norm_type=2.0, total=None, ws=None):
 def mxgg_clip_grads_with_norm(grads, max_norm, total):
     """Scale the gradients in place by min(1, max_norm / (total + 1e-6)); total:
     fp32 scalar on the device, e.g. combined over ranks from grad_norm."""
-    total = _total(total, total)
-    n, ptrs, numels, dtypes, _ = _grad_list(grads, total)
+    total = _total(total, None)
+    n, ptrs, numels, dtypes, like = _grad_list(grads, total)
+    _on(total, like, "total")
     _check(lib.mxgg_clip_grads_with_norm(ptrs, numels, dtypes, n, max_norm, _ptr(total), _stream(total)))
     return total
 
@@ -628,30 +645,25 @@ def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", reno
     weights): bf16 [tokens, hidden], int32 and fp32 [tokens, top_k]."""
     torch = _torch()
     f = _fmt(fmt)
+    if (f & 0xFF) not in (MXFP4, MXFP8, FP8_128x128, FP8_128x128_P2):
+        raise ValueError("fmt must be a weight format: mxfp4, mxfp8 or fp8_128x128(_p2)")
     _check_bf16_2d(x)
     T, H = x.shape
-    ldl = _rows2d(logits, "logits")
+    ldl, ldt = _rows2d(logits, "logits"), _dtype(logits, "logits")
     if logits.shape[0] != T:
         raise ValueError(f"logits must have {T} rows, got {logits.shape[0]}")
     E = logits.shape[1]
     inner = _q_rows(w13_q, f) // (2 * E) if E else 0
-    if (f & 0xFF) not in (MXFP4, MXFP8, FP8_128x128, FP8_128x128_P2):
-        raise ValueError("fmt must be a weight format: mxfp4, mxfp8 or fp8_128x128(_p2)")
     _expect(w13_q, "w13_q", _q_shape(f, E * 2 * inner, H), torch.uint8)
     _expect(w13_s, "w13_s", _row_scale_shape(f, E * 2 * inner, H), _sdtype(f))
     _expect(w2_q, "w2_q", _q_shape(f, E * H, inner), torch.uint8)
     _expect(w2_s, "w2_s", _row_scale_shape(f, E * H, inner), _sdtype(f))
-    if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
-    if ids is None:
-        ids = torch.empty((T, top_k), dtype=torch.int32, device=x.device)
-    if weights is None:
-        weights = torch.empty((T, top_k), dtype=torch.float32, device=x.device)
-    _expect(out, "out", (T, H), torch.bfloat16)
-    _expect(ids, "ids", (T, top_k), torch.int32)
-    _expect(weights, "weights", (T, top_k), torch.float32)
+    out = x.new_empty((T, H)) if out is None else _expect(out, "out", (T, H), torch.bfloat16)
+    ids = x.new_empty((T, top_k), dtype=torch.int32) if ids is None else _expect(ids, "ids", (T, top_k), torch.int32)
+    weights = x.new_empty((T, top_k), dtype=torch.float32) if weights is None \
+        else _expect(weights, "weights", (T, top_k), torch.float32)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_moe_layer_workspace(T, E, top_k, inner)), x)
-    _check(lib.mxgg_moe_layer(_ptr(x), x.stride(0) if T > 1 else H, _ptr(logits), ldl, _dtype(logits, "logits"), T, H,
+    _check(lib.mxgg_moe_layer(_ptr(x), x.stride(0) if T > 1 else H, _ptr(logits), ldl, ldt, T, H,
                               inner, E, top_k, _ptr(w13_q), _ptr(w13_s), _ptr(w2_q), _ptr(w2_s), f,
                               MOE_RENORMALIZE if renormalize else 0, _ptr(out), _ptr(ids), _ptr(weights), _ptr(ws),
                               ws_bytes, _stream(x)))

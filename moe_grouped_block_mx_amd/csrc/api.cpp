@@ -617,7 +617,7 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     const int f = base_format(format_bits((int)w_fmt));
     const bool kb = f == MXGG_FP8_128x128 || kblock_bits((int)w_fmt) != 0;
     uint8_t* at = static_cast<uint8_t*>(ws);
-    MoeParams p;
+    MoeParams p{};
     p.x = static_cast<const uint16_t*>(x);
     p.logits = logits;
     p.w13_q = static_cast<const uint8_t*>(w13_q);
@@ -627,20 +627,21 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     p.out = static_cast<uint16_t*>(out);
     p.ids = ids;
     p.weights = weights;
-    p.counts = reinterpret_cast<int32_t*>(at);
-    p.table = reinterpret_cast<MoeExpert*>(at + w.table);
+    p.count = reinterpret_cast<int32_t*>(at);
     p.segments = reinterpret_cast<MoeSegment*>(at + w.segments);
     p.row_list = reinterpret_cast<MoeRow*>(at + w.rows);
+    p.parts = reinterpret_cast<float*>(at + w.parts);
     p.inner_x = reinterpret_cast<uint16_t*>(at + w.inner);
     p.ldx = ldx;
     p.ldl = ldl;
+    p.logits_f32 = ldtype == MXGG_F32;
+    p.renormalize = (flags & MXGG_MOE_RENORMALIZE) != 0;
     p.tokens = (int32_t)tokens;
     p.experts = (int32_t)experts;
     p.top_k = (int32_t)top_k;
     p.hidden = (int32_t)hidden;
     p.inner = (int32_t)inner;
     p.rows = (int32_t)(tokens * top_k);
-    p.most_segments = (int32_t)moe_most_segments(tokens, experts, top_k);
     const int64_t rows13 = experts * 2 * inner, rows2 = experts * hidden;
     const int per_byte = f == MXGG_MXFP4 ? 2 : 1;
     p.q13_row = kb ? 64 : hidden / per_byte;
@@ -650,7 +651,7 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     p.q2_piece = kb ? rows2 * 64 : 64;
     p.s2_block = mx_scale_stride(rows2);
     const MoeFormat mf = f == MXGG_MXFP4 ? kMoeFp4 : f == MXGG_MXFP8 ? kMoeFp8 : kMoeBlock;
-    return hip_status(launch_moe_layer(p, mf, ldtype == MXGG_F32, (flags & MXGG_MOE_RENORMALIZE) != 0, stream),
+    return hip_status(launch_moe_layer(p, mf, cus, stream),
                       "expert layer launch");
   });
 }

@@ -65,39 +65,40 @@ hipError_t launch_clip(const ClipBatch& b, const double* part, int n, bool max_n
 // --- the expert layer for a few tokens ---------------------------------------
 constexpr int kMoeTokens = 64;        // an expert's tokens are the bits of one 64-bit word
 constexpr int kMoeTopK = 16;
+constexpr int kMoeDownGroups = 256;   // workgroups that the second product is split for
 
-// One chosen expert: its tokens, and where their rows of the inner activation
-// start (in the order of the tokens).
-struct MoeExpert {
-  int32_t expert, base;
-  uint64_t tokens;
-};
-// At most 16 of its tokens (one column tile of the second product), and the
-// weight and token of one row.
+// A chosen expert and some of its tokens: `tokens` rows of the inner activation
+// from `base` on (an expert's rows follow each other in the order of its
+// tokens).
 struct MoeSegment {
   int32_t expert, base, tokens, unused;
 };
+// Weight and token of one row.
 struct MoeRow {
   float weight;
   int32_t token;
 };
-inline int64_t moe_most_segments(int64_t tokens, int64_t experts, int64_t top_k) {
+// Every chosen expert has one segment that is not full at most; a segment has
+// room for at least 4 tokens.
+inline int64_t moe_most_segments(int64_t tokens, int64_t experts, int64_t top_k, int64_t segment = 4) {
   const int64_t rows = tokens * top_k;
-  return rows / 16 + (rows < experts ? rows : experts);
+  return rows / segment + (rows < experts ? rows : experts);
 }
-// Workspace: how many experts and segments there are, their lists, the rows
-// and the inner activation, bf16 (laid out as its reader takes it: inner_at in
+// Workspace: how many segments there are, their list, the rows,
+// the second product's parts and the inner activation, bf16 (laid out as its reader takes it: inner_at in
 // moe_layer.hip).
 struct MoeWorkspace {
-  size_t table, segments, rows, inner, bytes;
+  size_t segments, rows, parts, inner, bytes;
 };
 inline MoeWorkspace moe_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner) {
   const auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   MoeWorkspace w;
-  w.table = 256;
-  w.segments = w.table + up((size_t)experts * sizeof(MoeExpert));
+  w.segments = 256;
   w.rows = w.segments + up((size_t)moe_most_segments(tokens, experts, top_k) * sizeof(MoeSegment));
-  w.inner = w.rows + up((size_t)(tokens * top_k) * sizeof(MoeRow));
+  w.parts = w.rows + up((size_t)(tokens * top_k) * sizeof(MoeRow));
+  // fp32 [splits, tokens, hidden], splits * hidden <= 64 kMoeDownGroups when
+  // there is more than one
+  w.inner = w.parts + up((size_t)tokens * 64 * kMoeDownGroups * 4);
   // whole pieces of 128 elements: the second product reads whole ones
   w.bytes = w.inner + up((size_t)(tokens * top_k) * (size_t)((inner + 127) / 128 * 128) * 2);
   return w;
@@ -113,20 +114,50 @@ struct MoeParams {
   int32_t* ids;
   float* weights;
   // workspace
-  int32_t* counts;
-  MoeExpert* table;
+  int32_t* count;                     // of the segments
   MoeSegment* segments;
   MoeRow* row_list;
   uint16_t* inner_x;
+  float* parts;
   int64_t ldx, ldl;
+  bool logits_f32, renormalize;
   int32_t tokens, experts, top_k, hidden, inner;
   int32_t rows;                       // of the inner activation: tokens * top_k
-  int32_t most_segments;
+  // the plan of a call (moe_plan): tokens of a segment, 1 KiB loads that bring
+  // a piece of them, segments at most, 16-row tiles of a wave in
+  // the second product and the parts that its segments are split into
+  int32_t segment, dmas, most_segments;
+  int32_t down_tiles, splits;
   // byte strides of the codes: between rows, and between the 64-byte pieces of
   // a row; of the MX scales: between blocks of 32
   int64_t q13_row, q13_piece, s13_block, q2_row, q2_piece, s2_block;
 };
 enum MoeFormat { kMoeFp4 = 0, kMoeFp8 = 1, kMoeBlock = 2 };
-hipError_t launch_moe_layer(const MoeParams& p, MoeFormat fmt, bool logits_f32, bool renormalize, hipStream_t st);
+// How a call is cut. A segment of few tokens leaves more of the LDS to weights
+// in flight, one of many reads an expert's weights less often (again out of the
+// caches): about the tokens that a chosen expert has, by chance spread
+// included. With E2M1 codes a 1 KiB load brings 4 tokens' piece, with E4M3
+// codes 8.
+inline void moe_plan(MoeParams& p, MoeFormat fmt) {
+  const int each = fmt == kMoeFp4 ? 4 : 8, most = fmt == kMoeFp4 ? 3 : 2;
+  const int chosen = p.rows < p.experts ? p.rows : p.experts;
+  const int want = p.tokens <= each ? p.tokens : (3 * p.rows + 2 * chosen - 1) / (2 * chosen) + 1;
+  p.dmas = (want + each - 1) / each;
+  if (p.dmas > most) p.dmas = most;
+  p.segment = p.dmas * each;
+  // A wave's 16 rows of weights cost as much in loads of tokens as 64 do. With
+  // few tokens that is little, and small tiles give every CU a workgroup; with
+  // more the tiles are 64 rows, and the segments are split over workgroups.
+  if (p.tokens <= 16 && p.dmas <= 2) {
+    p.down_tiles = p.hidden >= 6144 ? 2 : 1;
+    p.splits = 1;
+  } else {
+    p.down_tiles = 4;
+    p.splits = kMoeDownGroups * 64 / p.hidden;
+    p.splits = p.splits < 1 ? 1 : p.splits > 8 ? 8 : p.splits;
+  }
+  p.most_segments = (int32_t)moe_most_segments(p.tokens, p.experts, p.top_k, p.segment);
+}
+hipError_t launch_moe_layer(MoeParams p, MoeFormat fmt, int num_cus, hipStream_t st);
 
 }  // namespace mxgg

@@ -46,148 +46,125 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k == 0xFFFFFFFFu ? 0x7FC00000u : k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// Reductions over the wave by DPP (rows of 16 lanes, then across rows): a few
-// cycles a step, where a shuffle through LDS takes a hundred. The result is
-// lane 63's, read into a scalar.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint32_t dpp(uint32_t old, uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS, 0xF, false);
+// Reductions over rows of 16 lanes by DPP rotations: a few cycles a step,
+// where a shuffle through LDS takes a hundred. Halving rotations give every
+// lane the same pairs, so all 16 get the same bits.
+template <int N>
+__device__ __forceinline__ uint32_t rotate(uint32_t v) {   // row_ror:N
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 + N, 0xF, 0xF, false);
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  v = max(v, dpp<0x111, 0xF>(v, v));   // row_shr 1, 2, 4, 8
-  v = max(v, dpp<0x112, 0xF>(v, v));
-  v = max(v, dpp<0x114, 0xF>(v, v));
-  v = max(v, dpp<0x118, 0xF>(v, v));
-  v = max(v, dpp<0x142, 0xA>(v, v));   // lane 15 of a row to the next row
-  v = max(v, dpp<0x143, 0xC>(v, v));   // lane 31 to the upper half
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+template <class Op>
+__device__ __forceinline__ uint32_t row_reduce(uint32_t v, Op op) {
+  v = op(v, rotate<8>(v));
+  v = op(v, rotate<4>(v));
+  v = op(v, rotate<2>(v));
+  return op(v, rotate<1>(v));
 }
-__device__ __forceinline__ float wave_sum(float f) {
-  const auto add = [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); };
-  uint32_t v = __float_as_uint(f);
-  v = add(v, dpp<0x111, 0xF>(0, v));
-  v = add(v, dpp<0x112, 0xF>(0, v));
-  v = add(v, dpp<0x114, 0xF>(0, v));
-  v = add(v, dpp<0x118, 0xF>(0, v));
-  v = add(v, dpp<0x142, 0xA>(0, v));
-  v = add(v, dpp<0x143, 0xC>(0, v));
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)v, 63));
+__device__ __forceinline__ float row_total(float f) {
+  return __uint_as_float(row_reduce(__float_as_uint(f), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
 }
 
-// The top-k of TPW tokens by one wave (side by side: one token's steps depend
-// on each other). Lane j holds choice j's expert (-1: none) and weight. Expert
-// 64 i + l sits in slot i of lane l, so the lowest index among equal logits is
-// the first slot's first lane.
-template <class T, bool RENORM, int PER, int TPW>
-__device__ __forceinline__ void route_tokens(const T* const (&row)[TPW], int experts, int top_k, int (&id)[TPW],
-                                             float (&weight)[TPW]) {
-  const int lane = threadIdx.x % 64;
-  float v[TPW][PER], mine[TPW], high[TPW];
-  uint32_t key[TPW][PER];
+// The top-k of four tokens by a wave, 16 lanes to a token: lane l has experts
+// 16 i + l. Lane j is left with choice j's expert (-1: none) and its weight.
+template <int PER>
+__device__ __forceinline__ void route_token(const MoeParams& p, int t, int& id, float& weight) {
+  const int lane = threadIdx.x % 16;
+  float v[PER];
+  uint32_t key[PER];
+  const int64_t at = t * p.ldl + lane;
+  if (p.logits_f32) {
+    const float* row = static_cast<const float*>(p.logits) + at;
 #pragma unroll
-  for (int u = 0; u < TPW; ++u) {
+    for (int i = 0; i < PER; ++i) v[i] = i * 16 + lane < p.experts ? row[i * 16] : -INFINITY;
+  } else {
+    const bf16_t* row = static_cast<const bf16_t*>(p.logits) + at;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = i * 16 + lane < p.experts ? load_one(row + i * 16) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = order_key(v[i]);
+  id = -1;
+  float mine = 0.f, high = 0.f;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+    m = row_reduce(m, [](uint32_t a, uint32_t b) { return max(a, b); });
+    uint32_t first = 0xFFFF;             // the lowest index among equal logits
+#pragma unroll
+    for (int i = PER - 1; i >= 0; --i)
+      if (key[i] == m) first = i * 16 + lane;
+    first = row_reduce(first, [](uint32_t a, uint32_t b) { return min(a, b); });
+    if (j == 0) high = key_value(m);
+    if (lane == j && m != 0) {           // 0: only -inf is left
+      id = (int)first;
+      mine = key_value(m);
+    }
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      v[u][i] = i * 64 + lane < experts ? load_one(row[u] + i * 64 + lane) : -INFINITY;
-    id[u] = -1;
-    mine[u] = high[u] = 0.f;
+      if (i * 16 + lane == (int)first) key[i] = 0;
   }
+  const float e = id >= 0 ? expf(mine - high) : 0.f;
+  float total = e;
+  if (!p.renormalize) {
+    total = 0.f;
 #pragma unroll
-  for (int u = 0; u < TPW; ++u)
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[u][i] = order_key(v[u][i]);
-  for (int j = 0; j < top_k; ++j) {
-#pragma unroll
-    for (int u = 0; u < TPW; ++u) {
-      uint32_t m = key[u][0];
-#pragma unroll
-      for (int i = 1; i < PER; ++i) m = max(m, key[u][i]);
-      m = wave_max(m);
-      if (j == 0) high[u] = key_value(m);
-      int at = -1;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i) {
-        const uint64_t has = __ballot(key[u][i] == m);
-        if (has) at = i * 64 + __builtin_ctzll(has);
-      }
-      if (m == 0) at = -1;           // only -inf is left
-      if (lane == j) {
-        id[u] = at;
-        mine[u] = key_value(m);
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i * 64 + lane == at) key[u][i] = 0;
-    }
+    for (int i = 0; i < PER; ++i) total += i * 16 + lane < p.experts ? expf(v[i] - high) : 0.f;
   }
-#pragma unroll
-  for (int u = 0; u < TPW; ++u) {
-    const float e = id[u] >= 0 ? expf(mine[u] - high[u]) : 0.f;
-    float total = e;
-    if constexpr (!RENORM) {
-      total = 0.f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) total += i * 64 + lane < experts ? expf(v[u][i] - high[u]) : 0.f;
-    }
-    total = wave_sum(total);
-    weight[u] = id[u] >= 0 ? e / total : 0.f;
-  }
+  total = row_total(total);
+  weight = id >= 0 ? e / total : 0.f;
 }
 
-// One workgroup routes all tokens and lists the chosen experts, their segments
-// of at most 16 tokens, and the (expert, token) rows.
-template <class T, bool RENORM, int PER, int TPW, int THREADS>
+// One workgroup routes all tokens (THREADS / 16 of them at a time) and lists
+// the segments (a chosen expert and at most p.segment of its tokens) and the
+// (expert, token) rows.
+template <int PER, int THREADS>
 __global__ __launch_bounds__(THREADS) void moe_route_kernel(MoeParams p) {
-  constexpr int WAVES = THREADS / 64;
-  __shared__ unsigned long long mask[kMaxExperts];
-  __shared__ int64_t first[kMaxExperts + 1], wave_tot[WAVES];
+  constexpr int TOKENS = THREADS / 16, ROUNDS = THREADS == 1024 ? kMoeTokens / TOKENS : 1;
+  __shared__ unsigned long long mask[kMaxExperts];   // an expert's tokens
+  __shared__ int64_t first[kMaxExperts + 1], wave_tot[THREADS / 64];
   for (int e = threadIdx.x; e < p.experts; e += THREADS) mask[e] = 0;
   __syncthreads();
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const T* row[TPW];
-  int id[TPW];
-  float weight[TPW];
+  const int lane = threadIdx.x % 16;
+  int id[ROUNDS];
+  float weight[ROUNDS];
 #pragma unroll
-  for (int u = 0; u < TPW; ++u) row[u] = static_cast<const T*>(p.logits) + min(wave + u * WAVES, p.tokens - 1) * p.ldl;
-  route_tokens<T, RENORM, PER, TPW>(row, p.experts, p.top_k, id, weight);
-#pragma unroll
-  for (int u = 0; u < TPW; ++u) {
-    const int t = wave + u * WAVES;
-    if (t < p.tokens && lane < p.top_k) {
-      p.ids[t * p.top_k + lane] = id[u];
-      p.weights[t * p.top_k + lane] = weight[u];
-      if (id[u] >= 0) atomicOr(&mask[id[u]], 1ull << t);
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int t = i * TOKENS + threadIdx.x / 16;
+    id[i] = -1;
+    if (t < p.tokens) {
+      route_token<PER>(p, t, id[i], weight[i]);
+      if (lane < p.top_k) {
+        p.ids[t * p.top_k + lane] = id[i];
+        p.weights[t * p.top_k + lane] = weight[i];
+        if (id[i] >= 0) atomicOr(&mask[id[i]], 1ull << t);
+      }
     }
   }
   __syncthreads();
-  // before expert e: chosen experts, and segments << 16; rows in the high half
+  // before expert e: segments, and rows in the high half
   block_prefix64<THREADS>(
       p.experts,
       [&](int e) {
         const int n = __popcll(mask[e]);
-        return (int64_t)((n != 0) | (n + 15) / 16 << 16) + ((int64_t)n << 32);
+        return (int64_t)((n + p.segment - 1) / p.segment) + ((int64_t)n << 32);
       },
       first, wave_tot);
   for (int e = threadIdx.x; e < p.experts; e += THREADS) {
-    uint64_t m = mask[e];
-    if (!m) continue;
-    const int32_t lists = (int32_t)first[e];
-    int32_t base = (int32_t)(first[e] >> 32);
-    p.table[lists & 0xFFFF] = MoeExpert{e, base, m};
-    MoeSegment* seg = p.segments + (lists >> 16);
-    for (int left = __popcll(m); left > 0; left -= 16, base += 16) *seg++ = MoeSegment{e, base, min(left, 16), 0};
-  }
-  if (threadIdx.x == 0) {
-    const int32_t lists = (int32_t)first[p.experts];
-    p.counts[0] = lists & 0xFFFF;
-    p.counts[1] = lists >> 16;
+    MoeSegment* at = p.segments + (int32_t)first[e];
+    int base = (int32_t)(first[e] >> 32);
+    for (int left = __popcll(mask[e]); left > 0; left -= p.segment, base += p.segment)
+      *at++ = MoeSegment{e, base, min(left, p.segment), 0};
   }
 #pragma unroll
-  for (int u = 0; u < TPW; ++u) {
-    const int t = wave + u * WAVES;
-    if (t < p.tokens && lane < p.top_k && id[u] >= 0)
-      p.row_list[(int32_t)(first[id[u]] >> 32) + __popcll(mask[id[u]] & ((1ull << t) - 1))] = MoeRow{weight[u], t};
+  for (int i = 0; i < ROUNDS; ++i) {
+    const int t = i * TOKENS + threadIdx.x / 16;
+    if (id[i] >= 0)
+      p.row_list[(int32_t)(first[id[i]] >> 32) + __popcll(mask[id[i]] & ((1ull << t) - 1))] = MoeRow{weight[i], t};
   }
+  if (threadIdx.x == 0) *p.count = (int32_t)first[p.experts];
 }
 
 // ---------------------------------------------------------------------------
@@ -222,298 +199,355 @@ __device__ __forceinline__ v8bf decode(const uint4& c, int j, float scale) {
   return __builtin_bit_cast(v8bf, uint4{o[0], o[1], o[2], o[3]});
 }
 
-// RT 16-row tiles of a weight operand against CT column tiles of 16 tokens.
-// One stage holds one piece of each; D stages are in flight. Addresses are a
-// uniform base and a 32-bit lane offset. A column without a token reads a
-// token's column all the same: what the MFMA computes for it is its own and is
-// dropped. So no branch surrounds a load, and each stage waits for its own
-// loads only.
-template <MoeFormat F, int RT, int CT, int D>
-struct Products {
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
+
+// Where element e of a row of the inner activation lies: a piece of all rows
+// after the other, so the rows of a segment, which follow each other, are one
+// run of each piece.
+template <MoeFormat F>
+__device__ __forceinline__ int64_t inner_at(int64_t row, int e, int64_t rows) {
+  return (e / Piece<F>::ELEMS * rows + row) * Piece<F>::ELEMS + e % Piece<F>::ELEMS;
+}
+
+#define MXGG_LDS __attribute__((address_space(3)))
+
+// gfx9 s_waitcnt: vmcnt in bits 3:0 and 15:14, expcnt 6:4, lgkmcnt 11:8; a
+// field at its maximum does not wait.
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | (N >> 4) << 14 | 0x7 << 4 | 0xF << 8);
+  asm volatile("" ::: "memory");
+}
+
+// RT 16-row tiles of a weight operand against a segment's tokens, one piece at
+// a time. The operands come to LDS by DMA, into a ring of D pieces for each
+// wave (D - 1 in flight; a wave waits for its own loads only, so no barriers).
+// A load to registers has to fetch 16 bytes of 16 rows at a time, which occupies
+// the address unit for 30 to 60 cycles; a DMA takes its 1 KiB as it lies (rows
+// of 64 bytes, tokens of ELEMS elements), and one brings the scales of all RT
+// tiles. XN DMAs hold COLS tokens. A column past the segment's tokens repeats
+// some token's: what the MFMA computes for it is its own and is dropped.
+template <MoeFormat F, int RT, int XN, int D, bool TAIL>
+struct Ring {
   static constexpr int M = Piece<F>::MFMAS, LANE = Piece<F>::LANE, ELEMS = Piece<F>::ELEMS;
-  const uint8_t* q[RT];            // the tiles' codes and scales
-  const uint8_t* s[RT];
-  const uint16_t* x;               // the columns
-  int64_t q_row, q_piece, s_block;
-  int64_t x_piece;                 // elements between the pieces of a column
-  uint32_t x_col[CT];              // this lane's column in each column tile
-  uint32_t x_group, x_mfma;        // elements between lane groups, between MFMAs
-  uint32_t q_lane, s_lane, x_lane[CT];
-  v4f acc[RT][CT];
+  static constexpr int CHUNKS = ELEMS / 8;             // 16-byte chunks of a token's piece
+  static constexpr int COLS = XN * 64 / CHUNKS;
+  static constexpr int BLOCKS = F == kMoeFp4 ? 4 : 2;  // of 32, in a piece
+  static constexpr int S_AT = RT * 1024, X_AT = S_AT + 256, STAGE = X_AT + XN * 1024;
+  static constexpr int BYTES = D * STAGE;              // of LDS, for a wave
+  static constexpr int DMAS = RT + 1 + XN, SLOTS = D;
 
-  struct Stage {
-    uint4 c[RT];
-    uint32_t s[RT];
-    uint4 x[CT][M];
-  };
+  const uint8_t* q[RT];
+  const uint8_t* s;
+  const uint16_t* x;
+  int64_t q_piece, s_block, x_piece;
+  uint32_t q_lane, s_lane, x_lane[XN];
+  uint32_t q_first, s_first, x_first[XN];   // the same at the start of the piece
+  int32_t k;
+  uint8_t* lds;
+  v4f acc[RT];
 
-  __device__ __forceinline__ void tile(int i, const uint8_t* codes, const void* scales, int64_t row0, int32_t k) {
-    q[i] = codes + row0 * q_row;
-    s[i] = static_cast<const uint8_t*>(scales) + (F == kMoeBlock ? row0 / 128 * (k / 128) * 4 : row0);
+  // Chunk c of row r lies at place c ^ swizzle: a fragment read takes one
+  // chunk of 16 rows, and this spreads it over all banks.
+  static __device__ __forceinline__ int q_place(int r, int c) { return c ^ (r >> 2 & 3); }
+  static __device__ __forceinline__ int x_place(int t, int c) { return c ^ (CHUNKS == 16 ? t & 15 : t >> 1 & 7); }
+
+  __device__ __forceinline__ void init(uint8_t* ring, int64_t row_stride, int64_t piece_stride, int64_t block_stride,
+                                       int32_t width) {
+    const int lane = threadIdx.x % 64;
+    lds = ring;
+    q_piece = piece_stride;
+    s_block = block_stride;
+    k = width;
+    q_first = (uint32_t)(lane / 4 * row_stride);
+    q_lane = q_first + q_place(lane / 4, lane % 4) * 16;
   }
-  // the lane's place in a piece: row lane % 16, group g
-  __device__ __forceinline__ void lanes(int g) {
-    const int r = threadIdx.x % 16;
-    q_lane = (uint32_t)(r * q_row + g * 16);
-    s_lane = F == kMoeBlock ? 0 : (uint32_t)((F == kMoeFp4 ? g : g / 2) * s_block + r);
+  // which four rows (of which tile, which block) the lane's dword of scales
+  // holds; tile i's scales begin at offset `at(i)`
+  template <class At>
+  __device__ __forceinline__ void scales(const void* base, At at) {
+    const int lane = threadIdx.x % 64;
+    s = static_cast<const uint8_t*>(base);
+    if constexpr (F == kMoeBlock) {
+      s_lane = s_first = at(lane % RT);
+    } else {
+      s_first = at(lane / 4 % RT) + lane % 4 * 4;
+      s_lane = s_first + (uint32_t)(lane / (4 * RT) % BLOCKS * s_block);
+    }
+  }
+  // the lane's token in each DMA, as an element offset
+  template <class Row>
+  __device__ __forceinline__ void columns(const uint16_t* base, int64_t piece_stride, Row row) {
+    const int lane = threadIdx.x % 64;
+    x = base;
+    x_piece = piece_stride;
 #pragma unroll
-    for (int c = 0; c < CT; ++c) x_lane[c] = x_col[c] + g * x_group;
+    for (int i = 0; i < XN; ++i) {
+      const int t = i * (64 / CHUNKS) + lane / CHUNKS;
+      x_first[i] = row(t);
+      x_lane[i] = x_first[i] + x_place(t, lane % CHUNKS) * 8;
+    }
   }
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[i][c] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
   }
 
-  __device__ __forceinline__ void load(Stage& st, int piece) const {
+  static __device__ __forceinline__ void dma16(const void* from, uint8_t* to) {
+    __builtin_amdgcn_global_load_lds(from, (MXGG_LDS void*)to, 16, 0, 0);
+  }
+  __device__ __forceinline__ void issue(int slot, int piece) const {
+    const int lane = threadIdx.x % 64;
+    uint8_t* to = lds + slot * STAGE;
+    // lanes past the row's end bring the piece's first bytes once more
+    const int left = k - piece * ELEMS;
+    const bool q_in = !TAIL || q_place(lane / 4, lane % 4) * LANE < left;
+    const bool s_in = !TAIL || lane / (4 * RT) % BLOCKS * 32 < left;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) dma16(q[i] + piece * q_piece + (q_in ? q_lane : q_first), to + i * 1024);
+    const int64_t s_at = F == kMoeBlock ? (int64_t)(piece / 2 * 4) : piece * BLOCKS * s_block;
+    __builtin_amdgcn_global_load_lds(s + s_at + (s_in ? s_lane : s_first), (MXGG_LDS void*)(to + S_AT), 4, 0, 0);
+#pragma unroll
+    for (int i = 0; i < XN; ++i) {
+      const int t = i * (64 / CHUNKS) + lane / CHUNKS;
+      const bool x_in = !TAIL || x_place(t, lane % CHUNKS) * 8 < left;
+      dma16(x + piece * x_piece + (x_in ? x_lane[i] : x_first[i]), to + X_AT + i * 1024);
+    }
+  }
+
+  // acc += the piece in a slot
+  __device__ __forceinline__ void compute(int slot, int piece) {
+    const int lane = threadIdx.x % 64, r = lane % 16, g = lane / 16;
+    const uint8_t* from = lds + slot * STAGE;
+    const bool in = !TAIL || piece * ELEMS + g * LANE < k;
+    const auto keep = [&](v4i v) { return v4i{in ? v[0] : 0, in ? v[1] : 0, in ? v[2] : 0, in ? v[3] : 0}; };
+    v4i xs[M], c[RT];
+    float scale[RT];
+    const int t = r < COLS ? r : r % COLS;   // columns past the ring's tokens repeat some
+#pragma unroll
+    for (int j = 0; j < M; ++j)
+      xs[j] = *reinterpret_cast<const v4i*>(from + X_AT + (t * CHUNKS + x_place(t, g * M + j)) * 16);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-      st.c[i] = *reinterpret_cast<const uint4*>(q[i] + piece * q_piece + q_lane);
+      c[i] = *reinterpret_cast<const v4i*>(from + i * 1024 + (r * 4 + q_place(r, g)) * 16);
       if constexpr (F == kMoeBlock)
-        st.s[i] = reinterpret_cast<const uint32_t*>(s[i])[piece / 2];
+        scale[i] = *reinterpret_cast<const float*>(from + S_AT + i * 4);
       else
-        st.s[i] = (s[i] + piece * ((F == kMoeFp4 ? 4 : 2) * s_block))[s_lane];
+        scale[i] = __uint_as_float((uint32_t)from[S_AT + ((F == kMoeFp4 ? g : g / 2) * RT + i) * 16 + r] << 23);
     }
+    if constexpr (TAIL) {
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+      for (int j = 0; j < M; ++j) xs[j] = keep(xs[j]);
 #pragma unroll
-      for (int j = 0; j < M; ++j)
-        st.x[c][j] = *reinterpret_cast<const uint4*>(x + piece * x_piece + j * x_mfma + x_lane[c]);
-  }
-
-  __device__ __forceinline__ void compute(const Stage& st) {
+      for (int i = 0; i < RT; ++i) c[i] = keep(c[i]);
+    }
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       // MX: 2^(s - 127) goes into the conversion; blocks: the fp32 scale onto
       // the product, since a code times a general scale would round in bf16
-      const float scale = F == kMoeBlock ? 1.f : __uint_as_float(st.s[i] << 23);
-      v8bf a[M];
+      v4f v = F == kMoeBlock ? v4f{0.f, 0.f, 0.f, 0.f} : acc[i];
 #pragma unroll
-      for (int j = 0; j < M; ++j) a[j] = decode<F>(st.c[i], j, scale);
+      for (int j = 0; j < M; ++j)
+        v = __builtin_amdgcn_mfma_f32_16x16x32_bf16(decode<F>(__builtin_bit_cast(uint4, c[i]), j, F == kMoeBlock ? 1.f : scale[i]),
+                                                    __builtin_bit_cast(v8bf, xs[j]), v, 0, 0, 0);
+      if constexpr (F == kMoeBlock) {
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        v4f t = F == kMoeBlock ? v4f{0.f, 0.f, 0.f, 0.f} : acc[i][c];
-#pragma unroll
-        for (int j = 0; j < M; ++j)
-          t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[j], __builtin_bit_cast(v8bf, st.x[c][j]), t, 0, 0, 0);
-        if constexpr (F == kMoeBlock) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) t[k] = fmaf(__uint_as_float(st.s[i]), t[k], acc[i][c][k]);
-        }
-        acc[i][c] = t;
+        for (int e = 0; e < 4; ++e) v[e] = fmaf(scale[i], v[e], acc[i][e]);
       }
+      acc[i] = v;
     }
   }
 
-  // pieces first, first + step, ... (count of them, all whole)
-  __device__ __forceinline__ void run(int first, int count, int step) {
-    if (count <= 0) return;
-    Stage st[D];
-#pragma unroll
-    for (int d = 0; d < D; ++d) load(st[d], first + min(d, count - 1) * step);
-    int i = 0;
-    for (; i + D <= count; i += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        compute(st[d]);
-        // past the end the last piece again, out of the cache: cheaper than a
-        // branch, after which the compiler would wait for everything. The
-        // fence keeps the scheduler from moving loads to their use.
-        load(st[d], first + min(i + d + D, count - 1) * step);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-      if (i + d < count) compute(st[d]);
-  }
-
-  // zeros on both sides in lane groups that are past the row's end
-  __device__ __forceinline__ void mask(Stage& st, bool in) const {
-    const auto keep = [&](uint4& v) { v = uint4{in ? v.x : 0, in ? v.y : 0, in ? v.z : 0, in ? v.w : 0}; };
-#pragma unroll
-    for (int i = 0; i < RT; ++i) keep(st.c[i]);
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int j = 0; j < M; ++j) keep(st.x[c][j]);
-  }
-
-  // the piece that the row ends in: lane groups past the end read the first
-  // group's place
-  __device__ __forceinline__ void run_tail(int piece, int32_t k) {
-    const int g = threadIdx.x % 64 / 16;
-    const bool in = piece * ELEMS + g * LANE < k;
-    lanes(in ? g : 0);
-    Stage st;
-    load(st, piece);
-    mask(st, in);
-    compute(st);
-    lanes(g);
-  }
+  static __device__ __forceinline__ int next(int slot) { return slot == D - 1 ? 0 : slot + 1; }
+  static __device__ __forceinline__ int before(int slot) { return slot == 0 ? D - 1 : slot - 1; }
+  // the oldest piece in flight is in LDS, D - 2 are still coming
+  static __device__ __forceinline__ void wait() { wait_loads<(D - 2) * DMAS>(); }
 };
 
-__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x / 64); }
-
-// The n-th set bit of a word that has that many
-__device__ __forceinline__ int nth_bit(uint64_t m, int n) {
-  int at = 0;
-  for (int i = 0; m; ++i, m &= m - 1)
-    if (i == n) at = __builtin_ctzll(m);
-  return at;
+// Workgroup barrier that orders LDS only: loads in flight stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x3 << 14 | 0xF | 0x7 << 4);   // lgkmcnt(0)
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
-// Where element e of a row of the inner activation lies, for the second
-// product: a piece's MFMAs one after the other, and in each of them all rows'
-// 32 elements, so the 16 bytes of a column's four lanes are one run and the
-// columns of an expert, whose rows follow each other, are too.
-template <MoeFormat F>
-__device__ __forceinline__ int64_t inner_at(int64_t row, int e, int64_t rows) {
-  constexpr int LANE = Piece<F>::LANE, ELEMS = Piece<F>::ELEMS;
-  const int piece = e / ELEMS, w = e % ELEMS, g = w / LANE, j = w % LANE / 8;
-  return ((int64_t)(piece * Piece<F>::MFMAS + j) * rows + row) * 32 + g * 8 + e % 8;
-}
+// How the first product is cut, by the token DMAs of a piece: tiles of W1 (and
+// W3) that a wave holds, waves, and pieces in a ring. What the rings leave of
+// 160 KiB holds the lists and sums. More tokens want more rows for each load
+// of them.
+template <int XN>
+struct UpCut {
+  static constexpr int TILES = XN == 1 ? 1 : 2, WAVES = XN == 1 ? 8 : 4, SLOTS = XN == 1 ? 5 : XN == 2 ? 5 : 4;
+};
 
-constexpr int kUpWaves = 4;    // waves of a workgroup, sharing the contraction
-constexpr int kUpTiles = 2;    // 16-row tiles of W1, and as many of W3
-constexpr int kUpStages = 2;   // pieces in flight
-constexpr int kDownStages = 3;
-constexpr int kDownWaves = 8;
-inline bool kDownTiles2(const MoeParams& p) { return p.hidden >= 6144; }
-
-template <MoeFormat F, int CT>
-__device__ __forceinline__ void up_columns(const MoeParams& p, const MoeExpert& ex, int n, int c0, int tile, v4f* lds) {
-  constexpr int RT = 2 * kUpTiles;
+// h, 16 TILES inner columns of one segment at a time: W1's and W3's rows
+// against the segment's tokens. The grid stays: workgroup b takes units b, b +
+// grid, ..., and its waves share the pieces of each, in one stream that runs on
+// over the ends of units. Neighbouring units at the same time on the same XCD
+// (the hardware deals workgroups out to the 8 in turn) share the lines of the
+// scales, 128 rows of one block each.
+template <MoeFormat F, int XN, bool TAIL>
+__global__ __launch_bounds__(64 * UpCut<XN>::WAVES) void moe_up_kernel(MoeParams p) {
+  constexpr int TILES = UpCut<XN>::TILES, WAVES = UpCut<XN>::WAVES, RT = 2 * TILES, THREADS = 64 * WAVES;
+  using R = Ring<F, RT, XN, UpCut<XN>::SLOTS, TAIL>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  v4f* sums = reinterpret_cast<v4f*>(lds + WAVES * R::BYTES);
+  int32_t* segments = reinterpret_cast<int32_t*>(sums + WAVES * RT * 64);
+  uint8_t* tokens = reinterpret_cast<uint8_t*>(segments + 2 * p.most_segments);
   const int lane = threadIdx.x % 64, wave = wave_id(), col = lane % 16, g = lane / 16;
-  Products<F, RT, CT, kUpStages> w;
-  w.q_row = p.q13_row;
-  w.q_piece = p.q13_piece;
-  w.s_block = p.s13_block;
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-    w.tile(i, p.w13_q, p.w13_s,
-           ((int64_t)ex.expert * 2 + i / kUpTiles) * p.inner + (tile * kUpTiles + i % kUpTiles) * 16, p.hidden);
-  w.x = p.x;
-  w.x_piece = Piece<F>::ELEMS;
-  w.x_group = Piece<F>::LANE;
-  w.x_mfma = 8;
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    const int r = c0 + c * 16 + col;
-    w.x_col[c] = (uint32_t)nth_bit(ex.tokens, r < n ? r : 0) * (uint32_t)p.ldx;
+  const int tiles = p.inner / (16 * TILES);
+  for (int i = threadIdx.x; i < p.most_segments; i += THREADS) {
+    const MoeSegment sg = p.segments[i];
+    segments[2 * i] = sg.expert << 8 | sg.tokens;
+    segments[2 * i + 1] = sg.base;
   }
-  w.lanes(g);
-  w.clear();
-  const int whole = p.hidden / Piece<F>::ELEMS;
-  w.run(wave, (whole - wave + kUpWaves - 1) / kUpWaves, kUpWaves);
-  if (p.hidden % Piece<F>::ELEMS && whole % kUpWaves == wave) w.run_tail(whole, p.hidden);
-  if (c0) __syncthreads();   // the sums of the columns before have been read
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) lds[(wave * RT * CT + i * CT + c) * 64 + lane] = w.acc[i][c];
+  for (int i = threadIdx.x; i < p.rows; i += THREADS) tokens[i] = (uint8_t)p.row_list[i].token;
+  const int units = *p.count * tiles;
+  const int start = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;   // the grid is a multiple of 8
   __syncthreads();
-  for (int o = wave; o < kUpTiles * CT; o += kUpWaves) {
-    const int i = o / CT, c = o % CT;
-    v4f gate = lds[(i * CT + c) * 64 + lane], up = lds[((kUpTiles + i) * CT + c) * 64 + lane];
+  if (start >= units) return;
+  const int pieces = (p.hidden + R::ELEMS - 1) / R::ELEMS;
+  const int mine = (pieces - wave + WAVES - 1) / WAVES;   // of a unit; 0 where there are fewer pieces than waves
+  const int rounds = (units - start + (int)gridDim.x - 1) / (int)gridDim.x;
+  R w;
+  w.init(lds + wave * R::BYTES, p.q13_row, p.q13_piece, p.s13_block, p.hidden);
+  const auto aim = [&](int unit) {
+    const int seg = unit / tiles, tile = unit % tiles;
+    const int head = __builtin_amdgcn_readfirstlane(segments[2 * seg]),
+              base = __builtin_amdgcn_readfirstlane(segments[2 * seg + 1]);
+    const int n = head & 255;
+    const int64_t gate = (int64_t)(head >> 8) * 2 * p.inner + tile * (16 * TILES);
 #pragma unroll
-    for (int k = 1; k < kUpWaves; ++k) {
-      gate += lds[((k * RT + i) * CT + c) * 64 + lane];
-      up += lds[((k * RT + kUpTiles + i) * CT + c) * 64 + lane];
+    for (int i = 0; i < RT; ++i) w.q[i] = p.w13_q + (gate + i / TILES * p.inner + i % TILES * 16) * p.q13_row;
+    if constexpr (F == kMoeBlock)
+      // the rows of W1 in a unit share a 128-row block, those of W3 too
+      w.scales(p.w13_s, [&](int i) { return (uint32_t)((gate + i / TILES * p.inner) / 128 * (p.hidden / 128) * 4); });
+    else
+      w.scales(static_cast<const uint8_t*>(p.w13_s) + gate,
+               [&](int i) { return (uint32_t)(i / TILES * p.inner + i % TILES * 16); });
+    w.columns(p.x, R::ELEMS, [&](int t) { return (uint32_t)tokens[base + min(t, n - 1)] * (uint32_t)p.ldx; });
+  };
+  int load_unit = start, load_piece = wave, loads = rounds * mine;
+  const auto load = [&](int slot) {
+    w.issue(slot, load_piece);
+    if (--loads > 0 && (load_piece += WAVES) >= pieces) {   // after the last, it again
+      load_piece = wave;
+      load_unit += gridDim.x;
+      aim(load_unit);
     }
-    const int r = c0 + c * 16 + col;
-    if (r < n) {
-      float h[4];
+  };
+  if (mine > 0) {
+    aim(start);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = gate[k] / (1.f + expf(-gate[k])) * up[k];
-      // bf16, as between the two grouped products of a training step: the
-      // second product reads it as its MFMA operand
-      uint16_t* to = p.inner_x + inner_at<F>(ex.base + r, (tile * kUpTiles + i) * 16 + g * 4, p.rows);
-      *reinterpret_cast<uint2*>(to) = uint2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
+    for (int d = 0; d < R::SLOTS - 1; ++d) load(d);
+  }
+  int slot = 0;
+  for (int round = 0; round < rounds; ++round) {
+    w.clear();
+    for (int i = 0; i < mine; ++i) {
+      R::wait();
+      load(R::before(slot));   // the slot whose piece went into the products last
+      w.compute(slot, wave + i * WAVES);
+      __builtin_amdgcn_sched_barrier(0);
+      slot = R::next(slot);
+    }
+    if (round) lds_barrier();  // the sums before have been read
+#pragma unroll
+    for (int i = 0; i < RT; ++i) sums[(wave * RT + i) * 64 + lane] = w.acc[i];
+    lds_barrier();
+    const int tile0 = (wave - round) & (WAVES - 1);   // another wave each round
+    if (tile0 < TILES) {
+      v4f a = sums[tile0 * 64 + lane], u = sums[(TILES + tile0) * 64 + lane];
+#pragma unroll
+      for (int k = 1; k < WAVES; ++k) {
+        a += sums[(k * RT + tile0) * 64 + lane];
+        u += sums[(k * RT + TILES + tile0) * 64 + lane];
+      }
+      const int unit = start + round * (int)gridDim.x, seg = unit / tiles, tile = unit % tiles * TILES + tile0;
+      if (col < (segments[2 * seg] & 255)) {
+        float h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = a[k] / (1.f + expf(-a[k])) * u[k];
+        // bf16, as between the two grouped products of a training step: the
+        // second product reads it as its MFMA operand
+        uint16_t* to = p.inner_x + inner_at<F>(segments[2 * seg + 1] + col, tile * 16 + g * 4, p.rows);
+        *reinterpret_cast<uint2*>(to) = uint2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
+      }
     }
   }
+  wait_loads<0>();
 }
 
-// h of one chosen expert, 32 of its inner columns: W1's and W3's rows against
-// the expert's tokens.
-template <MoeFormat F, int CT>
-__global__ __launch_bounds__(64 * kUpWaves) void moe_up_kernel(MoeParams p) {
-  __shared__ v4f lds[kUpWaves * 2 * kUpTiles * CT * 64];
-  const int tiles = p.inner / (16 * kUpTiles);
-  // four neighbouring tiles (128 rows: one line of every scale block) go to
-  // workgroups of the same XCD, which the hardware deals out in turn
-  const int b = blockIdx.x, group = b / 32 * 8 + b % 8, item = group * 4 + b % 32 / 8;
-  const int slot = item / tiles, tile = item % tiles;
-  if (slot >= p.experts) return;      // the grid is rounded up
-  const int active = p.counts[0];
-  const MoeExpert ex = p.table[slot];
-  if (slot >= active) return;
-  const int n = __popcll(ex.tokens);
-  if (CT == 1 || n <= 16) {
-    up_columns<F, 1>(p, ex, n, 0, tile, lds);
-  } else if constexpr (CT > 1) {
-    for (int c0 = 0; c0 < n; c0 += 16 * CT) up_columns<F, CT>(p, ex, n, c0, tile, lds);
-  }
-}
+// How the second product is cut: 16-row tiles of W2 that a wave holds, waves,
+// and pieces in a ring, by the token DMAs of a piece; the waves' sums (16 RT
+// rows of all tokens in fp32) share the LDS.
+template <int RT, int XN, bool MANY>   // MANY: more than 32 tokens
+struct DownCut {
+  static constexpr int WAVES = RT == 4 ? 4 : 8;
+  static constexpr int SLOTS = RT == 4 ? (XN == 1 ? 5 : 4) - (MANY ? 1 : 0) : RT == 2 ? 6 - XN : 9 - 2 * XN;
+};
 
-// y for 16 RT output columns and all tokens: the workgroup goes through every
-// segment, so a token's sum over its experts stays here (no atomics, one
-// order). The segments' pieces are dealt out to the waves in equal runs, and a
-// wave goes through its run in one stream: while it multiplies one segment's
-// last pieces, the next one's first are on their way. When a segment is done,
-// its 16 columns go, weighted, into the wave's sums in LDS.
-template <MoeFormat F, int RT, int WAVES, bool TAIL>
-__global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeParams p) {
-  constexpr int ROWS = RT * 16, D = kDownStages, ELEMS = Piece<F>::ELEMS;
-  using P = Products<F, RT, 1, D>;
-  extern __shared__ v4f lds[];
+// The same for the second product: y for 16 RT output columns and all tokens.
+// A workgroup goes through all segments, or through one of p.splits parts of
+// them, so a token's sum over its experts stays here (no atomics, one order);
+// the segments' pieces are dealt out to the waves in equal runs, each one
+// stream. When a segment is done, its columns go, weighted, into the wave's
+// sums in LDS.
+template <MoeFormat F, int RT, int XN, bool TAIL, bool MANY>
+__global__ __launch_bounds__(RT == 4 ? 256 : 512) void moe_down_kernel(MoeParams p) {
+  using C = DownCut<RT, XN, MANY>;
+  constexpr int WAVES = C::WAVES, THREADS = 64 * WAVES;
+  using R = Ring<F, RT, XN, C::SLOTS, TAIL>;
+  constexpr int ROWS = RT * 16;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // neighbouring tiles of 128 rows on one XCD, as above
   constexpr int NEAR = 128 / ROWS;
-  const int b = blockIdx.x, tile = (b / (8 * NEAR) * 8 + b % 8) * NEAR + b % (8 * NEAR) / 8;
+  const int b = blockIdx.x, tile = (b / (8 * NEAR) * 8 + b % 8) * NEAR + b % (8 * NEAR) / 8, part = blockIdx.y;
   if (tile * ROWS >= p.hidden) return;
-  float* sums = reinterpret_cast<float*>(lds);
-  int4* segments = reinterpret_cast<int4*>(sums + WAVES * p.tokens * ROWS);
-  MoeRow* rows = reinterpret_cast<MoeRow*>(segments + p.most_segments);
-  const int count = p.counts[1];
-  for (int i = threadIdx.x; i < p.most_segments; i += 64 * WAVES)
-    segments[i] = reinterpret_cast<const int4*>(p.segments)[i];
-  for (int i = threadIdx.x; i < p.rows; i += 64 * WAVES) rows[i] = p.row_list[i];
-  const int wave = wave_id(), lane = threadIdx.x % 64, col = lane % 16, g = lane / 16;
-  sums += wave * p.tokens * ROWS;
-  for (int i = lane; i < p.tokens * ROWS; i += 64) sums[i] = 0.f;
+  v4f* sums = reinterpret_cast<v4f*>(lds + WAVES * R::BYTES);   // [wave][token][ROWS / 4]
+  int32_t* segments = reinterpret_cast<int32_t*>(sums + WAVES * p.tokens * (ROWS / 4));
+  float* weights = reinterpret_cast<float*>(segments + 2 * p.most_segments);
+  uint8_t* tokens = reinterpret_cast<uint8_t*>(weights + p.rows);
+  const int lane = threadIdx.x % 64, wave = wave_id(), col = lane % 16, g = lane / 16;
+  for (int i = threadIdx.x; i < p.most_segments; i += THREADS) {
+    const MoeSegment sg = p.segments[i];
+    segments[2 * i] = sg.expert << 8 | sg.tokens;
+    segments[2 * i + 1] = sg.base;
+  }
+  for (int i = threadIdx.x; i < p.rows; i += THREADS) {
+    weights[i] = p.row_list[i].weight;
+    tokens[i] = (uint8_t)p.row_list[i].token;
+  }
+  for (int i = threadIdx.x; i < WAVES * p.tokens * (ROWS / 4); i += THREADS) sums[i] = v4f{0.f, 0.f, 0.f, 0.f};
+  const int count = *p.count;
   __syncthreads();
-
-  const int pieces = (p.inner + ELEMS - 1) / ELEMS;
+  const int pieces = (p.inner + R::ELEMS - 1) / R::ELEMS;
   const int total = count * pieces;
-  const int begin = total * wave / WAVES, items = total * (wave + 1) / WAVES - begin;
-  P w;
-  w.q_row = p.q2_row;
-  w.q_piece = p.q2_piece;
-  w.s_block = p.s2_block;
-  w.x = p.inner_x;
-  w.x_piece = (int64_t)p.rows * 32 * P::M;
-  w.x_group = 8;
-  w.x_mfma = p.rows * 32;
-  // where the loads are, and where the products are
-  int load_segment = begin / pieces, load_piece = begin % pieces;
+  const int runs = p.splits * WAVES, run = part * WAVES + wave;
+  const int begin = (int)((int64_t)total * run / runs), items = (int)((int64_t)total * (run + 1) / runs) - begin;
+  R w;
+  w.init(lds + wave * R::BYTES, p.q2_row, p.q2_piece, p.s2_block, p.inner);
+  // rows past the last (64 need not divide them) repeat its tile, unwritten
+  const int last = p.hidden - 16 - tile * ROWS;
+  int load_segment = begin / pieces, load_piece = begin % pieces, loads = items;
   int segment = load_segment, piece = load_piece;
   const auto aim = [&]() {
-    const int4 sg = segments[load_segment];
-    const int expert = __builtin_amdgcn_readfirstlane(sg.x), base = __builtin_amdgcn_readfirstlane(sg.y),
-              n = __builtin_amdgcn_readfirstlane(sg.z);
+    const int head = __builtin_amdgcn_readfirstlane(segments[2 * load_segment]),
+              base = __builtin_amdgcn_readfirstlane(segments[2 * load_segment + 1]);
+    const int n = head & 255;
+    const int64_t row0 = (int64_t)(head >> 8) * p.hidden + tile * ROWS;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) w.tile(i, p.w2_q, p.w2_s, (int64_t)expert * p.hidden + tile * ROWS + i * 16, p.inner);
-    w.x_col[0] = (uint32_t)(base + min(col, n - 1)) * 32;
-    w.lanes(g);
+    for (int i = 0; i < RT; ++i) w.q[i] = p.w2_q + (row0 + min(i * 16, last)) * p.q2_row;
+    if constexpr (F == kMoeBlock)
+      w.scales(p.w2_s, [&](int) { return (uint32_t)(row0 / 128 * (p.inner / 128) * 4); });
+    else
+      w.scales(static_cast<const uint8_t*>(p.w2_s) + row0, [&](int i) { return (uint32_t)min(i * 16, last); });
+    w.columns(p.inner_x, (int64_t)p.rows * R::ELEMS, [&](int t) { return (uint32_t)(base + min(t, n - 1)) * R::ELEMS; });
   };
-  int loads = items;
-  const auto load = [&](typename P::Stage& st) {
-    if constexpr (TAIL) {
-      // lane groups past the row's end read the first group's place
-      w.lanes(load_piece * ELEMS + g * P::LANE < p.inner ? g : 0);
-    }
-    w.load(st, load_piece);
+  const auto load = [&](int slot) {
+    w.issue(slot, load_piece);
     if (--loads > 0 && ++load_piece == pieces) {   // after the last, it again
       load_piece = 0;
       ++load_segment;
@@ -521,122 +555,155 @@ __global__ __launch_bounds__(64 * WAVES) void moe_down_kernel(MoeParams p) {
     }
   };
   const auto finish = [&]() {
-    const int4 sg = segments[segment];
-    if (col < sg.z) {
-      const MoeRow r = rows[sg.y + col];
+    const int n = segments[2 * segment] & 255, row = segments[2 * segment + 1] + col;
+    if (col < n) {
+      const float weight = weights[row];
+      v4f* to = sums + (wave * p.tokens + tokens[row]) * (ROWS / 4) + g;
 #pragma unroll
       for (int i = 0; i < RT; ++i) {
-        v4f* to = reinterpret_cast<v4f*>(sums + r.token * ROWS + i * 16 + g * 4);
-        v4f v = *to;
+        v4f v = to[i * 4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = fmaf(r.weight, w.acc[i][0][k], v[k]);
-        *to = v;
+        for (int k = 0; k < 4; ++k) v[k] = fmaf(weight, w.acc[i][k], v[k]);
+        to[i * 4] = v;
       }
     }
     w.clear();
-  };
-  const auto compute = [&](typename P::Stage& st) {
-    if constexpr (TAIL) w.mask(st, piece * ELEMS + g * P::LANE < p.inner);
-    w.compute(st);
-    if (++piece == pieces) {
-      finish();
-      piece = 0;
-      ++segment;
-    }
   };
   if (items > 0) {
     w.clear();
     aim();
-    typename P::Stage st[D];
 #pragma unroll
-    for (int d = 0; d < D; ++d) load(st[d]);
-    int i = 0;
-    for (; i + D <= items; i += D) {
-#pragma unroll
-      for (int d = 0; d < D; ++d) {
-        compute(st[d]);
-        load(st[d]);
-        __builtin_amdgcn_sched_barrier(0);
+    for (int d = 0; d < R::SLOTS - 1; ++d) load(d);
+    for (int i = 0, slot = 0; i < items; ++i) {
+      R::wait();
+      load(R::before(slot));
+      w.compute(slot, piece);
+      __builtin_amdgcn_sched_barrier(0);
+      slot = R::next(slot);
+      if (++piece == pieces) {
+        finish();
+        piece = 0;
+        ++segment;
       }
     }
-#pragma unroll
-    for (int d = 0; d < D - 1; ++d)
-      if (i + d < items) compute(st[d]);
     if (piece > 0) finish();    // the rest of this segment is another wave's
+    wait_loads<0>();
   }
   __syncthreads();
-  sums = reinterpret_cast<float*>(lds);
-  for (int i = threadIdx.x; i < p.tokens * ROWS / 4; i += 64 * WAVES) {
-    v4f v = *reinterpret_cast<v4f*>(sums + i * 4);
+  for (int i = threadIdx.x; i < p.tokens * (ROWS / 4); i += THREADS) {
+    v4f v = sums[i];
 #pragma unroll
-    for (int k = 1; k < WAVES; ++k) v += *reinterpret_cast<v4f*>(sums + k * p.tokens * ROWS + i * 4);
-    *reinterpret_cast<uint2*>(p.out + (int64_t)(i * 4 / ROWS) * p.hidden + tile * ROWS + i * 4 % ROWS) =
-        uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    for (int k = 1; k < WAVES; ++k) v += sums[k * p.tokens * (ROWS / 4) + i];
+    const int row = tile * ROWS + i % (ROWS / 4) * 4;
+    if (row >= p.hidden) continue;
+    const int64_t at = (int64_t)(i / (ROWS / 4)) * p.hidden + row;
+    if (p.splits == 1)
+      *reinterpret_cast<uint2*>(p.out + at) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    else
+      *reinterpret_cast<v4f*>(p.parts + (int64_t)part * p.tokens * p.hidden + at) = v;
   }
 }
 
-template <class T, bool RENORM, int PER>
+// y from the parts
+__global__ __launch_bounds__(256) void moe_sum_kernel(MoeParams p) {
+  const int64_t n = (int64_t)p.tokens * p.hidden, at = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (at >= n) return;
+  v4f v = *reinterpret_cast<const v4f*>(p.parts + at);
+  for (int k = 1; k < p.splits; ++k) v += *reinterpret_cast<const v4f*>(p.parts + k * n + at);
+  *reinterpret_cast<uint2*>(p.out + at) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+}
+
+constexpr int kLdsBytes = 160 * 1024;
+
+template <int PER>
 void route_per(const MoeParams& p, hipStream_t st) {
-  if (p.tokens <= 4) moe_route_kernel<T, RENORM, PER, 1, 256><<<1, 256, 0, st>>>(p);
-  else if (p.tokens <= 16) moe_route_kernel<T, RENORM, PER, 1, 1024><<<1, 1024, 0, st>>>(p);
-  else moe_route_kernel<T, RENORM, PER, 4, 1024><<<1, 1024, 0, st>>>(p);
+  if (p.tokens <= 16) moe_route_kernel<PER, 256><<<1, 256, 0, st>>>(p);
+  else moe_route_kernel<PER, 1024><<<1, 1024, 0, st>>>(p);
 }
 
-template <class T, bool RENORM>
 hipError_t route(const MoeParams& p, hipStream_t st) {
-  if (p.experts <= 64) route_per<T, RENORM, 1>(p, st);
-  else if (p.experts <= 128) route_per<T, RENORM, 2>(p, st);
-  else if (p.experts <= 256) route_per<T, RENORM, 4>(p, st);
-  else route_per<T, RENORM, 8>(p, st);
+  if (p.experts <= 64) route_per<4>(p, st);
+  else if (p.experts <= 128) route_per<8>(p, st);
+  else if (p.experts <= 256) route_per<16>(p, st);
+  else route_per<32>(p, st);
   return hipGetLastError();
 }
 
-template <class T>
-hipError_t route_any(const MoeParams& p, bool renormalize, hipStream_t st) {
-  return renormalize ? route<T, true>(p, st) : route<T, false>(p, st);
+template <MoeFormat F, int XN, bool TAIL>
+hipError_t up(const MoeParams& p, int num_cus, hipStream_t st) {
+  using C = UpCut<XN>;
+  using R = Ring<F, 2 * C::TILES, XN, C::SLOTS, TAIL>;
+  const int bytes = C::WAVES * (R::BYTES + 2 * C::TILES * 64 * (int)sizeof(v4f)) + p.most_segments * 8 + p.rows;
+  if (bytes > kLdsBytes) return hipErrorInvalidValue;
+  const hipError_t e =
+      ensure_dynamic_lds(reinterpret_cast<const void*>(&moe_up_kernel<F, XN, TAIL>), kLdsBytes, st);
+  if (e != hipSuccess) return e;
+  const int64_t units = (int64_t)p.most_segments * (p.inner / (16 * C::TILES));
+  const uint32_t grid = (uint32_t)((units < num_cus ? units : num_cus) + 7) / 8 * 8;
+  moe_up_kernel<F, XN, TAIL><<<grid, 64 * C::WAVES, bytes, st>>>(p);
+  return hipGetLastError();
 }
 
-template <MoeFormat F, int RT, int WAVES, bool TAIL>
+template <MoeFormat F, int RT, int XN, bool TAIL, bool MANY>
 hipError_t down(const MoeParams& p, hipStream_t st) {
-  const uint32_t grid = (uint32_t)((p.hidden + 1023) / 1024 * (1024 / (16 * RT)));   // whole 8 x 128-row rounds
-  const int bytes = WAVES * p.tokens * RT * 16 * 4 + p.most_segments * 16 + p.rows * (int)sizeof(MoeRow);
-  const void* kernel = reinterpret_cast<const void*>(&moe_down_kernel<F, RT, WAVES, TAIL>);
-  if (bytes > 65536) {
-    const hipError_t e = ensure_dynamic_lds(kernel, 160 * 1024, st);
-    if (e != hipSuccess) return e;
-  }
-  moe_down_kernel<F, RT, WAVES, TAIL><<<grid, 64 * WAVES, bytes, st>>>(p);
+  using C = DownCut<RT, XN, MANY>;
+  using R = Ring<F, RT, XN, C::SLOTS, TAIL>;
+  const int bytes = C::WAVES * (R::BYTES + p.tokens * RT * 64) + p.most_segments * 8 + p.rows * 5;
+  if (bytes > kLdsBytes) return hipErrorInvalidValue;
+  hipError_t e =
+      ensure_dynamic_lds(reinterpret_cast<const void*>(&moe_down_kernel<F, RT, XN, TAIL, MANY>), kLdsBytes, st);
+  if (e != hipSuccess) return e;
+  const uint32_t tiles = (uint32_t)((p.hidden + 1023) / 1024 * (1024 / (16 * RT)));   // whole 8 x 128-row rounds
+  moe_down_kernel<F, RT, XN, TAIL, MANY><<<dim3(tiles, (uint32_t)p.splits), 64 * C::WAVES, bytes, st>>>(p);
+  if ((e = hipGetLastError()) != hipSuccess || p.splits == 1) return e;
+  moe_sum_kernel<<<(uint32_t)(((int64_t)p.tokens * p.hidden + 1023) / 1024), 256, 0, st>>>(p);
   return hipGetLastError();
 }
 
-template <MoeFormat F, int RT, int WAVES>
+template <MoeFormat F, int XN, bool TAIL>
+hipError_t down_tiles(const MoeParams& p, hipStream_t st) {
+  if constexpr (XN < 3) {
+    if (p.down_tiles == 1) return down<F, 1, XN, TAIL, false>(p, st);
+    if (p.down_tiles == 2) return down<F, 2, XN, TAIL, false>(p, st);
+  }
+  return p.tokens > 32 ? down<F, 4, XN, TAIL, true>(p, st) : down<F, 4, XN, TAIL, false>(p, st);
+}
+
+template <MoeFormat F, bool TAIL>
 hipError_t down_any(const MoeParams& p, hipStream_t st) {
-  if constexpr (F != kMoeBlock)
-    if (p.inner % Piece<F>::ELEMS) return down<F, RT, WAVES, true>(p, st);
-  return down<F, RT, WAVES, false>(p, st);
+  if (p.dmas == 1) return down_tiles<F, 1, TAIL>(p, st);
+  if (F != kMoeFp4 || p.dmas == 2) return down_tiles<F, 2, TAIL>(p, st);
+  return down_tiles<F, F == kMoeFp4 ? 3 : 2, TAIL>(p, st);
+}
+
+template <MoeFormat F, bool TAIL>
+hipError_t up_any(const MoeParams& p, int num_cus, hipStream_t st) {
+  if (p.dmas == 1) return up<F, 1, TAIL>(p, num_cus, st);
+  if (F != kMoeFp4 || p.dmas == 2) return up<F, 2, TAIL>(p, num_cus, st);
+  return up<F, F == kMoeFp4 ? 3 : 2, TAIL>(p, num_cus, st);
 }
 
 template <MoeFormat F>
-hipError_t products(const MoeParams& p, hipStream_t st) {
-  const int most = p.tokens * p.top_k < p.experts ? p.tokens * p.top_k : p.experts;
-  const int64_t items = (int64_t)most * (p.inner / (16 * kUpTiles));
-  const uint32_t grid = (uint32_t)((items + 31) / 32 * 32);
-  if (p.tokens <= 16) moe_up_kernel<F, 1><<<grid, 64 * kUpWaves, 0, st>>>(p);
-  else moe_up_kernel<F, 2><<<grid, 64 * kUpWaves, 0, st>>>(p);
-  hipError_t e = hipGetLastError();
+hipError_t products(const MoeParams& p, int num_cus, hipStream_t st) {
+  // a row that ends inside a piece has kernels of its own (never with 128x128
+  // blocks)
+  hipError_t e;
+  if (F != kMoeBlock && p.hidden % Piece<F>::ELEMS) e = up_any<F, F != kMoeBlock>(p, num_cus, st);
+  else e = up_any<F, false>(p, num_cus, st);
   if (e != hipSuccess) return e;
-  if (kDownTiles2(p)) return down_any<F, 2, 8>(p, st);
-  return down_any<F, 1, kDownWaves>(p, st);
+  if (F != kMoeBlock && p.inner % Piece<F>::ELEMS) return down_any<F, F != kMoeBlock>(p, st);
+  return down_any<F, false>(p, st);
 }
 
 }  // namespace
 
-hipError_t launch_moe_layer(const MoeParams& p, MoeFormat fmt, bool logits_f32, bool renormalize, hipStream_t st) {
-  const hipError_t e = logits_f32 ? route_any<float>(p, renormalize, st) : route_any<bf16_t>(p, renormalize, st);
+hipError_t launch_moe_layer(MoeParams p, MoeFormat fmt, int num_cus, hipStream_t st) {
+  moe_plan(p, fmt);
+  const hipError_t e = route(p, st);
   if (e != hipSuccess) return e;
-  if (fmt == kMoeFp4) return products<kMoeFp4>(p, st);
-  if (fmt == kMoeFp8) return products<kMoeFp8>(p, st);
-  return products<kMoeBlock>(p, st);
+  if (fmt == kMoeFp4) return products<kMoeFp4>(p, num_cus, st);
+  if (fmt == kMoeFp8) return products<kMoeFp8>(p, num_cus, st);
+  return products<kMoeBlock>(p, num_cus, st);
 }
 
 }  // namespace mxgg
