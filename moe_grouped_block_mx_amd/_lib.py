@@ -7,7 +7,9 @@ loudly when the built library is missing -- there is no fallback.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 import os
 import re
 
@@ -562,25 +564,28 @@ def mxgg_layer_norm_bwd(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=
     return dx, dweight, dbias
 
 
+def _host_array(kind, code, values, n):
+    """A ctypes array of n values (array.array takes them faster)."""
+    return (kind * n).from_buffer(array.array(code, values)) if n else (kind * 1)()
+
+
 def _grad_list(grads, total):
-    """The host arrays of a gradient list, and a tensor of its device."""
-    torch = _torch()
+    """The host arrays of a gradient list, and a tensor of its device (the
+    library checks that every pointer is memory of that GPU)."""
     grads = list(grads)
-    n, T = len(grads), torch.Tensor
+    n, T = len(grads), _torch().Tensor
     like = grads[0] if grads else total
+    if n and like.get_device() < 0:
+        raise ValueError(f"the gradients must be on a GPU, got one on {like.device}")
     # one pass in C for each property: a list of hundreds is the common case
-    dtypes = [_KINDS.get(g.dtype) for g in grads]
+    dtypes = list(map(_KINDS.get, map(operator.attrgetter("dtype"), grads)))
     if None in dtypes or not all(map(T.is_contiguous, grads)):
         for i, g in enumerate(grads):
             if g.dtype not in _KINDS or not g.is_contiguous():
                 raise ValueError(f"gradient {i} must be a contiguous bf16 or fp32 tensor, got "
                                  f"{str(g.dtype).replace('torch.', '')} {tuple(g.shape)} with strides {g.stride()}")
-    devices = set(map(T.get_device, grads))
-    if len(devices) > 1 or -1 in devices:
-        raise ValueError(f"all gradients must be on one GPU, got {sorted({str(g.device) for g in grads})}")
-    ptrs = (ctypes.c_void_p * max(1, n))(*map(T.data_ptr, grads))
-    numels = (ctypes.c_int64 * max(1, n))(*map(T.numel, grads))
-    return n, ptrs, numels, (ctypes.c_int32 * max(1, n))(*dtypes), like
+    return (n, _host_array(ctypes.c_void_p, "Q", map(T.data_ptr, grads), n),
+            _host_array(ctypes.c_int64, "q", map(T.numel, grads), n), _host_array(ctypes.c_int32, "i", dtypes, n), like)
 
 
 def _norm_kind(norm_type):

@@ -149,9 +149,23 @@ std::vector<ClipBatch> clip_batches(void* const* grads, const int64_t* numels, c
   return out;
 }
 
+// Gradients are often slices of few allocations: one look at the runtime's
+// table answers for all tensors that begin in the same one.
 Check check_grads_on_device(void* const* grads, const int64_t* numels, int64_t n, int dev) {
-  for (int64_t i = 0; i < n; ++i)
-    if (numels[i] > 0) MXGG_TRY(check_on_device(grads[i], dev, "a gradient"));
+  uintptr_t from = 0, size = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    if (numels[i] == 0 || (uintptr_t)grads[i] - from < size) continue;
+    MXGG_TRY(check_on_device(grads[i], dev, "a gradient"));
+    hipDeviceptr_t base = nullptr;
+    size_t bytes = 0;
+    if (hipMemGetAddressRange(&base, &bytes, grads[i]) == hipSuccess) {
+      from = (uintptr_t)base;
+      size = bytes;
+    } else {
+      (void)hipGetLastError();
+      size = 0;
+    }
+  }
   return Check{};
 }
 
@@ -523,7 +537,7 @@ mxgg_status mxgg_layer_norm_fwd(const void* x, int64_t rows, int64_t cols, int64
 
 size_t mxgg_layer_norm_bwd_workspace(int64_t rows, int64_t cols) {
   if (!check_norm_dims(rows, cols).ok()) return 0;
-  return (size_t)norm_bwd_groups(rows, cols) * 2 * (size_t)cols * sizeof(float);
+  return (size_t)norm_bwd_groups(rows) * 2 * (size_t)cols * sizeof(float);
 }
 
 mxgg_status mxgg_layer_norm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, int64_t rows, int64_t cols,

@@ -75,12 +75,28 @@ struct Chunk {
   }
 };
 
-// Sum over W consecutive lanes (a power of two, at most a wave), in every one
-// of them. The lanes' partners are the same in each, so all get the same bits.
-template <int W, class T>
-__device__ __forceinline__ T lanes_sum(T v) {
-#pragma unroll
-  for (int d = 1; d < W; d <<= 1) v += __shfl_xor(v, d, 64);
+// A 32-bit value rotated by N within rows of 16 lanes (DPP row_ror): a few
+// cycles, where a shuffle through LDS takes a hundred.
+template <int N>
+__device__ __forceinline__ uint32_t rotate(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 + N, 0xF, 0xF, false);
+}
+template <int N>
+__device__ __forceinline__ float rotate(float v) {
+  return __uint_as_float(rotate<N>(__float_as_uint(v)));
+}
+
+// Sum over W neighbouring lanes (a power of two, at most a wave), in every one
+// of them. Halving steps give all lanes the same pairs, so all get the same
+// bits.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (W >= 16) v += rotate<8>(v);
+  if constexpr (W >= 8) v += rotate<4>(v);   // W < 16: of values that repeat with period W
+  if constexpr (W >= 4) v += rotate<2>(v);
+  if constexpr (W >= 2) v += rotate<1>(v);
+  if constexpr (W >= 32) v += __shfl_xor(v, 16, 64);
+  if constexpr (W >= 64) v += __shfl_xor(v, 32, 64);
   return v;
 }
 

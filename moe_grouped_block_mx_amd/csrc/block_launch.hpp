@@ -31,8 +31,9 @@ struct NormBwdParams {
   int64_t rows, lddy, ldx, lddx;
   int32_t cols;
 };
-// workgroups of the backward pass: one partial sum of both gradients each
-int norm_bwd_groups(int64_t rows, int64_t cols);
+// workgroups of the backward pass at most: one partial sum of both gradients
+// each
+int norm_bwd_groups(int64_t rows);
 hipError_t launch_layer_norm_fwd(const NormFwdParams& p, bool f32, bool wf32, hipStream_t st);
 // dweight / dbias: fp32 [cols] or NULL
 hipError_t launch_layer_norm_bwd(const NormBwdParams& p, bool f32, bool wf32, float* dweight, float* dbias,
@@ -41,7 +42,7 @@ hipError_t launch_layer_norm_bwd(const NormBwdParams& p, bool f32, bool wf32, fl
 // --- gradient norm and clipping --------------------------------------------
 // Tensors of one launch: they travel as kernel arguments, so a call needs no
 // device copy of the caller's pointer list.
-constexpr int kClipTensors = 128;
+constexpr int kClipTensors = 192;
 constexpr int kClipChunk = 8192;      // elements of one tensor that a workgroup takes at a time
 constexpr int kClipGroups = 1024;     // workgroups (and partial norms) of a launch at most
 struct ClipBatch {

@@ -22,192 +22,227 @@ __device__ __forceinline__ void row_sum(float (&v)[K], float (*lds)[THREADS / 64
 #pragma unroll
   for (int k = 0; k < K; ++k) v[k] = lanes_sum<(L < 64 ? L : 64)>(v[k]);
   if constexpr (L > 64) {
+    constexpr int W = L / 64;
     const int wave = threadIdx.x / 64;
     if (threadIdx.x % 64 == 0)
 #pragma unroll
       for (int k = 0; k < K; ++k) lds[slot][wave][k] = v[k];
     __syncthreads();
-    const int first = wave / (L / 64) * (L / 64);
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float s = 0.f;
-#pragma unroll
-      for (int i = 0; i < L / 64; ++i) s += lds[slot][first + i][k];
-      v[k] = s;
-    }
+    for (int k = 0; k < K; ++k) v[k] = lanes_sum<W>(lds[slot][wave / W * W + threadIdx.x % W][k]);
   }
 }
 
-template <class E>
-__device__ __forceinline__ void load_chunk(Chunk<E>& c, const E* row, int col, int cols) {
-  const int left = cols - col;
-  if (left >= Chunk<E>::N)
-    c.load(row + col);
-  else if (left > 0)
-    c.load_part(row + col, left);
-  else
-    c.w[0] = c.w[1] = c.w[2] = c.w[3] = 0;
-}
-
-template <class E>
-__device__ __forceinline__ void store_chunk(const Chunk<E>& c, E* row, int col, int cols) {
-  const int left = cols - col;
-  if (left >= Chunk<E>::N)
-    c.store(row + col);
-  else if (left > 0)
-    c.store_part(row + col, left);
-}
-
-// N consecutive values of a per-column vector (N = 4 or 8), as fp32
+// N values of a vector over the columns, as they lie in memory
 template <class W, int N>
-__device__ __forceinline__ void load_cols(float (&v)[N], const W* p, int col, int cols) {
-  constexpr int M = Chunk<W>::N < N ? Chunk<W>::N : N;
+struct ColumnValues {
+  static constexpr int M = Chunk<W>::N < N ? Chunk<W>::N : N;
+  Chunk<W> c[N / M];
+  __device__ __forceinline__ float get(int j) const { return c[j / M].get(j % M); }
+  __device__ __forceinline__ void fill(float v) {
+    float all[Chunk<W>::N];
 #pragma unroll
-  for (int h = 0; h < N / M; ++h) {
-    Chunk<W> c;
-    if constexpr (M == Chunk<W>::N) {
-      load_chunk(c, p, col + h * M, cols);
-    } else {            // 4 bf16 for 4 fp32
-      const int left = cols - col;
-      if (left >= M) memcpy(c.w, p + col, M * sizeof(W));
-      else c.load_part(p + col, left > 0 ? left : 0);
-    }
+    for (int i = 0; i < Chunk<W>::N; ++i) all[i] = v;
 #pragma unroll
-    for (int i = 0; i < M; ++i) v[h * M + i] = c.get(i);
+    for (int h = 0; h < N / M; ++h) c[h].set(all);
   }
-}
+};
 
-template <class E, class W, int L, int NV, int THREADS>
-__global__ __launch_bounds__(THREADS) void layer_norm_fwd_kernel(NormFwdParams p) {
-  constexpr int N = Chunk<E>::N, G = THREADS / L;
-  __shared__ float lds[2][THREADS / 64][1];
+// A lane's N columns. A chunk that would pass the row's end is moved back to
+// end there; its first `skip` elements are its neighbour's then (all N in a lane
+// past the end) and count here as nothing, so every access is a whole chunk. A
+// row shorter than a chunk (SHORT) is read and written by element.
+template <int N, bool SHORT>
+struct Columns {
+  int start, skip, size;
+  __device__ __forceinline__ Columns(int col, int cols) {
+    start = min(col, cols - N);
+    if (SHORT) start = max(start, 0);
+    skip = col - start;
+    size = SHORT ? min(cols, N) : N;
+  }
+  __device__ __forceinline__ bool has(int j) const { return j >= skip && (!SHORT || j < size); }
+  __device__ __forceinline__ bool any() const { return skip < size; }
+
+  template <class E>
+  __device__ __forceinline__ void load(Chunk<E>& c, const E* row) const {
+    if (SHORT && size < N) c.load_part(row + start, size);
+    else c.load(row + start);
+  }
+  template <class E>
+  __device__ __forceinline__ void store(const Chunk<E>& c, E* row) const {
+    if (SHORT && size < N) c.store_part(row + start, size);
+    else c.store(row + start);
+  }
+  // the same columns of a vector
+  template <class W>
+  __device__ __forceinline__ void vector(ColumnValues<W, N>& v, const W* p) const {
+    constexpr int M = ColumnValues<W, N>::M;
+#pragma unroll
+    for (int h = 0; h < N / M; ++h) {
+      const int left = size - h * M;
+      if (SHORT && left < M) v.c[h].load_part(p + start + h * M, max(left, 0));
+      else memcpy(v.c[h].w, p + start + h * M, M * sizeof(W));
+    }
+  }
+};
+
+constexpr int kThreads = 1024;
+
+// The G = T / L rows that a workgroup has at a time. It goes through rows
+// blockIdx G, + gridDim G, ... with the weights in registers and the next
+// rows' loads on their way while it works on these.
+template <class E, class W, int L, int NV, int T>
+__global__ __launch_bounds__(T) void layer_norm_fwd_kernel(NormFwdParams p) {
+  constexpr int N = Chunk<E>::N, G = T / L;
+  __shared__ float lds[2][T / 64][1];
+  using Cols = Columns<N, L == 16>;
   const int lane = threadIdx.x % L;
-  const int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / L;
-  const bool on = row < p.rows;
-  const E* x = static_cast<const E*>(p.x) + (on ? row : 0) * p.ldx;
-  Chunk<E> c[NV];
+  ColumnValues<W, N> w[NV], b[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) load_chunk(c[i], x, (i * L + lane) * N, p.cols);
-  float s[1] = {0.f};
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < N; ++j) s[0] += c[i].get(j);
-  row_sum<L, THREADS, 1>(s, lds, 0);
-  const float mean = s[0] / (float)p.cols;
+  for (int i = 0; i < NV; ++i) {
+    const Cols at((i * L + lane) * N, p.cols);
+    w[i].fill(1.f);
+    b[i].fill(0.f);
+    if (p.weight) at.vector(w[i], static_cast<const W*>(p.weight));
+    if (p.bias) at.vector(b[i], static_cast<const W*>(p.bias));
+  }
   // squares of (x - mu) / sqrt(C): their sum is the variance, and finite
   // wherever that is
   const float root = 1.f / sqrtf((float)p.cols);
-  float q[1] = {0.f};
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / L;
+  Chunk<E> next[NV];
+  const auto load = [&](int64_t r) {
+    const E* x = static_cast<const E*>(p.x) + (r < p.rows ? r : p.rows - 1) * p.ldx;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) Cols((i * L + lane) * N, p.cols).load(next[i], x);
+  };
+  load(row);
+  for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += step, row += step) {
+    Chunk<E> c[NV];
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float d = (c[i].get(j) - mean) * root;
-      q[0] += (i * L + lane) * N + j < p.cols ? d * d : 0.f;
+    for (int i = 0; i < NV; ++i) c[i] = next[i];
+    if (base + step < p.rows) load(row + step);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const Cols at((i * L + lane) * N, p.cols);
+#pragma unroll
+      for (int j = 0; j < N; ++j) s[0] += at.has(j) ? c[i].get(j) : 0.f;
     }
-  row_sum<L, THREADS, 1>(q, lds, 1);
-  const float rstd = 1.f / sqrtf(q[0] + p.eps);
-  if (!on) return;
-  if (lane == 0) {
-    p.mean[row] = mean;
-    p.rstd[row] = rstd;
-  }
-  E* y = static_cast<E*>(p.y) + row * p.ldy;
+    row_sum<L, T, 1>(s, lds, 0);
+    const float mean = s[0] / (float)p.cols;
+    float q[1] = {0.f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = (i * L + lane) * N;
-    float v[N], t[N];
+    for (int i = 0; i < NV; ++i) {
+      const Cols at((i * L + lane) * N, p.cols);
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = (c[i].get(j) - mean) * rstd;
-    if (p.weight) {
-      load_cols<W, N>(t, static_cast<const W*>(p.weight), col, p.cols);
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] *= t[j];
+      for (int j = 0; j < N; ++j) {
+        const float d = (c[i].get(j) - mean) * root;
+        q[0] += at.has(j) ? d * d : 0.f;
+      }
     }
-    if (p.bias) {
-      load_cols<W, N>(t, static_cast<const W*>(p.bias), col, p.cols);
+    row_sum<L, T, 1>(q, lds, 1);
+    const float rstd = 1.f / sqrtf(q[0] + p.eps);
+    if (row < p.rows) {
+      if (lane == 0) {
+        p.mean[row] = mean;
+        p.rstd[row] = rstd;
+      }
+      E* y = static_cast<E*>(p.y) + row * p.ldy;
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] += t[j];
+      for (int i = 0; i < NV; ++i) {
+        float v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = (c[i].get(j) - mean) * rstd * w[i].get(j) + b[i].get(j);
+        Chunk<E> o;
+        o.set(v);
+        const Cols at((i * L + lane) * N, p.cols);
+        if (at.any()) at.store(o, y);
+      }
     }
-    Chunk<E> o;
-    o.set(v);
-    store_chunk(o, y, col, p.cols);
   }
 }
 
-// A workgroup walks rows blockIdx, + gridDim, ... (G rows at a time) and keeps
-// its column sums of dy xh and dy in registers; at the end the G row groups
-// meet in LDS and the workgroup writes one partial sum per column.
-template <class E, class W, int L, int NV, int THREADS>
-__global__ __launch_bounds__(THREADS) void layer_norm_bwd_kernel(NormBwdParams p) {
-  constexpr int N = Chunk<E>::N, G = THREADS / L;
-  __shared__ float lds[2][THREADS / 64][2];
-  __shared__ float cross[G > 1 ? THREADS * N : 1];
+// The same walk, with the column sums of dy xh and dy in registers; at the end
+// the G row groups meet in LDS and the workgroup writes one partial sum per
+// column.
+template <class E, class W, int L, int NV, int T>
+__global__ __launch_bounds__(T) void layer_norm_bwd_kernel(NormBwdParams p) {
+  constexpr int N = Chunk<E>::N, G = T / L;
+  __shared__ float lds[2][T / 64][2];
+  __shared__ float cross[G > 1 ? T * N : 1];
+  using Cols = Columns<N, L == 16>;
   const int lane = threadIdx.x % L, grp = threadIdx.x / L;
   float dw[NV][N], db[NV][N];
+  ColumnValues<W, N> w[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
 #pragma unroll
     for (int j = 0; j < N; ++j) dw[i][j] = db[i][j] = 0.f;
+    w[i].fill(1.f);
+    if (p.weight) Cols((i * L + lane) * N, p.cols).vector(w[i], static_cast<const W*>(p.weight));
+  }
   const float inv = 1.f / (float)p.cols;
-  int slot = 0;
-  for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += (int64_t)gridDim.x * G, slot ^= 1) {
-    const int64_t row = base + grp;
-    const bool on = row < p.rows;   // a group past the last row adds zeros
-    const E* x = static_cast<const E*>(p.x) + (on ? row : 0) * p.ldx;
-    const E* dy = static_cast<const E*>(p.dy) + (on ? row : 0) * p.lddy;
-    const float mean = on ? p.mean[row] : 0.f, rstd = on ? p.rstd[row] : 0.f;
-    const int cols = on ? p.cols : 0;
-    Chunk<E> cx[NV], cg[NV];
+  const int64_t step = (int64_t)gridDim.x * G;
+  int64_t row = (int64_t)blockIdx.x * G + grp;
+  Chunk<E> next_x[NV], next_g[NV];
+  float next_mean, next_rstd;
+  const auto load = [&](int64_t r) {
+    // a group past the last row computes it again and adds nothing
+    const int64_t at = r < p.rows ? r : p.rows - 1;
+    const E* x = static_cast<const E*>(p.x) + at * p.ldx;
+    const E* dy = static_cast<const E*>(p.dy) + at * p.lddy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      load_chunk(cx[i], x, (i * L + lane) * N, cols);
-      load_chunk(cg[i], dy, (i * L + lane) * N, cols);
+      const Cols c((i * L + lane) * N, p.cols);
+      c.load(next_x[i], x);
+      c.load(next_g[i], dy);
     }
+    next_mean = p.mean[at];
+    next_rstd = p.rstd[at];
+  };
+  load(row);
+  int slot = 0;
+  for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += step, row += step, slot ^= 1) {
+    const bool on = row < p.rows;
+    Chunk<E> cx[NV], cg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) cx[i] = next_x[i], cg[i] = next_g[i];
+    const float mean = next_mean, rstd = next_rstd;
+    if (base + step < p.rows) load(row + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = (i * L + lane) * N;
-      float w[N];
-      if (p.weight) {
-        load_cols<W, N>(w, static_cast<const W*>(p.weight), col, p.cols);
-      } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) w[j] = 1.f;
-      }
+      const Cols at((i * L + lane) * N, p.cols);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        // past the row's end dy and w are 0, but xh is not
-        const float xh = col + j < cols ? (cx[i].get(j) - mean) * rstd : 0.f, d = cg[i].get(j);
-        s[0] += d * w[j];
-        s[1] += d * w[j] * xh;
+        // an element that does not count has dy = 0; where its xh is not finite
+        // the row's results are not either
+        const float xh = (cx[i].get(j) - mean) * rstd, d = on && at.has(j) ? cg[i].get(j) : 0.f;
+        s[0] += d * w[i].get(j);
+        s[1] += d * w[i].get(j) * xh;
         dw[i][j] += d * xh;
         db[i][j] += d;
       }
     }
-    row_sum<L, THREADS, 2>(s, lds, slot);
+    row_sum<L, T, 2>(s, lds, slot);
     const float c1 = s[0] * inv, c2 = s[1] * inv;
     if (on) {
       E* dx = static_cast<E*>(p.dx) + row * p.lddx;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int col = (i * L + lane) * N;
-        float w[N], v[N];
-        if (p.weight) {
-          load_cols<W, N>(w, static_cast<const W*>(p.weight), col, p.cols);
-        } else {
-#pragma unroll
-          for (int j = 0; j < N; ++j) w[j] = 1.f;
-        }
+        float v[N];
 #pragma unroll
         for (int j = 0; j < N; ++j) {
           const float xh = (cx[i].get(j) - mean) * rstd;
-          v[j] = rstd * (cg[i].get(j) * w[j] - c1 - xh * c2);
+          v[j] = rstd * (cg[i].get(j) * w[i].get(j) - c1 - xh * c2);
         }
         Chunk<E> o;
         o.set(v);
-        store_chunk(o, dx, col, p.cols);
+        const Cols at((i * L + lane) * N, p.cols);
+        if (at.any()) at.store(o, dx);
       }
     }
   }
@@ -222,59 +257,65 @@ __global__ __launch_bounds__(THREADS) void layer_norm_bwd_kernel(NormBwdParams p
 #pragma unroll
         for (int j = 0; j < N; ++j) cross[(grp * N + j) * L + lane] = v[j];
         __syncthreads();
-        for (int e = threadIdx.x; e < L * N; e += THREADS) {
-          const int j = e / L, l = e % L, col = (i * L + l) * N + j;
+        for (int e = threadIdx.x; e < L * N; e += T) {
+          const int j = e / L, l = e % L;
+          const Cols at((i * L + l) * N, p.cols);
           float t = 0.f;
           for (int g = 0; g < G; ++g) t += cross[(g * N + j) * L + l];
-          if (col < p.cols) part[(int64_t)k * p.cols + col] = t;
+          if (at.has(j)) part[(int64_t)k * p.cols + at.start + j] = t;
         }
       } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-          const int col = (i * L + lane) * N + j;
-          if (col < p.cols) part[(int64_t)k * p.cols + col] = v[j];
+          const Cols at((i * L + lane) * N, p.cols);
+          if (at.has(j)) part[(int64_t)k * p.cols + at.start + j] = v[j];
         }
       }
     }
 }
 
-// Column sums of the partials: 16 columns of dweight (blockIdx.y == 0) or
-// dbias per workgroup, 16 lanes of each wave on consecutive columns.
-__global__ __launch_bounds__(256) void layer_norm_grad_kernel(const float* part, int n, int cols, float* dweight,
-                                                              float* dbias, int accumulate) {
+// Column sums of the partials: a wave's lanes take 64 neighbouring columns of
+// dweight (blockIdx.y == 0) or dbias, the workgroup's waves every 16th partial.
+__global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(const float* part, int n, int cols, float* dweight,
+                                                                   float* dbias, int accumulate) {
   float* out = blockIdx.y ? dbias : dweight;
   if (!out) return;
-  __shared__ float lds[16][17];
-  const int c = threadIdx.x % 16, r = threadIdx.x / 16;
-  const int col = blockIdx.x * 16 + c;
+  constexpr int WAVES = kThreads / 64;
+  __shared__ float lds[WAVES][64];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int col = blockIdx.x * 64 + lane;
   float s = 0.f;
   if (col < cols) {
     const float* q = part + (int64_t)blockIdx.y * cols + col;
-#pragma unroll 4
-    for (int i = r; i < n; i += 16) s += q[(int64_t)i * 2 * cols];
+#pragma unroll 8
+    for (int i = wave; i < n; i += WAVES) s += q[(int64_t)i * 2 * cols];
   }
-  lds[r][c] = s;
+  lds[wave][lane] = s;
   __syncthreads();
-  if (r == 0 && col < cols) {
+  if (wave == 0 && col < cols) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) s += lds[i][c];
+    for (int i = 0; i < WAVES; ++i) s += lds[i][lane];
     out[col] = accumulate ? out[col] + s : s;
   }
 }
 
+constexpr int kFwdThreads = 1 << 20, kBwdGroups = 256;
+
 template <class E, class W, int L, int NV>
 hipError_t fwd(const NormFwdParams& p, hipStream_t st) {
-  constexpr int T = L < 256 ? 256 : L;
-  const int64_t grid = (p.rows + T / L - 1) / (T / L);
-  layer_norm_fwd_kernel<E, W, L, NV, T><<<dim3((uint32_t)grid), dim3(T), 0, st>>>(p);
+  constexpr int T = L < 256 ? 256 : L, G = T / L, MOST = kFwdThreads / T;
+  const int64_t need = (p.rows + G - 1) / G;
+  layer_norm_fwd_kernel<E, W, L, NV, T><<<(uint32_t)(need < MOST ? need : MOST), T, 0, st>>>(p);
   return hipGetLastError();
 }
 
 template <class E, class W, int L, int NV>
-hipError_t bwd(const NormBwdParams& p, int grid, hipStream_t st) {
-  constexpr int T = L < 512 ? 512 : L;
-  layer_norm_bwd_kernel<E, W, L, NV, T><<<dim3((uint32_t)grid), dim3(T), 0, st>>>(p);
+hipError_t bwd(const NormBwdParams& p, int& grid, hipStream_t st) {
+  constexpr int T = NV == 1 ? 1024 : L < 512 ? 512 : L, G = T / L;
+  const int64_t need = (p.rows + G - 1) / G;
+  grid = (int)(need < kBwdGroups ? need : kBwdGroups);
+  layer_norm_bwd_kernel<E, W, L, NV, T><<<grid, T, 0, st>>>(p);
   return hipGetLastError();
 }
 
@@ -284,33 +325,31 @@ hipError_t fwd_any(const NormFwdParams& p, hipStream_t st) {
   if (chunks <= 16) return fwd<E, W, 16, 1>(p, st);
   if (chunks <= 64) return fwd<E, W, 64, 1>(p, st);
   if (chunks <= 128) return fwd<E, W, 64, 2>(p, st);
-  if (chunks <= 256) return fwd<E, W, 256, 1>(p, st);
+  if (chunks <= 256) return fwd<E, W, 128, 2>(p, st);
   if (chunks <= 512) return fwd<E, W, 256, 2>(p, st);
-  if (chunks <= 1024) return fwd<E, W, 256, 4>(p, st);
+  if (chunks <= 1024) return fwd<E, W, 512, 2>(p, st);
   if (chunks <= 2048) return fwd<E, W, 1024, 2>(p, st);
-  return fwd<E, W, 1024, 4>(p, st);
+  return fwd<E, W, 1024, Chunk<E>::N == 4 ? 4 : 2>(p, st);
 }
 
 template <class E, class W>
-hipError_t bwd_any(const NormBwdParams& p, int grid, hipStream_t st) {
+hipError_t bwd_any(const NormBwdParams& p, int& grid, hipStream_t st) {
   const int chunks = (p.cols + Chunk<E>::N - 1) / Chunk<E>::N;
   if (chunks <= 16) return bwd<E, W, 16, 1>(p, grid, st);
   if (chunks <= 64) return bwd<E, W, 64, 1>(p, grid, st);
   if (chunks <= 128) return bwd<E, W, 64, 2>(p, grid, st);
-  if (chunks <= 256) return bwd<E, W, 256, 1>(p, grid, st);
+  if (chunks <= 256) return bwd<E, W, 128, 2>(p, grid, st);
   if (chunks <= 512) return bwd<E, W, 256, 2>(p, grid, st);
+  if (chunks <= 768) return bwd<E, W, 256, 3>(p, grid, st);
   if (chunks <= 1024) return bwd<E, W, 512, 2>(p, grid, st);
-  if (chunks <= 2048) return bwd<E, W, 1024, 2>(p, grid, st);
-  return bwd<E, W, 1024, 4>(p, grid, st);
+  if (chunks <= 1536) return bwd<E, W, 512, 3>(p, grid, st);
+  if (chunks <= 2048) return bwd<E, W, 512, 4>(p, grid, st);
+  return bwd<E, W, 1024, Chunk<E>::N == 4 ? 4 : 2>(p, grid, st);
 }
 
 }  // namespace
 
-int norm_bwd_groups(int64_t rows, int64_t cols) {
-  (void)cols;
-  const int64_t most = 512;
-  return (int)(rows < most ? rows : most);
-}
+int norm_bwd_groups(int64_t rows) { return (int)(rows < kBwdGroups ? rows : kBwdGroups); }
 
 hipError_t launch_layer_norm_fwd(const NormFwdParams& p, bool f32, bool wf32, hipStream_t st) {
   if (f32) return wf32 ? fwd_any<float, float>(p, st) : fwd_any<float, bf16_t>(p, st);
@@ -319,14 +358,14 @@ hipError_t launch_layer_norm_fwd(const NormFwdParams& p, bool f32, bool wf32, hi
 
 hipError_t launch_layer_norm_bwd(const NormBwdParams& p, bool f32, bool wf32, float* dweight, float* dbias,
                                  bool accumulate, hipStream_t st) {
-  const int grid = norm_bwd_groups(p.rows, p.cols);
+  int grid = 0;   // without rows the sums are of nothing
   hipError_t e = hipSuccess;
-  if (grid > 0) {
+  if (p.rows > 0) {
     if (f32) e = wf32 ? bwd_any<float, float>(p, grid, st) : bwd_any<float, bf16_t>(p, grid, st);
     else e = wf32 ? bwd_any<bf16_t, float>(p, grid, st) : bwd_any<bf16_t, bf16_t>(p, grid, st);
   }
   if (e != hipSuccess || (!dweight && !dbias)) return e;
-  layer_norm_grad_kernel<<<dim3((uint32_t)((p.cols + 15) / 16), 2), dim3(256), 0, st>>>(
+  layer_norm_grad_kernel<<<dim3((uint32_t)((p.cols + 63) / 64), 2), kThreads, 0, st>>>(
       p.part, grid, p.cols, dweight, dbias, accumulate ? 1 : 0);
   return hipGetLastError();
 }

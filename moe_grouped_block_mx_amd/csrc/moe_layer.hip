@@ -46,24 +46,13 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k == 0xFFFFFFFFu ? 0x7FC00000u : k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
-// Reductions over rows of 16 lanes by DPP rotations: a few cycles a step,
-// where a shuffle through LDS takes a hundred. Halving rotations give every
-// lane the same pairs, so all 16 get the same bits.
-template <int N>
-__device__ __forceinline__ uint32_t rotate(uint32_t v) {   // row_ror:N
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, 0x120 + N, 0xF, 0xF, false);
-}
+// Over rows of 16 lanes, in every lane
 template <class Op>
 __device__ __forceinline__ uint32_t row_reduce(uint32_t v, Op op) {
   v = op(v, rotate<8>(v));
   v = op(v, rotate<4>(v));
   v = op(v, rotate<2>(v));
   return op(v, rotate<1>(v));
-}
-__device__ __forceinline__ float row_total(float f) {
-  return __uint_as_float(row_reduce(__float_as_uint(f), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
 }
 
 // The top-k of four tokens by a wave, 16 lanes to a token: lane l has experts
@@ -113,7 +102,7 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, int& id, 
 #pragma unroll
     for (int i = 0; i < PER; ++i) total += i * 16 + lane < p.experts ? expf(v[i] - high) : 0.f;
   }
-  total = row_total(total);
+  total = lanes_sum<16>(total);
   weight = id >= 0 ? e / total : 0.f;
 }
 
