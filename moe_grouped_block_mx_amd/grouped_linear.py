@@ -188,6 +188,14 @@ class GroupedLinear(torch.nn.Module):
         m_splits = [int(m) for m in m_splits]
         return _GroupedLinearFn.apply(x, self.weight, m_splits, self, is_first_microbatch, out, dgrad_out)
 
+    def quantized_weight(self):
+        """(codes, scales, format) of the weight as the forward reads it, from
+        the same cache (quantized again only when the weight changed): what the
+        serving form of the layer (mxgg_moe_layer) takes."""
+        (q, s), _ = self._cache.get(self.weight, self.recipe, self.num_experts, self.out_features, self.in_features)
+        f = _formats(self.recipe, self.out_features, self.in_features)["fwd_w"]
+        return q, s, L.FORMATS[f] if isinstance(f, str) else f
+
     def _run_wgrad(self, job):
         dq, ds, xq, xs, m_splits, mpad, accumulate = job
         L.mxgg_grouped_wgrad(dq, ds, xq, xs, m_splits, self.out_features, self.in_features, mpad,
