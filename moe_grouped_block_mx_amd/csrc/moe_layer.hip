@@ -362,6 +362,28 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// The lists of a call to LDS: segments as expert << 8 | tokens and base, the
+// rows as `put` keeps them. Returns how many segments there are. The loads of a
+// thread's first elements go out together: one latency, where a loop after the
+// other pays three.
+template <int THREADS, class Put>
+__device__ __forceinline__ int lists_to_lds(const MoeParams& p, int32_t* segments, Put put) {
+  const int t = threadIdx.x;
+  const int count = *p.count;
+  MoeSegment sg = p.segments[min(t, p.most_segments - 1)];
+  MoeRow row = p.row_list[min(t, p.rows - 1)];
+  for (int i = t; i < p.most_segments; i += THREADS) {
+    if (i != t) sg = p.segments[i];
+    segments[2 * i] = sg.expert << 8 | sg.tokens;
+    segments[2 * i + 1] = sg.base;
+  }
+  for (int i = t; i < p.rows; i += THREADS) {
+    if (i != t) row = p.row_list[i];
+    put(i, row);
+  }
+  return count;
+}
+
 // How the first product is cut, by the token DMAs of a piece: tiles of W1 (and
 // W3) that a wave holds, waves, and pieces in a ring. What the rings leave of
 // 160 KiB holds the lists and sums. More tokens want more rows for each load
@@ -387,13 +409,7 @@ __global__ __launch_bounds__(64 * UpCut<XN>::WAVES) void moe_up_kernel(MoeParams
   uint8_t* tokens = reinterpret_cast<uint8_t*>(segments + 2 * p.most_segments);
   const int lane = threadIdx.x % 64, wave = wave_id(), col = lane % 16, g = lane / 16;
   const int tiles = p.inner / (16 * TILES);
-  for (int i = threadIdx.x; i < p.most_segments; i += THREADS) {
-    const MoeSegment sg = p.segments[i];
-    segments[2 * i] = sg.expert << 8 | sg.tokens;
-    segments[2 * i + 1] = sg.base;
-  }
-  for (int i = threadIdx.x; i < p.rows; i += THREADS) tokens[i] = (uint8_t)p.row_list[i].token;
-  const int units = *p.count * tiles;
+  const int units = lists_to_lds<THREADS>(p, segments, [&](int i, const MoeRow& r) { tokens[i] = (uint8_t)r.token; }) * tiles;
   const int start = blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8;   // the grid is a multiple of 8
   __syncthreads();
   if (start >= units) return;
@@ -475,7 +491,7 @@ __global__ __launch_bounds__(64 * UpCut<XN>::WAVES) void moe_up_kernel(MoeParams
 template <int RT, int XN, bool MANY>   // MANY: more than 32 tokens
 struct DownCut {
   static constexpr int WAVES = RT == 4 ? 4 : 8;
-  static constexpr int SLOTS = RT == 4 ? (XN == 1 ? 5 : 4) - (MANY ? 1 : 0) : RT == 2 ? 6 - XN : 9 - 2 * XN;
+  static constexpr int SLOTS = RT == 4 ? (XN == 1 ? 5 : 4) - (MANY ? 1 : 0) : RT == 2 ? 6 - XN : 4;
 };
 
 // The same for the second product: y for 16 RT output columns and all tokens.
@@ -500,17 +516,11 @@ __global__ __launch_bounds__(RT == 4 ? 256 : 512) void moe_down_kernel(MoeParams
   float* weights = reinterpret_cast<float*>(segments + 2 * p.most_segments);
   uint8_t* tokens = reinterpret_cast<uint8_t*>(weights + p.rows);
   const int lane = threadIdx.x % 64, wave = wave_id(), col = lane % 16, g = lane / 16;
-  for (int i = threadIdx.x; i < p.most_segments; i += THREADS) {
-    const MoeSegment sg = p.segments[i];
-    segments[2 * i] = sg.expert << 8 | sg.tokens;
-    segments[2 * i + 1] = sg.base;
-  }
-  for (int i = threadIdx.x; i < p.rows; i += THREADS) {
-    weights[i] = p.row_list[i].weight;
-    tokens[i] = (uint8_t)p.row_list[i].token;
-  }
+  const int count = lists_to_lds<THREADS>(p, segments, [&](int i, const MoeRow& r) {
+    weights[i] = r.weight;
+    tokens[i] = (uint8_t)r.token;
+  });
   for (int i = threadIdx.x; i < WAVES * p.tokens * (ROWS / 4); i += THREADS) sums[i] = v4f{0.f, 0.f, 0.f, 0.f};
-  const int count = *p.count;
   __syncthreads();
   const int pieces = (p.inner + R::ELEMS - 1) / R::ELEMS;
   const int total = count * pieces;
