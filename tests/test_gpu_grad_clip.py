@@ -151,3 +151,10 @@ def test_graph_replays():
         torch.cuda.synchronize()
         want = mxg.clip_grad_norm(fresh, 1.0)
         assert torch.equal(total, want) and all(torch.equal(a, b) for a, b in zip(grads, fresh))
+
+
+def test_more_elements_than_32_bits_count():
+    g = torch.zeros(2 ** 31 + 5, dtype=BF16, device="cuda")
+    g[0], g[-1] = 3.0, 4.0
+    assert float(mxg.clip_grad_norm([g], 1.0)) == 5.0
+    assert torch.equal(g[[0, -1]].cpu(), torch.tensor([0.6, 0.8]).bfloat16()) and int(g.count_nonzero()) == 2

@@ -214,3 +214,16 @@ def test_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, step()))
+
+
+def test_offsets_past_32_bits():
+    # row 2 begins 2.4e9 elements into its buffer
+    ld = 1_200_000_000
+    buf = torch.empty(2 * ld + 1000, dtype=BF16, device="cuda")
+    x = torch.as_strided(buf, (3, 1000), (ld, 1))
+    x.copy_(make(3, 1000, BF16, 0, 1))
+    y, mean, rstd = check_fwd(x, None, None)
+    dy = make(3, 1000, BF16, 0, 2)
+    check_bwd(dy, x, None, mean, rstd, mxg.layer_norm_bwd(dy, x, None, mean, rstd))
+    mxg.layer_norm_fwd(x, y=x)
+    assert torch.equal(x, y)

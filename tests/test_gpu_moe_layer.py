@@ -262,3 +262,50 @@ def test_output_and_workspace_end_where_they_should():
     outs = torch.full((7, 64), 3.0, dtype=torch.bfloat16, device="cuda")
     layer.run(x, logits, 2, ws=buf[:need], out=outs[:5])
     assert (buf[need:] == 7).all() and (outs[5:] == 3).all()
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_scales_at_the_ends_of_their_range(fmt):
+    # as above, one scale for each of 2 x 32 columns: 2^-127 to 2^127, within
+    # what bf16 holds of the products (its smallest step is 2^-133)
+    n = 64
+    w13 = np.zeros((2 * n, n), np.float32)
+    w13[np.arange(n), np.arange(n)] = 64.0
+    w13[n + np.arange(n), np.arange(n)] = 1.0 / 64
+    w13_q, w13_s = mxg.quantize_rowwise(torch.from_numpy(w13).cuda().bfloat16(), mxg.FORMATS[fmt])
+    rng = np.random.default_rng(2)
+    q = rng.integers(0, 256, (n, n // 2 if fmt == "mxfp4" else n), dtype=np.uint8)
+    q[(q & 0x7F) == 0x7F] = 0x7E
+    s = np.zeros((n, 2), np.uint8)
+    s[:, 0] = np.resize([0, 1, 2, 3, 8, 9, 10, 20], n)
+    s[:, 1] = np.resize([230, 240, 244, 245, 127, 126, 128, 100], n)
+    dense = omx.dequantize_rowwise(q, s, fmt)
+    x = torch.eye(n, device="cuda").bfloat16()
+    out, _, _ = mxg.moe_layer(x, torch.zeros((n, 1), device="cuda"), w13_q, w13_s, torch.from_numpy(q).cuda(),
+                              torch.from_numpy(np.ascontiguousarray(s.T)).cuda(), 1, fmt=fmt)
+    want = torch.from_numpy(np.ascontiguousarray(dense.T)).float().bfloat16()
+    assert torch.equal(out.cpu(), want)
+
+
+@pytest.mark.parametrize("layout", ["rows", "kblock"])
+def test_weights_past_32_bit_offsets(layout):
+    # 4.4 GB of W1 and W3 codes; only the last expert's are not zero
+    E, H, inner = 130, 8192, 2048
+    layer = Layer(1, H, inner, "mxfp8", layout, seed=5)
+
+    def last_of(t, rows, at):
+        shape = list(t.shape)
+        shape[at] = E * rows
+        big = torch.zeros(shape, dtype=t.dtype, device="cuda")
+        big.narrow(at, (E - 1) * rows, rows).copy_(t)
+        return big
+    axis = 1 if layout == "kblock" else 0
+    w13_q, w2_q = last_of(layer.w13_q, 2 * inner, axis), last_of(layer.w2_q, H, axis)
+    w13_s, w2_s = last_of(layer.w13_s, 2 * inner, 1), last_of(layer.w2_s, H, 1)
+    assert w13_q.numel() > 2 ** 32
+    x, _ = tokens(3, H, 1)
+    logits = torch.zeros((3, E), device="cuda")
+    logits[:, E - 1] = 1.0
+    out, ids, _ = mxg.moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, 1, fmt=layer.fmt)
+    assert (ids == E - 1).all()
+    assert torch.equal(out, layer.run(x, logits[:, :1], 1)[0])
