@@ -136,13 +136,8 @@ def _torch():
 
 
 def _stream(t):
-    """torch's current stream on the tensor's device, as the C ABI takes it
-    (the raw handle: building a torch.cuda.Stream around it takes longer than
-    a small launch)."""
-    index = t.get_device()
-    if index < 0:
-        raise ValueError(f"expected a GPU tensor, got one on {t.device}")
-    return ctypes.c_void_p(_torch()._C._cuda_getCurrentRawStream(index))
+    torch = _torch()
+    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
 
 
 def _ptr(t):
@@ -454,16 +449,30 @@ def mxgg_grouped_wgrad(dycol_q, dycol_s, xcol_q, xcol_s, m_splits, N, K, mpad, m
     return main_grad
 
 
-_KINDS = {_torch().bfloat16: BF16, _torch().float32: F32}
+# The operators below are called for single tokens too, where a launch takes a
+# few microseconds: their bindings pass addresses as plain ints and look a
+# caller's buffer over only where one was given.
+_f32_t, _u8_t, _i32_t = _torch().float32, _torch().uint8, _torch().int32
+_KINDS = {_torch().bfloat16: BF16, _f32_t: F32}
+_raw_stream = _torch()._C._cuda_getCurrentRawStream
 
 
 def _dtype(t, name):
-    torch = _torch()
-    if t.dtype is torch.bfloat16:
-        return BF16
-    if t.dtype is torch.float32:
-        return F32
-    raise ValueError(f"{name} must be bf16 or fp32, got {str(t.dtype).replace('torch.', '')}")
+    kind = _KINDS.get(t.dtype)
+    if kind is None:
+        raise ValueError(f"{name} must be bf16 or fp32, got {str(t.dtype).replace('torch.', '')}")
+    return kind
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(t):
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"expected a GPU tensor, got one on {t.device}")
+    return _raw_stream(index)
 
 
 def _rows2d(t, name):
@@ -504,15 +513,15 @@ def _cols_vector(t, name, x):
 def _f32_out(t, name, n, x):
     """fp32 [n] beside x: the caller's, or a new one."""
     if t is None:
-        return x.new_empty(n, dtype=_torch().float32)
-    return _on(_expect(t, name, (n,), _torch().float32), x, name)
+        return x.new_empty(n, dtype=_f32_t)
+    return _on(_expect(t, name, (n,), _f32_t), x, name)
 
 
 def _ws(ws, need, like):
     """The caller's workspace, or one from torch's allocator on the current
     stream (which keeps it from other streams until this one's work is done)."""
     if ws is None:
-        return like.new_empty(need, dtype=_torch().uint8), need
+        return like.new_empty(need, dtype=_u8_t), need
     if not ws.is_contiguous():
         raise ValueError("ws must be contiguous")
     return _on(ws, like, "ws"), ws.numel() * ws.element_size()
@@ -532,8 +541,8 @@ def mxgg_layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, y=None, mean=None, 
     else:
         ldy = _rows_like(y, x, "y")
     mean, rstd = _f32_out(mean, "mean", rows, x), _f32_out(rstd, "rstd", rows, x)
-    _check(lib.mxgg_layer_norm_fwd(_ptr(x), rows, cols, ldx, dt, _ptr(weight), _ptr(bias), wd or bd or 0, eps, _ptr(y),
-                                   ldy, _ptr(mean), _ptr(rstd), _stream(x)))
+    _check(lib.mxgg_layer_norm_fwd(x.data_ptr(), rows, cols, ldx, dt, _at(weight), _at(bias), wd or bd or 0, eps,
+                                   y.data_ptr(), ldy, mean.data_ptr(), rstd.data_ptr(), _stream_of(x)))
     return y, mean, rstd
 
 
@@ -558,9 +567,9 @@ def mxgg_layer_norm_bwd(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=
         raise ValueError("mean and rstd are required")
     mean, rstd = _f32_out(mean, "mean", rows, x), _f32_out(rstd, "rstd", rows, x)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_layer_norm_bwd_workspace(rows, cols)), x)
-    _check(lib.mxgg_layer_norm_bwd(_ptr(dy), lddy, _ptr(x), ldx, rows, cols, dt, _ptr(weight), wd or 0, _ptr(mean),
-                                   _ptr(rstd), _ptr(dx), lddx, _ptr(dweight), _ptr(dbias), 1 if accumulate else 0,
-                                   _ptr(ws), ws_bytes, _stream(x)))
+    _check(lib.mxgg_layer_norm_bwd(dy.data_ptr(), lddy, x.data_ptr(), ldx, rows, cols, dt, _at(weight), wd or 0,
+                                   mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), lddx, _at(dweight), _at(dbias),
+                                   1 if accumulate else 0, ws.data_ptr(), ws_bytes, _stream_of(x)))
     return dx, dweight, dbias
 
 
@@ -600,7 +609,7 @@ def _total(total, like):
     torch = _torch()
     if total is None:
         return torch.empty((), dtype=torch.float32, device="cuda") if like is None \
-            else like.new_empty((), dtype=torch.float32)
+            else like.new_empty((), dtype=_f32_t)
     if total.dtype != torch.float32 or total.numel() != 1:
         raise ValueError("total must be one fp32 value")
     return total if like is None else _on(total, like, "total")
@@ -614,7 +623,7 @@ def mxgg_grad_norm(grads, norm_type=2.0, total=None, ws=None):
     n, ptrs, numels, dtypes, like = _grad_list(grads, total)
     total = _total(total, like)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_grad_norm_workspace(n)), total)
-    _check(lib.mxgg_grad_norm(ptrs, numels, dtypes, n, kind, _ptr(total), _ptr(ws), ws_bytes, _stream(total)))
+    _check(lib.mxgg_grad_norm(ptrs, numels, dtypes, n, kind, total.data_ptr(), ws.data_ptr(), ws_bytes, _stream_of(total)))
     return total
 
 
@@ -625,8 +634,8 @@ def mxgg_clip_grad_norm(grads, max_norm, norm_type=2.0, total=None, ws=None):
     n, ptrs, numels, dtypes, like = _grad_list(grads, total)
     total = _total(total, like)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_grad_norm_workspace(n)), total)
-    _check(lib.mxgg_clip_grad_norm(ptrs, numels, dtypes, n, kind, max_norm, _ptr(total), _ptr(ws), ws_bytes,
-                                   _stream(total)))
+    _check(lib.mxgg_clip_grad_norm(ptrs, numels, dtypes, n, kind, max_norm, total.data_ptr(), ws.data_ptr(), ws_bytes,
+                                   _stream_of(total)))
     return total
 
 
@@ -636,7 +645,7 @@ def mxgg_clip_grads_with_norm(grads, max_norm, total):
     total = _total(total, None)
     n, ptrs, numels, dtypes, like = _grad_list(grads, total)
     _on(total, like, "total")
-    _check(lib.mxgg_clip_grads_with_norm(ptrs, numels, dtypes, n, max_norm, _ptr(total), _stream(total)))
+    _check(lib.mxgg_clip_grads_with_norm(ptrs, numels, dtypes, n, max_norm, total.data_ptr(), _stream_of(total)))
     return total
 
 
@@ -664,14 +673,14 @@ def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", reno
     _expect(w2_q, "w2_q", _q_shape(f, E * H, inner), torch.uint8)
     _expect(w2_s, "w2_s", _row_scale_shape(f, E * H, inner), _sdtype(f))
     out = x.new_empty((T, H)) if out is None else _expect(out, "out", (T, H), torch.bfloat16)
-    ids = x.new_empty((T, top_k), dtype=torch.int32) if ids is None else _expect(ids, "ids", (T, top_k), torch.int32)
-    weights = x.new_empty((T, top_k), dtype=torch.float32) if weights is None \
-        else _expect(weights, "weights", (T, top_k), torch.float32)
+    ids = x.new_empty((T, top_k), dtype=_i32_t) if ids is None else _expect(ids, "ids", (T, top_k), _i32_t)
+    weights = x.new_empty((T, top_k), dtype=_f32_t) if weights is None \
+        else _expect(weights, "weights", (T, top_k), _f32_t)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_moe_layer_workspace(T, E, top_k, inner)), x)
-    _check(lib.mxgg_moe_layer(_ptr(x), x.stride(0) if T > 1 else H, _ptr(logits), ldl, ldt, T, H,
-                              inner, E, top_k, _ptr(w13_q), _ptr(w13_s), _ptr(w2_q), _ptr(w2_s), f,
-                              MOE_RENORMALIZE if renormalize else 0, _ptr(out), _ptr(ids), _ptr(weights), _ptr(ws),
-                              ws_bytes, _stream(x)))
+    _check(lib.mxgg_moe_layer(x.data_ptr(), x.stride(0) if T > 1 else H, logits.data_ptr(), ldl, ldt, T, H, inner, E,
+                              top_k, w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), f,
+                              MOE_RENORMALIZE if renormalize else 0, out.data_ptr(), ids.data_ptr(),
+                              weights.data_ptr(), ws.data_ptr(), ws_bytes, _stream_of(x)))
     return out, ids, weights
 
 

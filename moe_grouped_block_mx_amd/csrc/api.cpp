@@ -93,11 +93,13 @@ Check check_on_device(const void* p, int dev, const char* name) {
 }
 
 // Arch + device membership of every pointer; returns the device's CU count.
-Check device_checks(hipStream_t st, std::initializer_list<std::pair<const void*, const char*>> ptrs, int* num_cus) {
+Check device_checks(hipStream_t st, std::initializer_list<std::pair<const void*, const char*>> ptrs, int* num_cus,
+                    int* device = nullptr) {
   int dev = 0;
   MXGG_TRY(stream_device(st, &dev));
   MXGG_TRY(check_arch(dev, num_cus));
   for (auto& pr : ptrs) MXGG_TRY(check_on_device(pr.first, dev, pr.second));
+  if (device) *device = dev;
   return Check{};
 }
 
@@ -179,8 +181,7 @@ Check grad_norm_and_clip(void* const* grads, const int64_t* numels, const int32_
   MXGG_TRY(check_workspace(ws, ws_bytes, mxgg_grad_norm_workspace(n)));
   const std::vector<ClipBatch> batches = clip_batches(grads, numels, dtypes, n);
   int cus = 0, dev = 0;
-  MXGG_TRY(stream_device(stream, &dev));
-  MXGG_TRY(device_checks(stream, {{total, "total"}, {ws, "ws"}}, &cus));
+  MXGG_TRY(device_checks(stream, {{total, "total"}, {ws, "ws"}}, &cus, &dev));
   MXGG_TRY(check_grads_on_device(grads, numels, n, dev));
   double* part = static_cast<double*>(ws);
   const bool mx = kind == MXGG_NORM_MAX;
@@ -599,8 +600,7 @@ mxgg_status mxgg_clip_grads_with_norm(void* const* grads, const int64_t* numels,
     const std::vector<ClipBatch> batches = clip_batches(grads, numels, dtypes, n);
     if (batches.empty()) return Check{};
     int cus = 0, dev = 0;
-    MXGG_TRY(stream_device(stream, &dev));
-    MXGG_TRY(device_checks(stream, {{total, "total"}}, &cus));
+    MXGG_TRY(device_checks(stream, {{total, "total"}}, &cus, &dev));
     MXGG_TRY(check_grads_on_device(grads, numels, n, dev));
     for (const ClipBatch& b : batches)
       MXGG_TRY(hip_status(launch_clip(b, nullptr, 0, false, max_norm, const_cast<float*>(total), false, stream),
