@@ -134,11 +134,22 @@ struct MoeParams {
   int64_t q13_row, q13_piece, s13_block, q2_row, q2_piece, s2_block;
 };
 enum MoeFormat { kMoeFp4 = 0, kMoeFp8 = 1, kMoeBlock = 2 };
-// How a call is cut. A segment of few tokens leaves more of the LDS to weights
-// in flight, one of many reads an expert's weights less often (again out of the
-// caches): about the tokens that a chosen expert has, by chance spread
-// included. With E2M1 codes a 1 KiB load brings 4 tokens' piece, with E4M3
-// codes 8.
+// How a call is cut.
+//
+// Segments: one of few tokens leaves more of the LDS to weights in flight, one of
+// many reads an expert's weights less often (again out of the caches). So about
+// the tokens of a chosen expert and half as many more, for the spread of chance:
+// with just their mean the whole layer took 90 us instead of 78 (32 tokens, 32
+// experts of 4096 x 1536 in MXFP4) and 584 instead of 505 (64 tokens, 64 experts
+// of 7168 x 2048, blockwise). With E2M1 codes a 1 KiB load brings 4 tokens'
+// piece, with E4M3 codes 8.
+//
+// Second product: a wave's 16 rows of weights cost as much in loads of tokens as
+// 64 do. With few tokens that is little, and 16-row tiles give every CU a
+// workgroup (1 token, 4096 outputs: 27.5 us, 64-row tiles 30.5). Otherwise the
+// tiles are 64 rows and the segments are split over workgroups, with the parts
+// added up after (8 tokens, 7168 outputs: 127 us, 16-row tiles 136; 64 tokens
+// there: 505 us, without the split 568; 32 tokens, 4096 outputs: 78 and 114).
 inline void moe_plan(MoeParams& p, MoeFormat fmt) {
   const int each = fmt == kMoeFp4 ? 4 : 8, most = fmt == kMoeFp4 ? 3 : 2;
   const int chosen = p.rows < p.experts ? p.rows : p.experts;
@@ -146,18 +157,15 @@ inline void moe_plan(MoeParams& p, MoeFormat fmt) {
   p.dmas = (want + each - 1) / each;
   if (p.dmas > most) p.dmas = most;
   p.segment = p.dmas * each;
-  // A wave's 16 rows of weights cost as much in loads of tokens as 64 do. With
-  // few tokens that is little, and small tiles give every CU a workgroup; with
-  // more the tiles are 64 rows, and the segments are split over workgroups.
-  if (p.tokens <= 16 && p.dmas <= 2) {
-    p.down_tiles = p.hidden >= 6144 ? 2 : 1;
+  p.most_segments = (int32_t)moe_most_segments(p.tokens, p.experts, p.top_k, p.segment);
+  if (p.tokens <= 16 && p.dmas <= 2 && p.hidden < 6144) {
+    p.down_tiles = 1;
     p.splits = 1;
   } else {
     p.down_tiles = 4;
     p.splits = kMoeDownGroups * 64 / p.hidden;
     p.splits = p.splits < 1 ? 1 : p.splits > 8 ? 8 : p.splits;
   }
-  p.most_segments = (int32_t)moe_most_segments(p.tokens, p.experts, p.top_k, p.segment);
 }
 hipError_t launch_moe_layer(MoeParams p, MoeFormat fmt, int num_cus, hipStream_t st);
 

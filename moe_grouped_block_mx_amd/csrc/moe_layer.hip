@@ -491,7 +491,7 @@ __global__ __launch_bounds__(64 * UpCut<XN>::WAVES) void moe_up_kernel(MoeParams
 template <int RT, int XN, bool MANY>   // MANY: more than 32 tokens
 struct DownCut {
   static constexpr int WAVES = RT == 4 ? 4 : 8;
-  static constexpr int SLOTS = RT == 4 ? (XN == 1 ? 5 : 4) - (MANY ? 1 : 0) : RT == 2 ? 6 - XN : 4;
+  static constexpr int SLOTS = RT == 4 ? (XN == 1 ? 5 : 4) - (MANY ? 1 : 0) : 4;
 };
 
 // The same for the second product: y for 16 RT output columns and all tokens.
@@ -661,10 +661,8 @@ hipError_t down(const MoeParams& p, hipStream_t st) {
 
 template <MoeFormat F, int XN, bool TAIL>
 hipError_t down_tiles(const MoeParams& p, hipStream_t st) {
-  if constexpr (XN < 3) {
+  if constexpr (XN < 3)
     if (p.down_tiles == 1) return down<F, 1, XN, TAIL, false>(p, st);
-    if (p.down_tiles == 2) return down<F, 2, XN, TAIL, false>(p, st);
-  }
   return p.tokens > 32 ? down<F, 4, XN, TAIL, true>(p, st) : down<F, 4, XN, TAIL, false>(p, st);
 }
 
