@@ -542,7 +542,8 @@ mxgg_status mxgg_clip_grads_with_norm(void* const* grads, const int64_t* numels,
  * A whole expert layer for a few tokens (decoding): routing, gate and up
  * projections, SiLU gating, down projection and the weighted sum, on weights
  * quantized as for the grouped GEMMs; activations are bf16 and not quantized.
- *   x         bf16 [tokens, hidden], leading dimension ldx (multiple of 8).
+ *   x         bf16 [tokens, hidden], leading dimension ldx (multiple of 8,
+ *             below 2^25).
  *   logits    [tokens, experts] of `ldtype`, leading dimension ldl: the gate's
  *             output, element-aligned. Per token the top_k largest are chosen,
  *             equal ones by the lowest index; -inf is never chosen; NaN ranks

@@ -21,9 +21,6 @@ __device__ __forceinline__ float bf16_low(uint32_t w) { return __uint_as_float(w
 __device__ __forceinline__ float bf16_high(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 __device__ __forceinline__ float load_one(const bf16_t* p) { return __uint_as_float((uint32_t)p->bits << 16); }
-__device__ __forceinline__ float load_one(const float* p) { return *p; }
-__device__ __forceinline__ void store_one(bf16_t* p, float v) { p->bits = (uint16_t)bf16_pair(v, 0.f); }
-__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 
 // 16 bytes of elements as they lie in memory: 8 bf16 or 4 fp32. Loads and
 // stores go through memcpy with the element's alignment only, which on gfx950
