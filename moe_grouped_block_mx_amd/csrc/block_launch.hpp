@@ -1,5 +1,5 @@
 // Internal launch interface of the operators around the expert layer, between
-// the C ABI (block_api.cpp) and their kernels. Not part of the public ABI.
+// the C ABI (api.cpp) and their kernels. Not part of the public ABI.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -86,8 +86,8 @@ inline int64_t moe_most_segments(int64_t tokens, int64_t experts, int64_t top_k,
   return rows / segment + (rows < experts ? rows : experts);
 }
 // Workspace: how many segments there are, their list, the rows,
-// the second product's parts and the inner activation, bf16 (laid out as its reader takes it: inner_at in
-// moe_layer.hip).
+// the second product's parts and the inner activation, bf16 (laid out as its
+// reader takes it: inner_at in moe_layer.hip).
 struct MoeWorkspace {
   size_t segments, rows, parts, inner, bytes;
 };

@@ -11,10 +11,10 @@
 // All sums are fp32.
 //
 // Both passes are bound by memory. Forward, 16384 x 7168 bf16: 90 us, 5.2 TB/s (a
-// plain 2 GiB copy: 4.9). Backward, 4096 x 4096 bf16: 25 us, 4.0 TB/s, then 4 us
-// for the columns' partial sums (8 MB); 2500 x 5001 fp32: 34 + 4 us, 4.4 TB/s;
-// 16384 x 7168 bf16: 159 us together, 4.4 TB/s. 8 x 4096 forward: 3.3 us, the
-// time of an empty launch and one trip to memory.
+// plain 2 GiB copy: 4.9). Backward, 4096 x 4096 bf16: 23 us, 4.4 TB/s, then 4 us
+// for the columns' partial sums (8 MB); 2500 x 5001 fp32: 37 us together, 4.1
+// TB/s; 16384 x 7168 bf16: 140 us, 5.0 TB/s. 8 x 4096 forward: 3.3 us, the time
+// of an empty launch and one trip to memory.
 #include "block_common.hpp"
 #include "block_launch.hpp"
 
@@ -117,6 +117,10 @@ __global__ __launch_bounds__(T) void layer_norm_fwd_kernel(NormFwdParams p) {
   // squares of (x - mu) / sqrt(C): their sum is the variance, and finite
   // wherever that is
   const float root = 1.f / sqrtf((float)p.cols);
+  // and x over the power of two from C up (exact): no sum is larger than the
+  // largest x
+  const int bits = 32 - __clz(p.cols - 1);
+  const float down = __uint_as_float((uint32_t)(127 - bits) << 23), count = (float)p.cols * down;
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t row = (int64_t)blockIdx.x * G + threadIdx.x / L;
   Chunk<E> next[NV];
@@ -136,10 +140,10 @@ __global__ __launch_bounds__(T) void layer_norm_fwd_kernel(NormFwdParams p) {
     for (int i = 0; i < NV; ++i) {
       const Cols at((i * L + lane) * N, p.cols);
 #pragma unroll
-      for (int j = 0; j < N; ++j) s[0] += at.has(j) ? c[i].get(j) : 0.f;
+      for (int j = 0; j < N; ++j) s[0] = fmaf(at.has(j) ? c[i].get(j) : 0.f, down, s[0]);
     }
     row_sum<L, T, 1>(s, lds, 0);
-    const float mean = s[0] / (float)p.cols;
+    const float mean = s[0] / count;
     float q[1] = {0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -172,10 +176,10 @@ __global__ __launch_bounds__(T) void layer_norm_fwd_kernel(NormFwdParams p) {
   }
 }
 
-// The same walk, with the column sums of dy xh and dy in registers; at the end
-// the G row groups meet in LDS and the workgroup writes one partial sum per
-// column.
-template <class E, class W, int L, int NV, int T>
+// The same walk, AHEAD steps of loads on their way, with the column sums of dy
+// xh and dy in registers; at the end the G row groups meet in LDS and the
+// workgroup writes one partial sum per column.
+template <class E, class W, int L, int NV, int T, int AHEAD>
 __global__ __launch_bounds__(T) void layer_norm_bwd_kernel(NormBwdParams p) {
   constexpr int N = Chunk<E>::N, G = T / L;
   __shared__ float lds[2][T / 64][2];
@@ -194,31 +198,49 @@ __global__ __launch_bounds__(T) void layer_norm_bwd_kernel(NormBwdParams p) {
   const float inv = 1.f / (float)p.cols;
   const int64_t step = (int64_t)gridDim.x * G;
   int64_t row = (int64_t)blockIdx.x * G + grp;
-  Chunk<E> next_x[NV], next_g[NV];
-  float next_mean, next_rstd;
-  const auto load = [&](int64_t r) {
-    // a group past the last row computes it again and adds nothing
+  constexpr int SLOTS = AHEAD ? AHEAD : 1;
+  Chunk<E> next_x[SLOTS][NV], next_g[SLOTS][NV];
+  float next_mean[SLOTS], next_rstd[SLOTS];
+  const auto load = [&](int b, int64_t r) {
+    // a group past the last row reads that one, and counts it as zeros
     const int64_t at = r < p.rows ? r : p.rows - 1;
     const E* x = static_cast<const E*>(p.x) + at * p.ldx;
     const E* dy = static_cast<const E*>(p.dy) + at * p.lddy;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const Cols c((i * L + lane) * N, p.cols);
-      c.load(next_x[i], x);
-      c.load(next_g[i], dy);
+      c.load(next_x[b][i], x);
+      c.load(next_g[b][i], dy);
     }
-    next_mean = p.mean[at];
-    next_rstd = p.rstd[at];
+    next_mean[b] = p.mean[at];
+    next_rstd[b] = p.rstd[at];
   };
-  load(row);
+#pragma unroll
+  for (int b = 0; b < AHEAD; ++b)
+    if (b == 0 || (int64_t)blockIdx.x * G + b * step < p.rows) load(b, row + b * step);
   int slot = 0;
   for (int64_t base = (int64_t)blockIdx.x * G; base < p.rows; base += step, row += step, slot ^= 1) {
     const bool on = row < p.rows;
     Chunk<E> cx[NV], cg[NV];
+    if (AHEAD == 0) load(0, row);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) cx[i] = next_x[i], cg[i] = next_g[i];
-    const float mean = next_mean, rstd = next_rstd;
-    if (base + step < p.rows) load(row + step);
+    for (int i = 0; i < NV; ++i) {
+      cx[i] = next_x[0][i], cg[i] = next_g[0][i];
+      // of a group past the last row nothing counts: its dy below, nor its x,
+      // which is another group's dx by now where dx is over x
+      if constexpr (G > 1)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) cx[i].w[k] &= on ? ~0u : 0u;
+    }
+    const float mean = next_mean[0], rstd = next_rstd[0];
+#pragma unroll
+    for (int b = 1; b < AHEAD; ++b) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) next_x[b - 1][i] = next_x[b][i], next_g[b - 1][i] = next_g[b][i];
+      next_mean[b - 1] = next_mean[b];
+      next_rstd[b - 1] = next_rstd[b];
+    }
+    if (AHEAD && base + AHEAD * step < p.rows) load(AHEAD - 1, row + AHEAD * step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -316,7 +338,7 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(const float* 
 // each CU's two: enough rows in a workgroup to keep the weights, and a grid that
 // still evens out (16384 x 7168: 93 us; one row a workgroup 96; a grid that just
 // fills the card 106). The backward has one workgroup a CU, because each writes
-// a partial of both gradients (4096 x 4096: 29 us; two a CU 37).
+// a partial of both gradients (4096 x 4096: 27 us; two a CU 37).
 constexpr int kFwdThreads = 1 << 20, kBwdGroups = 256;
 
 template <class E, class W, int L, int NV>
@@ -329,13 +351,17 @@ hipError_t fwd(const NormFwdParams& p, hipStream_t st) {
 
 template <class E, class W, int L, int NV>
 hipError_t bwd(const NormBwdParams& p, int& grid, hipStream_t st) {
-  // 512 threads leave a thread the registers of two rows' chunks and the column
-  // sums; short rows need few, and more of them at a time (32768 x 500: 25 us
-  // with 1024 threads, 30 with 512)
-  constexpr int T = NV == 1 ? 1024 : L < 512 ? 512 : L, G = T / L;
+  // 512 threads leave a thread the registers for the column sums and the rows
+  // on their way; rows of 16 lanes need few (65536 x 96: 16 us with 1024
+  // threads, 19 with 512). Two rows ahead rather than one: 16384 x 7168 bf16 140
+  // us and 159 (three: 141); with one chunk a lane four: 32768 x 500 24 us and
+  // 25. Where the registers would spill, none: 2048 x 16384 fp32 98 us, with one
+  // 157; 4096 x 14000 bf16 92 and 101.
+  constexpr int T = L == 16 ? 1024 : L < 512 ? 512 : L, G = T / L;
+  constexpr int AHEAD = L == 16 ? 1 : NV == 1 ? 4 : NV == 4 || L == 1024 ? 0 : 2;
   const int64_t need = (p.rows + G - 1) / G;
   grid = (int)(need < kBwdGroups ? need : kBwdGroups);
-  layer_norm_bwd_kernel<E, W, L, NV, T><<<grid, T, 0, st>>>(p);
+  layer_norm_bwd_kernel<E, W, L, NV, T, AHEAD><<<grid, T, 0, st>>>(p);
   return hipGetLastError();
 }
 

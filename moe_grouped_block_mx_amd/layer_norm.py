@@ -9,6 +9,7 @@
 Every step runs in libmxgg's kernels; tensors must live on the GPU.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib as L
 
@@ -33,6 +34,7 @@ class _LayerNormFn(torch.autograd.Function):
         return y.view(x.shape)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         rows, weight, mean, rstd = ctx.saved_tensors
         m = ctx.module

@@ -227,3 +227,26 @@ def test_offsets_past_32_bits():
     check_bwd(dy, x, None, mean, rstd, mxg.layer_norm_bwd(dy, x, None, mean, rstd))
     mxg.layer_norm_fwd(x, y=x)
     assert torch.equal(x, y)
+
+
+def test_mean_of_rows_whose_sum_passes_fp32():
+    # powers of two: every partial sum is exact, so the row's deviations are 0
+    x = torch.full((3, 4096), 2.0 ** 126, device="cuda")
+    x[1] = -(2.0 ** 127)
+    y, mean, _ = mxg.layer_norm_fwd(x, None, torch.full((4096,), 0.5, device="cuda"))
+    assert torch.equal(mean, x[:, 0]) and (y == 0.5).all()
+
+
+@pytest.mark.parametrize("rows", [1, 513, 1031])
+@pytest.mark.parametrize("cols", [96, 500, 2501, 4096])
+def test_dx_over_x_with_a_last_row_that_is_not_finite(rows, cols):
+    # the groups of lanes past the last row read it too, maybe after dx is there
+    x, dy = make(rows, cols, BF16, 0, 1), make(rows, cols, BF16, 0, 2)
+    dy[-1, 5] = float("inf")
+    _, mean, rstd = mxg.layer_norm_fwd(x)
+    dx, dw, db = mxg.layer_norm_bwd(dy, x, None, mean, rstd)
+    assert not dx[-1].isfinite().any() and dx[:-1].isfinite().all()
+    assert dw.isfinite().sum() == cols - 1 and db.isfinite().sum() == cols - 1
+    got, dw2, db2 = mxg.layer_norm_bwd(dy, x, None, mean, rstd, dx=x)
+    assert got is x and torch.equal(got[:-1], dx[:-1]) and not got[-1].isfinite().any()
+    assert torch.equal(dw.nan_to_num(), dw2.nan_to_num()) and torch.equal(db, db2)
