@@ -642,6 +642,8 @@ def mxgg_clip_grad_norm(grads, max_norm, norm_type=2.0, total=None, ws=None):
 def mxgg_clip_grads_with_norm(grads, max_norm, total):
     """Scale the gradients in place by min(1, max_norm / (total + 1e-6)); total:
     fp32 scalar on the device, e.g. combined over ranks from grad_norm."""
+    if total is None:
+        raise ValueError("total is required")
     total = _total(total, None)
     n, ptrs, numels, dtypes, like = _grad_list(grads, total)
     _on(total, like, "total")

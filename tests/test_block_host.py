@@ -156,3 +156,10 @@ def test_moe_binding():
                 dict(weights=torch.zeros(T, k + 1)), dict(fmt=mx.MXFP4 | mx.KBLOCK_ROWS)):
         with pytest.raises(ValueError):
             mx.moe_layer(**{**good, **bad})
+
+
+def test_scaling_by_a_norm_needs_one():
+    # total is read here, not written: none is refused, not made up
+    for grads in ([torch.zeros(8)], []):
+        with pytest.raises(ValueError, match="total"):
+            mx.clip_grads_with_norm(grads, 1.0, None)
