@@ -223,16 +223,21 @@ __global__ __launch_bounds__(T) void layer_norm_bwd_kernel(NormBwdParams p) {
     const bool on = row < p.rows;
     Chunk<E> cx[NV], cg[NV];
     if (AHEAD == 0) load(0, row);
+    float mean = next_mean[0], rstd = next_rstd[0];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       cx[i] = next_x[0][i], cg[i] = next_g[0][i];
       // of a group past the last row nothing counts: its dy below, nor its x,
-      // which is another group's dx by now where dx is over x
+      // which is another group's dx by now where dx is over x; and with x, mean
+      // and rstd 0 so is xh (0 - mean of a large row, times rstd, may pass fp32)
       if constexpr (G > 1)
 #pragma unroll
         for (int k = 0; k < 4; ++k) cx[i].w[k] &= on ? ~0u : 0u;
     }
-    const float mean = next_mean[0], rstd = next_rstd[0];
+    if constexpr (G > 1) {
+      mean = on ? mean : 0.f;
+      rstd = on ? rstd : 0.f;
+    }
 #pragma unroll
     for (int b = 1; b < AHEAD; ++b) {
 #pragma unroll
@@ -247,9 +252,12 @@ __global__ __launch_bounds__(T) void layer_norm_bwd_kernel(NormBwdParams p) {
       const Cols at((i * L + lane) * N, p.cols);
 #pragma unroll
       for (int j = 0; j < N; ++j) {
-        // an element that does not count has dy = 0; where its xh is not finite
-        // the row's results are not either
-        const float xh = (cx[i].get(j) - mean) * rstd, d = on && at.has(j) ? cg[i].get(j) : 0.f;
+        // an element that does not count has dy = 0; one of the row's own is not
+        // finite in xh where the row's results are not either, one past a short
+        // row's end (0 - mean, times rstd) is taken as 0
+        float xh = (cx[i].get(j) - mean) * rstd;
+        if constexpr (L == 16) xh = at.has(j) ? xh : 0.f;
+        const float d = on && at.has(j) ? cg[i].get(j) : 0.f;
         s[0] += d * w[i].get(j);
         s[1] += d * w[i].get(j) * xh;
         dw[i][j] += d * xh;

@@ -250,3 +250,15 @@ def test_dx_over_x_with_a_last_row_that_is_not_finite(rows, cols):
     got, dw2, db2 = mxg.layer_norm_bwd(dy, x, None, mean, rstd, dx=x)
     assert got is x and torch.equal(got[:-1], dx[:-1]) and not got[-1].isfinite().any()
     assert torch.equal(dw.nan_to_num(), dw2.nan_to_num()) and torch.equal(db, db2)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(3, 5, F32), (3, 5, BF16), (70, 1, F32), (1, 96, BF16), (65, 128, BF16),
+                                             (9, 300, F32), (257, 4096, BF16)])
+def test_rows_whose_mean_over_their_deviation_passes_fp32(rows, cols, dtype):
+    # constant rows: xh is 0, but -mean * rstd (an element of 0 that stands in for
+    # one past the row's end, or for a row past the last) is beyond fp32
+    x = torch.full((rows, cols), 2.0 ** 123, device="cuda").to(dtype)
+    dy = make(rows, cols, dtype, 0, 2)
+    _, mean, rstd = mxg.layer_norm_fwd(x)
+    assert (mean == 2.0 ** 123).all() and not (mean * rstd).isfinite().any()
+    check_bwd(dy, x, None, mean, rstd, mxg.layer_norm_bwd(dy, x, None, mean, rstd))
