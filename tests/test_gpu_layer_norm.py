@@ -252,6 +252,7 @@ def test_dx_over_x_with_a_last_row_that_is_not_finite(rows, cols):
     assert torch.equal(dw.nan_to_num(), dw2.nan_to_num()) and torch.equal(db, db2)
 
 
+<<<<<<< Updated upstream
 @pytest.mark.parametrize("rows,cols,dtype", [(3, 5, F32), (3, 5, BF16), (70, 1, F32), (1, 96, BF16), (65, 128, BF16),
                                              (9, 300, F32), (257, 4096, BF16)])
 def test_rows_whose_mean_over_their_deviation_passes_fp32(rows, cols, dtype):
@@ -262,3 +263,37 @@ def test_rows_whose_mean_over_their_deviation_passes_fp32(rows, cols, dtype):
     _, mean, rstd = mxg.layer_norm_fwd(x)
     assert (mean == 2.0 ** 123).all() and not (mean * rstd).isfinite().any()
     check_bwd(dy, x, None, mean, rstd, mxg.layer_norm_bwd(dy, x, None, mean, rstd))
+=======
+# Rows enough that a workgroup goes through several (three trips or more, the
+# last one with some workgroups or row groups idle), for every number of lanes to
+# a row and of row loads ahead: what a trip leaves for the next is compared with
+# the reference, on rows that all differ.
+@pytest.mark.parametrize("rows,cols,dtype", [
+    (140_001, 65, BF16), (33_001, 130, BF16), (33_002, 515, BF16), (16_501, 1026, BF16), (8_300, 2050, BF16),
+    (4_200, 4100, BF16), (2_100, 8200, BF16), (140_001, 33, F32), (33_001, 250, F32), (8_300, 1030, F32), (2_100, 4100, F32),
+    (2_100, 8200, F32)])
+def test_forward_walks_many_rows(rows, cols, dtype):
+    x = make(rows, cols, dtype, 3, rows)
+    w, b = make(1, cols, F32, 0, 2, 1.0, 0.2)[0].contiguous(), make(1, cols, F32, 0, 3, 0.0)[0].contiguous()
+    y, _, _ = check_fwd(x, w, b)
+    mxg.layer_norm_fwd(x, w, b, y=x)
+    assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [
+    (35_001, 96, BF16), (12_301, 500, BF16), (7_003, 600, BF16), (3_501, 1100, BF16), (1_801, 2049, BF16),
+    (1_801, 4100, BF16), (901, 6200, BF16), (900, 8200, BF16), (600, 12_300, BF16), (600, 16_384, BF16),
+    (35_001, 61, F32), (12_301, 250, F32), (3_501, 1000, F32), (900, 4100, F32), (600, 8000, F32), (600, 8200, F32),
+    (520, 16_384, F32)])
+def test_backward_walks_many_rows(rows, cols, dtype):
+    x, dy = make(rows, cols, dtype, 3, rows), make(rows, cols, dtype, 5, rows + 1, 0.0)
+    w = make(1, cols, BF16, 0, 2, 1.0, 0.2)[0].contiguous()
+    _, mean, rstd = mxg.layer_norm_fwd(x, w)
+    first = mxg.layer_norm_bwd(dy, x, w, mean, rstd)
+    check_bwd(dy, x, w, mean, rstd, first)
+    dw0, db0 = make(1, cols, F32, 0, 4)[0].contiguous(), make(1, cols, F32, 0, 5)[0].contiguous()
+    got = mxg.layer_norm_bwd(dy, x, w, mean, rstd, dweight=dw0.clone(), dbias=db0.clone(), accumulate=True)
+    check_bwd(dy, x, w, mean, rstd, got, f64(dw0), f64(db0))
+    got = mxg.layer_norm_bwd(dy, x, w, mean, rstd, dx=x)
+    assert all(torch.equal(a, b) for a, b in zip(first, got))
+>>>>>>> Stashed changes

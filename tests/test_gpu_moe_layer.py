@@ -1,6 +1,7 @@
 """The few-token expert layer on the GPU against the fp64 reference (its bound
 is derived in oracle/block.py). Weights are quantized by the library's
 quantizers, whose codes are bit-exact with the oracle's."""
+import functools
 import math
 
 import numpy as np
@@ -309,3 +310,51 @@ def test_weights_past_32_bit_offsets(layout):
     out, ids, _ = mxg.moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, 1, fmt=layer.fmt)
     assert (ids == E - 1).all()
     assert torch.equal(out, layer.run(x, logits[:, :1], 1)[0])
+
+
+@functools.lru_cache(maxsize=None)
+def shared_layer(*args):
+    return Layer(*args)
+
+
+# The first product's workgroups (one a CU, 256) take several units of 16 or 32
+# inner columns in turn: here each has three or more, some none in the last round.
+# `inner` 1120: a last piece that is not whole; `hidden` 256 and 288: fewer pieces
+# than waves; 1056: more. One to three token loads a piece.
+@pytest.mark.parametrize("E,H,inner,fmt,layout,T,k", [
+    (16, 288, 1120, "mxfp4", "rows", 1, 8), (16, 288, 1120, "mxfp4", "rows", 13, 4), (16, 288, 1120, "mxfp4", "rows", 32, 6),
+    (16, 288, 1120, "mxfp4", "rows", 64, 4), (16, 256, 1152, "mxfp4", "kblock", 1, 8), (16, 256, 1152, "mxfp4", "kblock", 32, 6),
+    (16, 288, 1120, "mxfp8", "rows", 1, 8), (16, 288, 1120, "mxfp8", "rows", 13, 4), (16, 288, 1120, "mxfp8", "rows", 40, 5),
+    (16, 256, 1152, "fp8_128x128", "kblock", 1, 8), (16, 256, 1152, "fp8_128x128", "kblock", 13, 4),
+    (16, 256, 1152, "fp8_128x128", "kblock", 40, 5),
+    (4, 1056, 2272, "mxfp4", "rows", 1, 4), (4, 1056, 2272, "mxfp4", "rows", 26, 4), (4, 1056, 2272, "mxfp8", "rows", 3, 4)])
+def test_many_units_a_workgroup(E, H, inner, fmt, layout, T, k):
+    x, logits = tokens(T, H, E, T)
+    shared_layer(E, H, inner, fmt, layout).check(x, logits, k)
+
+
+# The second product with 64-row tiles, split over workgroups, for few tokens an
+# expert: one token load a piece (T k / E up to about 2 with E2M1 codes, 4 with E4M3)
+# or two (up to about 4; with E4M3 8), at most 32 tokens and more.
+@pytest.mark.parametrize("fmt,layout,H,inner", [
+    ("mxfp4", "rows", 96, 160), ("mxfp4", "kblock", 128, 128), ("mxfp8", "rows", 96, 160), ("mxfp8", "kblock", 128, 128),
+    ("fp8_128x128", "kblock", 128, 256)])
+@pytest.mark.parametrize("T,k", [(17, 2), (32, 4), (64, 2), (64, 4), (32, 14), (64, 6)])
+def test_many_tokens_few_to_an_expert(fmt, layout, H, inner, T, k):
+    x, logits = tokens(T, H, 100, T + k)
+    shared_layer(100, H, inner, fmt, layout).check(x, logits, k)
+
+
+@pytest.mark.parametrize("fmt,layout,inner", [("mxfp4", "rows", 96), ("mxfp8", "kblock", 128), ("fp8_128x128", "kblock", 128)])
+@pytest.mark.parametrize("T", [1, 6, 16])
+def test_wide_outputs_few_tokens(fmt, layout, inner, T):
+    # from 6144 outputs on the 64-row tiles serve single tokens too
+    x, logits = tokens(T, 6272, 5, T)
+    shared_layer(5, 6272, inner, fmt, layout).check(x, logits, 2)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+def test_most_tokens_choices_and_experts(fmt):
+    # the largest lists, and the most LDS that the second product asks for
+    x, logits = tokens(64, 32, 512, 3)
+    shared_layer(512, 32, 32, fmt, "rows").check(x, logits, 16)
