@@ -252,7 +252,6 @@ def test_dx_over_x_with_a_last_row_that_is_not_finite(rows, cols):
     assert torch.equal(dw.nan_to_num(), dw2.nan_to_num()) and torch.equal(db, db2)
 
 
-<<<<<<< Updated upstream
 @pytest.mark.parametrize("rows,cols,dtype", [(3, 5, F32), (3, 5, BF16), (70, 1, F32), (1, 96, BF16), (65, 128, BF16),
                                              (9, 300, F32), (257, 4096, BF16)])
 def test_rows_whose_mean_over_their_deviation_passes_fp32(rows, cols, dtype):
@@ -263,7 +262,7 @@ def test_rows_whose_mean_over_their_deviation_passes_fp32(rows, cols, dtype):
     _, mean, rstd = mxg.layer_norm_fwd(x)
     assert (mean == 2.0 ** 123).all() and not (mean * rstd).isfinite().any()
     check_bwd(dy, x, None, mean, rstd, mxg.layer_norm_bwd(dy, x, None, mean, rstd))
-=======
+
 # Rows enough that a workgroup goes through several (three trips or more, the
 # last one with some workgroups or row groups idle), for every number of lanes to
 # a row and of row loads ahead: what a trip leaves for the next is compared with
@@ -296,4 +295,3 @@ def test_backward_walks_many_rows(rows, cols, dtype):
     check_bwd(dy, x, w, mean, rstd, got, f64(dw0), f64(db0))
     got = mxg.layer_norm_bwd(dy, x, w, mean, rstd, dx=x)
     assert all(torch.equal(a, b) for a, b in zip(first, got))
->>>>>>> Stashed changes
