@@ -53,8 +53,8 @@ class MoEBlock(torch.nn.Module):
         """Serving: x bf16 [tokens, hidden], at most MOE_MAX_TOKENS tokens."""
         n, _, _ = mxg.layer_norm_fwd(x, self.norm.weight, self.norm.bias, self.norm.eps)
         w13_q, w13_s, fmt = self.fc1.quantized_weight()
-        w2_q, w2_s, _ = self.fc2.quantized_weight()
-        y, _, _ = mxg.moe_layer(n, n @ self.gate.t(), w13_q, w13_s, w2_q, w2_s, self.top_k, fmt=fmt)
+        w2_q, w2_s, w2_fmt = self.fc2.quantized_weight()   # its code layout goes by its own sizes
+        y, _, _ = mxg.moe_layer(n, n @ self.gate.t(), w13_q, w13_s, w2_q, w2_s, self.top_k, fmt=fmt, w2_fmt=w2_fmt)
         return x + y
 
     def gradients(self):

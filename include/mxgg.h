@@ -537,6 +537,11 @@ mxgg_status mxgg_clip_grads_with_norm(void* const* grads, const int64_t* numels,
 #define MXGG_MOE_MAX_TOP_K 16
 /* flags of mxgg_moe_layer */
 #define MXGG_MOE_RENORMALIZE 1u
+/* MX codes in 64-byte K blocks for one of the two matrices only (layers whose
+ * sizes differ in what divides them are quantized in different layouts); with
+ * MXGG_KBLOCK_ROWS in w_fmt both are */
+#define MXGG_MOE_W13_KBLOCK 4u
+#define MXGG_MOE_W2_KBLOCK 8u
 
 /*
  * A whole expert layer for a few tokens (decoding): routing, gate and up
@@ -555,8 +560,10 @@ mxgg_status mxgg_clip_grads_with_norm(void* const* grads, const int64_t* numels,
  *   w2_q/_s   [experts * hidden, inner] quantized along inner.
  *   w_fmt     MXGG_MXFP4 or MXGG_MXFP8 (hidden, inner multiples of 32; scales
  *             block-major), with MXGG_KBLOCK_ROWS for codes in 64-byte K
- *             blocks (multiples of 128); MXGG_FP8_128x128 / _P2 (multiples of
- *             128). As mxgg_quantize_rowwise writes them.
+ *             blocks (multiples of 128), or the flags above for those of one
+ *             matrix (W13_KBLOCK: hidden a multiple of 128, W2_KBLOCK: inner);
+ *             MXGG_FP8_128x128 / _P2 (multiples of 128). As
+ *             mxgg_quantize_rowwise writes them.
  *   out       bf16 [tokens, hidden], dense: out[t] = sum over the token's
  *             choices of weight * W2_e (silu(W1_e x[t]) * (W3_e x[t])); zeros
  *             when nothing was chosen. Products and sums fp32; the inner

@@ -11,7 +11,7 @@ from ._lib import (  # noqa: F401
     mxgg_grouped_dgrad, mxgg_grouped_fwd, mxgg_grouped_wgrad, mxgg_quantize_colwise_segpad, mxgg_quantize_dual,
     mxgg_mx_scale_stride, mxgg_mx_scales_relayout, mxgg_quantize_rowwise, mxgg_segpad_rows, mxgg_transpose_128x128,
     mxgg_workspace_size,
-    BF16, F32, MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_RENORMALIZE, NORM_L2, NORM_MAX,
+    BF16, F32, MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_RENORMALIZE, MOE_W13_KBLOCK, MOE_W2_KBLOCK, NORM_L2, NORM_MAX,
     mxgg_clip_grad_norm, mxgg_clip_grads_with_norm, mxgg_grad_norm, mxgg_layer_norm_bwd, mxgg_layer_norm_fwd,
     mxgg_moe_layer,
     clip_grad_norm, clip_grads_with_norm, grad_norm, layer_norm_bwd, layer_norm_fwd, moe_layer,

@@ -27,7 +27,7 @@ MAX_EXPERTS = 512
 # mxgg_dtype, mxgg_norm and the limits and flags of mxgg_moe_layer
 BF16, F32 = 0, 1
 NORM_L2, NORM_MAX = 0, 1
-MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_RENORMALIZE = 64, 16, 1
+MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_RENORMALIZE, MOE_W13_KBLOCK, MOE_W2_KBLOCK = 64, 16, 1, 4, 8
 # mxgg_scale_layout: OR-ed into an MX format to state the layout of its scales
 LAYOUT_BLOCK_MAJOR, LAYOUT_ROW_MAJOR, LAYOUT_MFMA, LAYOUT_MASK = 0x000, 0x100, 0x200, 0xF00
 # MX code layouts: row-wise / column-wise codes in 64-byte K blocks
@@ -652,15 +652,19 @@ def mxgg_clip_grads_with_norm(grads, max_norm, total):
 
 
 def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", renormalize=True, out=None, ids=None,
-                   weights=None, ws=None):
+                   weights=None, ws=None, w2_fmt=None):
     """The whole expert layer for at most 64 tokens. x: bf16 [tokens, hidden];
     logits: the gate's output, bf16 or fp32 [tokens, experts]; w13: [experts *
     2 * inner, hidden] (gate rows, then up rows of each expert) and w2: [experts
     * hidden, inner] as quantize_rowwise(..., fmt) writes them, fmt "mxfp4",
-    "mxfp8" (also | KBLOCK_ROWS) or "fp8_128x128" (_p2). Returns (out, ids,
+    "mxfp8" (also | KBLOCK_ROWS) or "fp8_128x128" (_p2); w2_fmt: w2's where its
+    code layout is another (with or without KBLOCK_ROWS). Returns (out, ids,
     weights): bf16 [tokens, hidden], int32 and fp32 [tokens, top_k]."""
     torch = _torch()
     f = _fmt(fmt)
+    f2 = f if w2_fmt is None else _fmt(w2_fmt)
+    if (f ^ f2) & ~KBLOCK_ROWS:
+        raise ValueError("w2_fmt may differ from fmt in the code layout only (KBLOCK_ROWS)")
     if (f & 0xFF) not in (MXFP4, MXFP8, FP8_128x128, FP8_128x128_P2):
         raise ValueError("fmt must be a weight format: mxfp4, mxfp8 or fp8_128x128(_p2)")
     _check_bf16_2d(x)
@@ -672,17 +676,20 @@ def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", reno
     inner = _q_rows(w13_q, f) // (2 * E) if E else 0
     _expect(w13_q, "w13_q", _q_shape(f, E * 2 * inner, H), torch.uint8)
     _expect(w13_s, "w13_s", _row_scale_shape(f, E * 2 * inner, H), _sdtype(f))
-    _expect(w2_q, "w2_q", _q_shape(f, E * H, inner), torch.uint8)
-    _expect(w2_s, "w2_s", _row_scale_shape(f, E * H, inner), _sdtype(f))
+    _expect(w2_q, "w2_q", _q_shape(f2, E * H, inner), torch.uint8)
+    _expect(w2_s, "w2_s", _row_scale_shape(f2, E * H, inner), _sdtype(f2))
+    flags = MOE_RENORMALIZE if renormalize else 0
+    if f != f2:
+        flags |= MOE_W13_KBLOCK if f & KBLOCK_ROWS else MOE_W2_KBLOCK
     out = x.new_empty((T, H)) if out is None else _expect(out, "out", (T, H), torch.bfloat16)
     ids = x.new_empty((T, top_k), dtype=_i32_t) if ids is None else _expect(ids, "ids", (T, top_k), _i32_t)
     weights = x.new_empty((T, top_k), dtype=_f32_t) if weights is None \
         else _expect(weights, "weights", (T, top_k), _f32_t)
     ws, ws_bytes = _ws(ws, int(lib.mxgg_moe_layer_workspace(T, E, top_k, inner)), x)
     _check(lib.mxgg_moe_layer(x.data_ptr(), x.stride(0) if T > 1 else H, logits.data_ptr(), ldl, ldt, T, H, inner, E,
-                              top_k, w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(), f,
-                              MOE_RENORMALIZE if renormalize else 0, out.data_ptr(), ids.data_ptr(),
-                              weights.data_ptr(), ws.data_ptr(), ws_bytes, _stream_of(x)))
+                              top_k, w13_q.data_ptr(), w13_s.data_ptr(), w2_q.data_ptr(), w2_s.data_ptr(),
+                              f & f2, flags, out.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(), ws_bytes,
+                              _stream_of(x)))
     return out, ids, weights
 
 

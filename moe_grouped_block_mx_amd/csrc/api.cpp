@@ -630,6 +630,7 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
                                     {w2_s, "w2_s"}, {out, "out"}, {ids, "ids"}, {weights, "weights"}, {ws, "ws"}}, &cus));
     const int f = base_format(format_bits((int)w_fmt));
     const bool kb = f == MXGG_FP8_128x128 || kblock_bits((int)w_fmt) != 0;
+    const bool kb13 = kb || (flags & MXGG_MOE_W13_KBLOCK) != 0, kb2 = kb || (flags & MXGG_MOE_W2_KBLOCK) != 0;
     uint8_t* at = static_cast<uint8_t*>(ws);
     MoeParams p{};
     p.x = static_cast<const uint16_t*>(x);
@@ -658,11 +659,11 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     p.rows = (int32_t)(tokens * top_k);
     const int64_t rows13 = experts * 2 * inner, rows2 = experts * hidden;
     const int per_byte = f == MXGG_MXFP4 ? 2 : 1;
-    p.q13_row = kb ? 64 : hidden / per_byte;
-    p.q13_piece = kb ? rows13 * 64 : 64;
+    p.q13_row = kb13 ? 64 : hidden / per_byte;
+    p.q13_piece = kb13 ? rows13 * 64 : 64;
     p.s13_block = mx_scale_stride(rows13);
-    p.q2_row = kb ? 64 : inner / per_byte;
-    p.q2_piece = kb ? rows2 * 64 : 64;
+    p.q2_row = kb2 ? 64 : inner / per_byte;
+    p.q2_piece = kb2 ? rows2 * 64 : 64;
     p.s2_block = mx_scale_stride(rows2);
     const MoeFormat mf = f == MXGG_MXFP4 ? kMoeFp4 : f == MXGG_MXFP8 ? kMoeFp8 : kMoeBlock;
     return hip_status(launch_moe_layer(p, mf, cus, stream),

@@ -155,11 +155,15 @@ inline Check validate_moe_layer(const void* x, int64_t ldx, const void* logits, 
   const int f = base_format(format_bits(w_fmt));
   if (f != MXGG_MXFP4 && f != MXGG_MXFP8 && f != MXGG_FP8_128x128)
     return fail(MXGG_ERR_FORMAT, "moe_layer takes MXFP4, MXFP8 or FP8_128x128 weights (got %lld)", w_fmt);
-  if (flags & ~(uint32_t)MXGG_MOE_RENORMALIZE) return fail(MXGG_ERR_FORMAT, "unknown flags 0x%llx", flags);
+  if (flags & ~(uint32_t)(MXGG_MOE_RENORMALIZE | MXGG_MOE_W13_KBLOCK | MXGG_MOE_W2_KBLOCK))
+    return fail(MXGG_ERR_FORMAT, "unknown flags 0x%llx", flags);
+  if (f == MXGG_FP8_128x128 && flags & (MXGG_MOE_W13_KBLOCK | MXGG_MOE_W2_KBLOCK))
+    return fail(MXGG_ERR_FORMAT, "the K-block flags are of MX formats (got %lld)", w_fmt);
   MXGG_TRY(validate_moe_dims(T, H, I, E, k));
-  const int unit = f == MXGG_FP8_128x128 || kblock_bits(w_fmt) ? 128 : 32;
-  if (H % unit || I % unit)
-    return fail(MXGG_ERR_SHAPE, "hidden=%lld and inner=%lld must be multiples of %lld", H, I, unit);
+  const bool all = f == MXGG_FP8_128x128 || kblock_bits(w_fmt);
+  const int unit_h = all || flags & MXGG_MOE_W13_KBLOCK ? 128 : 32, unit_i = all || flags & MXGG_MOE_W2_KBLOCK ? 128 : 32;
+  if (H % unit_h) return fail(MXGG_ERR_SHAPE, "hidden=%lld must be a multiple of %lld", H, unit_h);
+  if (I % unit_i) return fail(MXGG_ERR_SHAPE, "inner=%lld must be a multiple of %lld", I, unit_i);
   // 64 rows of x are addressed with 32-bit element offsets
   if (ldx < H || ldx >= ((int64_t)1 << 25)) return fail(MXGG_ERR_SHAPE, "ldx=%lld outside [hidden=%lld, 2^25)", ldx, H);
   if (ldx % 8) return fail(MXGG_ERR_ALIGN, "ldx=%lld not a multiple of 8 elements", ldx);

@@ -191,7 +191,9 @@ class GroupedLinear(torch.nn.Module):
     def quantized_weight(self):
         """(codes, scales, format) of the weight as the forward reads it, from
         the same cache (quantized again only when the weight changed): what the
-        serving form of the layer (mxgg_moe_layer) takes."""
+        serving form of the layer (mxgg_moe_layer) takes, as fmt of gate and up,
+        as w2_fmt of the down projection. The format's code layout goes by the
+        layer's sizes, so the two may differ in it."""
         (q, s), _ = self._cache.get(self.weight, self.recipe, self.num_experts, self.out_features, self.in_features)
         f = _formats(self.recipe, self.out_features, self.in_features)["fwd_w"]
         return q, s, L.FORMATS[f] if isinstance(f, str) else f

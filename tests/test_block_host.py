@@ -163,3 +163,27 @@ def test_scaling_by_a_norm_needs_one():
     for grads in ([torch.zeros(8)], []):
         with pytest.raises(ValueError, match="total"):
             mx.clip_grads_with_norm(grads, 1.0, None)
+
+
+def test_moe_code_layout_of_each_matrix():
+    w13, w2 = mx.MOE_W13_KBLOCK, mx.MOE_W2_KBLOCK
+    for fmt in (mx.MXFP4, mx.MXFP8):
+        assert moe(fmt=fmt, flags=1 | w13) == HIP and moe(fmt=fmt, flags=w2) == HIP and moe(fmt=fmt, flags=w13 | w2) == HIP
+        # 64-byte blocks need multiples of 128 along the matrix's own contraction only
+        assert moe(fmt=fmt, inner=96, flags=w13) == HIP and moe(fmt=fmt, inner=96, flags=w2) == SHAPE
+        assert moe(fmt=fmt, H=288, ldx=288, flags=w2) == HIP and moe(fmt=fmt, H=288, ldx=288, flags=w13) == SHAPE
+        assert moe(fmt=fmt | mx.KBLOCK_ROWS, flags=w2) == HIP
+        assert moe(fmt=fmt | mx.KBLOCK_ROWS, inner=96, flags=w13) == SHAPE
+    assert moe(fmt=mx.FP8_128x128, flags=w13) == FORMAT and moe(flags=16) == FORMAT
+    T, H, inner, E = 3, 128, 96, 4
+    u8 = torch.uint8
+    good = dict(x=torch.zeros(T, H, dtype=torch.bfloat16), logits=torch.zeros(T, E),
+                w13_q=torch.zeros(1, E * 2 * inner, 64, dtype=u8), w13_s=torch.zeros(H // 32, E * 2 * inner, dtype=u8),
+                w2_q=torch.zeros(E * H, inner // 2, dtype=u8), w2_s=torch.zeros(inner // 32, E * H, dtype=u8), top_k=2,
+                fmt=mx.MXFP4 | mx.KBLOCK_ROWS, w2_fmt="mxfp4")
+    with pytest.raises(ValueError, match="GPU"):           # the buffers fit their formats; host memory is refused
+        mx.moe_layer(**good)
+    for bad in (dict(w2_fmt=None), dict(w2_fmt=mx.MXFP4 | mx.KBLOCK_ROWS), dict(fmt="mxfp4"), dict(w2_fmt="mxfp8"),
+                dict(w2_fmt=mx.MXFP4 | mx.KBLOCK_COLS), dict(fmt="fp8_128x128", w2_fmt="fp8_128x128_p2")):
+        with pytest.raises(ValueError):
+            mx.moe_layer(**{**good, **bad})

@@ -109,3 +109,10 @@ def test_layer_norm_module_takes_broadcast_and_transposed_gradients():
     norm.bias.main_grad.zero_()
     norm(base.clone().requires_grad_()).sum().backward()  # dy: one element, expanded
     assert not norm.bias.main_grad.any() and norm.weight.main_grad.any()
+
+
+@pytest.mark.parametrize("inner,hidden", [(64, 256), (192, 256), (192, 320)])
+def test_block_whose_two_layers_have_different_code_layouts(inner, hidden):
+    # fc1 is in K blocks where 128 divides hidden, fc2 (inner inputs) in rows
+    history, off = example().main(["--steps", "2", "--inner", str(inner), "--hidden", str(hidden)])
+    assert all(np.isfinite(norm) for _, norm in history) and off < 0.1

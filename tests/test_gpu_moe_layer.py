@@ -358,3 +358,20 @@ def test_most_tokens_choices_and_experts(fmt):
     # the largest lists, and the most LDS that the second product asks for
     x, logits = tokens(64, 32, 512, 3)
     shared_layer(512, 32, 32, fmt, "rows").check(x, logits, 16)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "mxfp8"])
+@pytest.mark.parametrize("H,inner,layouts", [(256, 128, ("rows", "kblock")), (256, 96, ("kblock", "rows")),
+                                             (96, 256, ("rows", "kblock"))])
+@pytest.mark.parametrize("T", [2, 40])
+def test_code_layout_of_each_matrix(fmt, H, inner, layouts, T):
+    layer = Layer(5, H, inner, fmt, "rows", 7)
+    x, logits = tokens(T, H, 5, T)
+    want = layer.check(x, logits, 2)
+    f13, f2 = (mxg.FORMATS[fmt] | (mxg.KBLOCK_ROWS if l == "kblock" else 0) for l in layouts)
+    if f13 & mxg.KBLOCK_ROWS:
+        layer.w13_q, layer.w13_s, _ = weights(5, 2 * inner, H, fmt, "kblock", 8)
+    if f2 & mxg.KBLOCK_ROWS:
+        layer.w2_q, layer.w2_s, _ = weights(5, H, inner, fmt, "kblock", 9)
+    layer.fmt = f13
+    assert all(torch.equal(a, b) for a, b in zip(want, layer.run(x, logits, 2, w2_fmt=f2)))
