@@ -366,7 +366,7 @@ hipError_t bwd(const NormBwdParams& p, int& grid, hipStream_t st) {
   // 25. Where the registers would spill, none: 2048 x 16384 fp32 98 us, with one
   // 157; 4096 x 14000 bf16 92 and 101.
   constexpr int T = L == 16 ? 1024 : L < 512 ? 512 : L, G = T / L;
-  constexpr int AHEAD = L == 16 ? 1 : NV == 1 ? 4 : NV == 4 || L == 1024 ? 0 : 2;
+  constexpr int AHEAD = L == 16 ? 1 : NV == 1 ? 4 : NV == 4 ? 0 : 2;
   const int64_t need = (p.rows + G - 1) / G;
   grid = (int)(need < kBwdGroups ? need : kBwdGroups);
   layer_norm_bwd_kernel<E, W, L, NV, T, AHEAD><<<grid, T, 0, st>>>(p);
@@ -382,8 +382,9 @@ hipError_t fwd_any(const NormFwdParams& p, hipStream_t st) {
   if (chunks <= 256) return fwd<E, W, 128, 2>(p, st);
   if (chunks <= 512) return fwd<E, W, 256, 2>(p, st);
   if (chunks <= 1024) return fwd<E, W, 512, 2>(p, st);
-  if (chunks <= 2048) return fwd<E, W, 1024, 2>(p, st);
-  return fwd<E, W, 1024, Chunk<E>::N == 4 ? 4 : 2>(p, st);
+  if constexpr (Chunk<E>::N == 4)   // bf16 rows have 2048 chunks at most
+    if (chunks > 2048) return fwd<E, W, 1024, 4>(p, st);
+  return fwd<E, W, 1024, 2>(p, st);
 }
 
 template <class E, class W>
@@ -397,8 +398,9 @@ hipError_t bwd_any(const NormBwdParams& p, int& grid, hipStream_t st) {
   if (chunks <= 768) return bwd<E, W, 256, 3>(p, grid, st);
   if (chunks <= 1024) return bwd<E, W, 512, 2>(p, grid, st);
   if (chunks <= 1536) return bwd<E, W, 512, 3>(p, grid, st);
-  if (chunks <= 2048) return bwd<E, W, 512, 4>(p, grid, st);
-  return bwd<E, W, 1024, Chunk<E>::N == 4 ? 4 : 2>(p, grid, st);
+  if constexpr (Chunk<E>::N == 4)
+    if (chunks > 2048) return bwd<E, W, 1024, 4>(p, grid, st);
+  return bwd<E, W, 512, 4>(p, grid, st);
 }
 
 }  // namespace

@@ -115,30 +115,24 @@ __device__ __forceinline__ void route_token(const MoeParams& p, int t, int& id, 
   weight = id >= 0 ? e / total : 0.f;
 }
 
-// One workgroup routes all tokens (THREADS / 16 of them at a time) and lists
-// the segments (a chosen expert and at most p.segment of its tokens) and the
+// One workgroup routes all tokens (THREADS / 16 of them at most) and lists the
+// segments (a chosen expert and at most p.segment of its tokens) and the
 // (expert, token) rows.
 template <int PER, int THREADS>
 __global__ __launch_bounds__(THREADS) void moe_route_kernel(MoeParams p) {
-  constexpr int TOKENS = THREADS / 16, ROUNDS = THREADS == 1024 ? kMoeTokens / TOKENS : 1;
   __shared__ unsigned long long mask[kMaxExperts];   // an expert's tokens
   __shared__ int64_t first[kMaxExperts + 1], wave_tot[THREADS / 64];
   for (int e = threadIdx.x; e < p.experts; e += THREADS) mask[e] = 0;
   __syncthreads();
-  const int lane = threadIdx.x % 16;
-  int id[ROUNDS];
-  float weight[ROUNDS];
-#pragma unroll
-  for (int i = 0; i < ROUNDS; ++i) {
-    const int t = i * TOKENS + threadIdx.x / 16;
-    id[i] = -1;
-    if (t < p.tokens) {
-      route_token<PER>(p, t, id[i], weight[i]);
-      if (lane < p.top_k) {
-        p.ids[t * p.top_k + lane] = id[i];
-        p.weights[t * p.top_k + lane] = weight[i];
-        if (id[i] >= 0) atomicOr(&mask[id[i]], 1ull << t);
-      }
+  const int lane = threadIdx.x % 16, t = threadIdx.x / 16;
+  int id = -1;
+  float weight = 0.f;
+  if (t < p.tokens) {
+    route_token<PER>(p, t, id, weight);
+    if (lane < p.top_k) {
+      p.ids[t * p.top_k + lane] = id;
+      p.weights[t * p.top_k + lane] = weight;
+      if (id >= 0) atomicOr(&mask[id], 1ull << t);
     }
   }
   __syncthreads();
@@ -156,12 +150,7 @@ __global__ __launch_bounds__(THREADS) void moe_route_kernel(MoeParams p) {
     for (int left = __popcll(mask[e]); left > 0; left -= p.segment, base += p.segment)
       *at++ = MoeSegment{e, base, min(left, p.segment), 0};
   }
-#pragma unroll
-  for (int i = 0; i < ROUNDS; ++i) {
-    const int t = i * TOKENS + threadIdx.x / 16;
-    if (id[i] >= 0)
-      p.row_list[(int32_t)(first[id[i]] >> 32) + __popcll(mask[id[i]] & ((1ull << t) - 1))] = MoeRow{weight[i], t};
-  }
+  if (id >= 0) p.row_list[(int32_t)(first[id] >> 32) + __popcll(mask[id] & ((1ull << t) - 1))] = MoeRow{weight, t};
   if (threadIdx.x == 0) *p.count = (int32_t)first[p.experts];
 }
 
@@ -630,7 +619,7 @@ constexpr int kLdsBytes = 160 * 1024;
 template <int PER>
 void route_per(const MoeParams& p, hipStream_t st) {
   if (p.tokens <= 16) moe_route_kernel<PER, 256><<<1, 256, 0, st>>>(p);
-  else moe_route_kernel<PER, 1024><<<1, 1024, 0, st>>>(p);
+  else moe_route_kernel<PER, 16 * kMoeTokens><<<1, 16 * kMoeTokens, 0, st>>>(p);
 }
 
 hipError_t route(const MoeParams& p, hipStream_t st) {
