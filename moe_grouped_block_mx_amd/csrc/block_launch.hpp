@@ -167,6 +167,36 @@ inline void moe_plan(MoeParams& p, MoeFormat fmt) {
     p.splits = p.splits < 1 ? 1 : p.splits > 8 ? 8 : p.splits;
   }
 }
+
+// How a product's workgroup is cut: 16-row tiles that a wave holds (of W1, and as
+// many of W3), waves, and pieces in a wave's ring. What the rings leave of 160 KiB
+// holds the lists and sums. `xn`: the loads that bring a piece's tokens.
+struct MoeCut {
+  int tiles, waves, slots;
+};
+// First product: more tokens want more rows for each load of them (1 token of
+// 4096 x 1536: 28 us; with 32 rows of each a wave 30. 32 tokens: 78 us; with 16
+// rows 86).
+constexpr MoeCut moe_up_cut(int xn) { return xn == 1 ? MoeCut{1, 8, 5} : MoeCut{2, 4, xn == 2 ? 5 : 4}; }
+// Second product: the waves' sums (16 rt rows of all tokens in fp32) share the LDS;
+// `many`: of more than 32 tokens.
+constexpr MoeCut moe_down_cut(int rt, int xn, bool many) {
+  return rt == 4 ? MoeCut{4, 4, (xn == 1 ? 5 : 4) - (many ? 1 : 0)} : MoeCut{rt, 8, 4};
+}
+inline bool moe_down_many(const MoeParams& p) { return p.down_tiles == 4 && p.tokens > 32; }
+// A piece of rt tiles: 1 KiB of codes each, their scales, the tokens.
+constexpr int moe_stage_bytes(int rt, int xn) { return rt * 1024 + 256 + xn * 1024; }
+// LDS of the products' workgroups, of a planned call
+constexpr int kMoeLdsBytes = 160 * 1024;
+inline int moe_up_lds(const MoeParams& p) {
+  const MoeCut c = moe_up_cut(p.dmas);
+  return c.waves * (c.slots * moe_stage_bytes(2 * c.tiles, p.dmas) + 2 * c.tiles * 1024) + p.most_segments * 8 + p.rows;
+}
+inline int moe_down_lds(const MoeParams& p) {
+  const MoeCut c = moe_down_cut(p.down_tiles, p.dmas, moe_down_many(p));
+  return c.waves * (c.slots * moe_stage_bytes(c.tiles, p.dmas) + p.tokens * c.tiles * 64) + p.most_segments * 8 +
+         p.rows * 5;
+}
 hipError_t launch_moe_layer(MoeParams p, MoeFormat fmt, int num_cus, hipStream_t st);
 
 }  // namespace mxgg

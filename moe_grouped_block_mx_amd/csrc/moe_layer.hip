@@ -384,17 +384,6 @@ __device__ __forceinline__ int lists_to_lds(const MoeParams& p, int32_t* segment
   return count;
 }
 
-// How the first product is cut, by the token DMAs of a piece: tiles of W1 (and
-// W3) that a wave holds, waves, and pieces in a ring. What the rings leave of
-// 160 KiB holds the lists and sums. More tokens want more rows for each load
-// of them.
-// (1 token of 4096 x 1536: 28 us; with 32 rows of each a wave 30. 32 tokens: 78
-// us; with 16 rows 86.)
-template <int XN>
-struct UpCut {
-  static constexpr int TILES = XN == 1 ? 1 : 2, WAVES = XN == 1 ? 8 : 4, SLOTS = XN == 1 ? 5 : XN == 2 ? 5 : 4;
-};
-
 // h, 16 TILES inner columns of one segment at a time: W1's and W3's rows
 // against the segment's tokens. The grid stays: workgroup b takes units b, b +
 // grid, ..., and its waves share the pieces of each, in one stream that runs on
@@ -402,9 +391,10 @@ struct UpCut {
 // (the hardware deals workgroups out to the 8 in turn) share the lines of the
 // scales, 128 rows of one block each.
 template <MoeFormat F, int XN, bool TAIL>
-__global__ __launch_bounds__(64 * UpCut<XN>::WAVES) void moe_up_kernel(MoeParams p) {
-  constexpr int TILES = UpCut<XN>::TILES, WAVES = UpCut<XN>::WAVES, RT = 2 * TILES, THREADS = 64 * WAVES;
-  using R = Ring<F, RT, XN, UpCut<XN>::SLOTS, TAIL>;
+__global__ __launch_bounds__(64 * moe_up_cut(XN).waves) void moe_up_kernel(MoeParams p) {
+  constexpr MoeCut C = moe_up_cut(XN);
+  constexpr int TILES = C.tiles, WAVES = C.waves, RT = 2 * TILES, THREADS = 64 * WAVES;
+  using R = Ring<F, RT, XN, C.slots, TAIL>;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   v4f* sums = reinterpret_cast<v4f*>(lds + WAVES * R::BYTES);
   int32_t* segments = reinterpret_cast<int32_t*>(sums + WAVES * RT * 64);
@@ -487,15 +477,6 @@ __global__ __launch_bounds__(64 * UpCut<XN>::WAVES) void moe_up_kernel(MoeParams
   wait_loads<0>();
 }
 
-// How the second product is cut: 16-row tiles of W2 that a wave holds, waves,
-// and pieces in a ring, by the token DMAs of a piece; the waves' sums (16 RT
-// rows of all tokens in fp32) share the LDS.
-template <int RT, int XN, bool MANY>   // MANY: more than 32 tokens
-struct DownCut {
-  static constexpr int WAVES = RT == 4 ? 4 : 8;
-  static constexpr int SLOTS = RT == 4 ? (XN == 1 ? 5 : 4) - (MANY ? 1 : 0) : 4;
-};
-
 // The same for the second product: y for 16 RT output columns and all tokens.
 // A workgroup goes through all segments, or through one of p.splits parts of
 // them, so a token's sum over its experts stays here (no atomics, one order);
@@ -503,10 +484,10 @@ struct DownCut {
 // stream. When a segment is done, its columns go, weighted, into the wave's
 // sums in LDS.
 template <MoeFormat F, int RT, int XN, bool TAIL, bool MANY>
-__global__ __launch_bounds__(RT == 4 ? 256 : 512) void moe_down_kernel(MoeParams p) {
-  using C = DownCut<RT, XN, MANY>;
-  constexpr int WAVES = C::WAVES, THREADS = 64 * WAVES;
-  using R = Ring<F, RT, XN, C::SLOTS, TAIL>;
+__global__ __launch_bounds__(64 * moe_down_cut(RT, XN, MANY).waves) void moe_down_kernel(MoeParams p) {
+  constexpr MoeCut C = moe_down_cut(RT, XN, MANY);
+  constexpr int WAVES = C.waves, THREADS = 64 * WAVES;
+  using R = Ring<F, RT, XN, C.slots, TAIL>;
   constexpr int ROWS = RT * 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   // neighbouring tiles of 128 rows on one XCD, as above
@@ -614,8 +595,6 @@ __global__ __launch_bounds__(256) void moe_sum_kernel(MoeParams p) {
   *reinterpret_cast<uint2*>(p.out + at) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
 }
 
-constexpr int kLdsBytes = 160 * 1024;
-
 template <int PER>
 void route_per(const MoeParams& p, hipStream_t st) {
   if (p.tokens <= 16) moe_route_kernel<PER, 256><<<1, 256, 0, st>>>(p);
@@ -632,30 +611,30 @@ hipError_t route(const MoeParams& p, hipStream_t st) {
 
 template <MoeFormat F, int XN, bool TAIL>
 hipError_t up(const MoeParams& p, int num_cus, hipStream_t st) {
-  using C = UpCut<XN>;
-  using R = Ring<F, 2 * C::TILES, XN, C::SLOTS, TAIL>;
-  const int bytes = C::WAVES * (R::BYTES + 2 * C::TILES * 64 * (int)sizeof(v4f)) + p.most_segments * 8 + p.rows;
-  if (bytes > kLdsBytes) return hipErrorInvalidValue;
+  constexpr MoeCut C = moe_up_cut(XN);
+  static_assert(Ring<F, 2 * C.tiles, XN, C.slots, TAIL>::STAGE == moe_stage_bytes(2 * C.tiles, XN), "a piece in LDS");
+  const int bytes = moe_up_lds(p);
+  if (bytes > kMoeLdsBytes) return hipErrorInvalidValue;
   const hipError_t e =
-      ensure_dynamic_lds(reinterpret_cast<const void*>(&moe_up_kernel<F, XN, TAIL>), kLdsBytes, st);
+      ensure_dynamic_lds(reinterpret_cast<const void*>(&moe_up_kernel<F, XN, TAIL>), kMoeLdsBytes, st);
   if (e != hipSuccess) return e;
-  const int64_t units = (int64_t)p.most_segments * (p.inner / (16 * C::TILES));
+  const int64_t units = (int64_t)p.most_segments * (p.inner / (16 * C.tiles));
   const uint32_t grid = (uint32_t)((units < num_cus ? units : num_cus) + 7) / 8 * 8;
-  moe_up_kernel<F, XN, TAIL><<<grid, 64 * C::WAVES, bytes, st>>>(p);
+  moe_up_kernel<F, XN, TAIL><<<grid, 64 * C.waves, bytes, st>>>(p);
   return hipGetLastError();
 }
 
 template <MoeFormat F, int RT, int XN, bool TAIL, bool MANY>
 hipError_t down(const MoeParams& p, hipStream_t st) {
-  using C = DownCut<RT, XN, MANY>;
-  using R = Ring<F, RT, XN, C::SLOTS, TAIL>;
-  const int bytes = C::WAVES * (R::BYTES + p.tokens * RT * 64) + p.most_segments * 8 + p.rows * 5;
-  if (bytes > kLdsBytes) return hipErrorInvalidValue;
+  constexpr MoeCut C = moe_down_cut(RT, XN, MANY);
+  static_assert(Ring<F, RT, XN, C.slots, TAIL>::STAGE == moe_stage_bytes(RT, XN), "a piece in LDS");
+  const int bytes = moe_down_lds(p);
+  if (bytes > kMoeLdsBytes) return hipErrorInvalidValue;
   hipError_t e =
-      ensure_dynamic_lds(reinterpret_cast<const void*>(&moe_down_kernel<F, RT, XN, TAIL, MANY>), kLdsBytes, st);
+      ensure_dynamic_lds(reinterpret_cast<const void*>(&moe_down_kernel<F, RT, XN, TAIL, MANY>), kMoeLdsBytes, st);
   if (e != hipSuccess) return e;
   const uint32_t tiles = (uint32_t)((p.hidden + 1023) / 1024 * (1024 / (16 * RT)));   // whole 8 x 128-row rounds
-  moe_down_kernel<F, RT, XN, TAIL, MANY><<<dim3(tiles, (uint32_t)p.splits), 64 * C::WAVES, bytes, st>>>(p);
+  moe_down_kernel<F, RT, XN, TAIL, MANY><<<dim3(tiles, (uint32_t)p.splits), 64 * C.waves, bytes, st>>>(p);
   if ((e = hipGetLastError()) != hipSuccess || p.splits == 1) return e;
   moe_sum_kernel<<<(uint32_t)(((int64_t)p.tokens * p.hidden + 1023) / 1024), 256, 0, st>>>(p);
   return hipGetLastError();
@@ -665,7 +644,7 @@ template <MoeFormat F, int XN, bool TAIL>
 hipError_t down_tiles(const MoeParams& p, hipStream_t st) {
   if constexpr (XN < 3)
     if (p.down_tiles == 1) return down<F, 1, XN, TAIL, false>(p, st);
-  return p.tokens > 32 ? down<F, 4, XN, TAIL, true>(p, st) : down<F, 4, XN, TAIL, false>(p, st);
+  return moe_down_many(p) ? down<F, 4, XN, TAIL, true>(p, st) : down<F, 4, XN, TAIL, false>(p, st);
 }
 
 template <MoeFormat F, bool TAIL>
