@@ -139,17 +139,26 @@ enum MoeFormat { kMoeFp4 = 0, kMoeFp8 = 1, kMoeBlock = 2 };
 // Segments: one of few tokens leaves more of the LDS to weights in flight, one of
 // many reads an expert's weights less often (again out of the caches). So about
 // the tokens of a chosen expert and half as many more, for the spread of chance:
-// with just their mean the whole layer took 90 us instead of 78 (32 tokens, 32
-// experts of 4096 x 1536 in MXFP4) and 584 instead of 505 (64 tokens, 64 experts
+// with just their mean the whole layer took 91 us instead of 78 (32 tokens, 32
+// experts of 4096 x 1536 in MXFP4) and 583 instead of 506 (64 tokens, 64 experts
 // of 7168 x 2048, blockwise). With E2M1 codes a 1 KiB load brings 4 tokens'
 // piece, with E4M3 codes 8.
 //
 // Second product: a wave's 16 rows of weights cost as much in loads of tokens as
-// 64 do. With few tokens that is little, and 16-row tiles give every CU a
-// workgroup (1 token, 4096 outputs: 27.5 us, 64-row tiles 30.5). Otherwise the
-// tiles are 64 rows and the segments are split over workgroups, with the parts
-// added up after (8 tokens, 7168 outputs: 127 us, 16-row tiles 136; 64 tokens
-// there: 505 us, without the split 568; 32 tokens, 4096 outputs: 78 and 114).
+// 64 do. With few tokens that is little, and 16-row tiles give four times the
+// workgroups without a launch that adds parts up; hidden / 16 of them, so every CU
+// has one from 4096 outputs on, and narrower layers leave some idle. Otherwise the
+// tiles are 64 rows and the segments are split over workgroups, at most 8 parts,
+// added up after. Both sides, whole layer in us, 32 experts of 1536, top 8, MXFP4:
+//   outputs     1024         2048         4096         6144          7168
+//   tokens    16   64      16   64      16   64      16   64       16   64 rows
+//      1     20.7 22.1    22.8 25.2    26.8 30.3    37.0 36.9     41.3 41.5
+//      4     35.8 33.7    40.7 40.3    54.3 56.8    78.4 74.8     85.6 81.6
+//     16     41.2 36.4    54.2 47.2    74.3 71.3   112.9 98.4    124.2 109.6
+// The rule has the better side of one token and of the wide layers; at 16 tokens
+// below 6144 outputs the other would be 4 to 13 % faster. 8 tokens, 128 experts,
+// 7168 outputs: 128 us, 16-row tiles 136. The split itself: 64 tokens, blockwise, 7168
+// outputs 506 us, without it 570; 32 tokens, 4096 outputs 78 and 114.
 inline void moe_plan(MoeParams& p, MoeFormat fmt) {
   const int each = fmt == kMoeFp4 ? 4 : 8, most = fmt == kMoeFp4 ? 3 : 2;
   const int chosen = p.rows < p.experts ? p.rows : p.experts;
@@ -174,9 +183,10 @@ inline void moe_plan(MoeParams& p, MoeFormat fmt) {
 struct MoeCut {
   int tiles, waves, slots;
 };
-// First product: more tokens want more rows for each load of them (1 token of
-// 4096 x 1536: 28 us; with 32 rows of each a wave 30. 32 tokens: 78 us; with 16
-// rows 86).
+// First product: more tokens want more rows for each load of them (whole layer, 1
+// token of 4096 x 1536: 27 us; with 32 rows of each a wave 28; 8 tokens of 7168 x
+// 1024: 128 and 125. 32 tokens: 78 us; with 16 rows, and three pieces in a ring, 85;
+// 64 tokens of 7168 x 2048 blockwise 506 and 499).
 constexpr MoeCut moe_up_cut(int xn) { return xn == 1 ? MoeCut{1, 8, 5} : MoeCut{2, 4, xn == 2 ? 5 : 4}; }
 // Second product: the waves' sums (16 rt rows of all tokens in fp32) share the LDS;
 // `many`: of more than 32 tokens.

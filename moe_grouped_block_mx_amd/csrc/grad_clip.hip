@@ -13,9 +13,9 @@
 // A tensor is cut into chunks of 8192 elements, dealt out to the workgroups in
 // turn, so many small tensors cost what one of their size does; the scaling goes
 // backwards, onto what the norm pass left in the caches. 1.6 GB of fp32: 0.90 ms
-// (norm 0.28 to 0.32, 5.0 to 5.7 TB/s; scaling 0.57, 5.6 TB/s read and
-// written); 150 tensors of 30 million elements, bf16 and fp32: 18 + 32 us; 4
-// tensors of 300000 elements: 4 + 5 us, two launches.
+// (norm 0.28 to 0.32, 5.0 to 5.7 TB/s; scaling 0.58, 5.6 TB/s read and
+// written); 150 tensors of 30 million elements together, bf16 and fp32: 18 + 32 us;
+// 4 tensors of 300000 elements together: 4 + 5 us, two launches.
 #include "block_common.hpp"
 #include "block_launch.hpp"
 

@@ -10,11 +10,15 @@
 // mean of the same registers; the next row's chunks are on their way meanwhile.
 // All sums are fp32.
 //
-// Both passes are bound by memory. Forward, 16384 x 7168 bf16: 90 us, 5.2 TB/s (a
-// plain 2 GiB copy: 4.9). Backward, 4096 x 4096 bf16: 23 us, 4.4 TB/s, then 4 us
-// for the columns' partial sums (8 MB); 2500 x 5001 fp32: 37 us together, 4.1
-// TB/s; 16384 x 7168 bf16: 140 us, 5.0 TB/s. 8 x 4096 forward: 3.3 us, the time
-// of an empty launch and one trip to memory.
+// Both passes are bound by memory (all times in this file: medians of the
+// profiler's kernel times; they vary by some 4 % between runs). Forward, 16384 x
+// 7168 bf16: 94 us, 5.0 TB/s (a plain 2 GiB copy: 4.9). Backward, 4096 x 4096 bf16:
+// 24.5 us, 4.1 TB/s, then 4 us for the columns' partial sums (8 MB); 2500 x 5001
+// fp32: 30 + 4 us, 4.4 TB/s; 16384 x 7168 bf16: 136 + 5 us, 5.0 TB/s. Narrow rows
+// are not: 65536 x 96 bf16 backward takes 14 + 4 us where its bytes take 8. None is
+// moved twice (26 MB read, 13 written), but a CU has two loads of 12 lanes for each
+// of its 64 rows in flight (25 KB), and waits for such a step four times. 8 x 4096
+// forward: 3.4 us, the time of an empty launch and one trip to memory.
 #include "block_common.hpp"
 #include "block_launch.hpp"
 
@@ -339,14 +343,15 @@ __global__ __launch_bounds__(kThreads) void layer_norm_grad_kernel(const float* 
 
 // Lanes of a row: two chunks each where the row has them, since a wave then has
 // twice the bytes in flight for the same barriers (forward, 16384 rows of bf16:
-// 2048 columns 29 us with two chunks a lane, 31 with one; 4096 columns 52 and
-// 62; 7168 columns 93, with one 122, with four 107).
+// 2048 columns 25.6 us with two chunks a lane, 30.7 with one; 4096 columns 48.5 and
+// 60.4; 7168 columns 90.9, with one 121, with four 95.8).
 //
 // The forward's grid goes up to 2^20 threads, eight 512-thread workgroups for
-// each CU's two: enough rows in a workgroup to keep the weights, and a grid that
-// still evens out (16384 x 7168: 93 us; one row a workgroup 96; a grid that just
-// fills the card 106). The backward has one workgroup a CU, because each writes
-// a partial of both gradients (4096 x 4096: 27 us; two a CU 37).
+// each CU's two: a grid that still evens out (16384 x 7168: 90.9 us; one that just
+// fills the card 98.7), and rows enough in a workgroup that the weights are not
+// loaded for each (one row a workgroup: 90.6, the same). The backward has one
+// workgroup a CU, because each writes a partial of both gradients (4096 x 4096, both
+// launches: 28.8 us; two a CU 37.0).
 constexpr int kFwdThreads = 1 << 20, kBwdGroups = 256;
 
 template <class E, class W, int L, int NV>
@@ -360,11 +365,13 @@ hipError_t fwd(const NormFwdParams& p, hipStream_t st) {
 template <class E, class W, int L, int NV>
 hipError_t bwd(const NormBwdParams& p, int& grid, hipStream_t st) {
   // 512 threads leave a thread the registers for the column sums and the rows
-  // on their way; rows of 16 lanes need few (65536 x 96: 16 us with 1024
-  // threads, 19 with 512). Two rows ahead rather than one: 16384 x 7168 bf16 140
-  // us and 159 (three: 141); with one chunk a lane four: 32768 x 500 24 us and
-  // 25. Where the registers would spill, none: 2048 x 16384 fp32 98 us, with one
-  // 157; 4096 x 14000 bf16 92 and 101.
+  // on their way; rows of 16 lanes need few (65536 x 96, both launches: 18.0 us with
+  // 1024 threads, 20.6 with 512; two rows ahead there 19.5). Two rows ahead rather
+  // than one: 16384 x 7168 bf16 140 us and 158 (three: 141); 4096 x 4096 28.8 and
+  // 31.6. With one chunk a lane four (32768 x 500: 25.4 us; two 24.7, one 32.5).
+  // Where the registers would spill, none: 2048 x 16384 fp32 98 us, with one 147;
+  // 4096 x 14000 bf16 91 and 100. (fp32 rows of 1024 lanes have 128 registers a
+  // thread and spill 3 or 4 of them all the same; no other form spills.)
   constexpr int T = L == 16 ? 1024 : L < 512 ? 512 : L, G = T / L;
   constexpr int AHEAD = L == 16 ? 1 : NV == 1 ? 4 : NV == 4 ? 0 : 2;
   const int64_t need = (p.rows + G - 1) / G;

@@ -12,13 +12,15 @@
 // takes 16 weight rows against 16 tokens.
 //
 // Three launches (four where the second product is split): the routing takes 4
-// to 7 us, the products what their weights take to read. 64 tokens, 64 experts of
-// 7168 x 2048, blockwise FP8 (2.8 GB): 505 us, 5.6 TB/s, where reading alone
-// reaches 5.7; 8 tokens, 128 experts of 7168 x 1024, MXFP4 (0.6 GB): 128 us, 4.7
-// TB/s; 32 tokens, 32 experts of 4096 x 1536, MXFP4 (0.32 GB): 78 us, 4.1 TB/s.
-// One token there (80 MB) takes 27.5 us, of which some 13 are three launches
+// to 7 us, the products what their weights take to read (times of a whole layer:
+// medians of replays from a graph, weights of three layers in turn). 64 tokens, 64
+// experts of 7168 x 2048, blockwise FP8 (2.8 GB): 506 us, 5.6 TB/s, where reading
+// alone reaches 5.7; 8 tokens, 128 experts of 7168 x 1024, MXFP4 (0.6 GB): 128 us,
+// 4.7 TB/s; 32 tokens, 32 experts of 4096 x 1536, MXFP4 (0.32 GB): 78 us, 4.1 TB/s.
+// One token there (80 MB) takes 27 us, of which some 13 are three launches
 // and the rings' filling. Routing inside the first product's workgroups took 5 us
-// there, more than its launch.
+// there, more than its launch. Where an expert has more tokens than a segment, its
+// weights are read again for each: 64 tokens there read 0.62 GB for 0.32, 120 us.
 //
 // How a lane reads: 64 bytes of each of 16 rows are one piece; lane l owns
 // bytes 16 (l/16) .. +15 of row l%16, whatever the layout (rows of codes or
@@ -468,7 +470,10 @@ __global__ __launch_bounds__(64 * moe_up_cut(XN).waves) void moe_up_kernel(MoePa
 #pragma unroll
         for (int k = 0; k < 4; ++k) h[k] = a[k] / (1.f + expf(-a[k])) * u[k];
         // bf16, as between the two grouped products of a training step: the
-        // second product reads it as its MFMA operand
+        // second product reads it as its MFMA operand. It leaves the output 2.3e-3
+        // off its 64-bit value (in norm), where rounding the output alone leaves
+        // 1.65e-3; the rest of h in a second bf16 would double that product's token
+        // loads and halve the tokens of a segment.
         uint16_t* to = p.inner_x + inner_at<F>(segments[2 * seg + 1] + col, tile * 16 + g * 4, p.rows);
         *reinterpret_cast<uint2*>(to) = uint2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
       }
