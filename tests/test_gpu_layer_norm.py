@@ -263,6 +263,7 @@ def test_rows_whose_mean_over_their_deviation_passes_fp32(rows, cols, dtype):
     assert (mean == 2.0 ** 123).all() and not (mean * rstd).isfinite().any()
     check_bwd(dy, x, None, mean, rstd, mxg.layer_norm_bwd(dy, x, None, mean, rstd))
 
+
 # Rows enough that a workgroup goes through several (three trips or more, the
 # last one with some workgroups or row groups idle), for every number of lanes to
 # a row and of row loads ahead: what a trip leaves for the next is compared with
