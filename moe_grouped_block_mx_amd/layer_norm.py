@@ -16,10 +16,11 @@ from . import _lib as L
 
 def _rows(t):
     """[..., C] as rows with unit inner stride; a copy only where the kernels
-    could not read it (a broadcast or transposed gradient, say)."""
+    could not read it (a broadcast or transposed gradient, a row stride of 2^31
+    or more)."""
     rows = t.reshape(-1, t.shape[-1])
     n, cols = rows.shape
-    if (cols > 1 and rows.stride(1) != 1) or (n > 1 and rows.stride(0) < cols):
+    if (cols > 1 and rows.stride(1) != 1) or (n > 1 and not cols <= rows.stride(0) < 1 << 31):
         rows = rows.contiguous()
     return rows
 

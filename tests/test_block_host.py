@@ -187,3 +187,17 @@ def test_moe_code_layout_of_each_matrix():
                 dict(w2_fmt=mx.MXFP4 | mx.KBLOCK_COLS), dict(fmt="fp8_128x128", w2_fmt="fp8_128x128_p2")):
         with pytest.raises(ValueError):
             mx.moe_layer(**{**good, **bad})
+
+
+def test_rows_that_the_kernels_cannot_read_are_copied():
+    # the layer norm module takes any strides; the C ABI row strides from the row
+    # length up, below 2^31 (a time step out of a long batch has more)
+    from moe_grouped_block_mx_amd.layer_norm import _rows
+    big = torch.empty((3, 1 << 19, 4096), dtype=torch.bfloat16, device="meta")
+    for x, copied in ((big[:, 7], True), (big[:, :2, :], True), (big[:, 7, :100][:1], False), (big[1, :5], False),
+                      (big[0, :4, :6].t(), True), (big[0, :1, :6].expand(3, 6), True), (big[0, 5], False)):
+        r = _rows(x)
+        assert r.shape == (x.numel() // x.shape[-1], x.shape[-1])
+        if r.shape[0] > 1:
+            assert r.stride(1) == 1 and r.shape[1] <= r.stride(0) < 1 << 31
+        assert r.is_contiguous() == copied or not copied
