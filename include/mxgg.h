@@ -64,6 +64,11 @@
  *                     mixing a _P2 format with a general one selects the
  *                     general path; the input and weight gradients take one
  *                     format for both operands, where _P2 asserts both.
+ *   MXGG_INT8         signed 8-bit integers, one fp32 scale per row (of an
+ *                     activation: per token; of a weight: per output channel).
+ *                     Codes i8 [rows, cols], scales f32 [rows]; no layout bits.
+ *                     Taken by mxgg_quantize_rowwise and, for both operands
+ *                     together, by mxgg_grouped_fwd.
  *
  * MX quantization rule (what mxgg_quantize_* produce): amax = max |x| over the
  * block; e = clamp(floor(log2 amax) - emax, -127, 127) with emax = 2 (E2M1) or
@@ -72,7 +77,10 @@
  * = e + 127. Blockwise FP8 with MXGG_POW2_SCALES: amax floored at fp32(1e-4),
  * s = 2^-t with t the largest integer such that amax * 2^t <= 448, codes =
  * RNE-saturating E4M3 of x * 2^t; without the flag: q = fp32(448/amax),
- * codes from fp32(x*q), s = fp32(1/q).
+ * codes from fp32(x*q), s = fp32(1/q). MXGG_INT8: s = fp32(amax / 127), code =
+ * the integer nearest 127 x / amax (the quotient itself, ties to even), all
+ * zero where amax is 0; a row with NaN or infinity has zero codes and its amax
+ * for a scale, so what is multiplied by it is NaN.
  *
  * Conventions shared by every entry point:
  *   - Every pointer argument except m_splits is a DEVICE pointer on the device
@@ -127,7 +135,8 @@ typedef enum mxgg_format {
   MXGG_FP8_1x128 = 2,
   MXGG_FP8_128x128 = 3,
   MXGG_FP8_1x128_P2 = 4,
-  MXGG_FP8_128x128_P2 = 5
+  MXGG_FP8_128x128_P2 = 5,
+  MXGG_INT8 = 6
 } mxgg_format;
 
 /*
@@ -235,13 +244,14 @@ mxgg_status mxgg_mx_scales_relayout(const void* src, mxgg_scale_layout src_layou
  *           optionally | MXGG_LAYOUT_MFMA (cols % 128 == 0).
  *           MXGG_FP8_1x128: blocks of 128 along cols (cols % 128 == 0).
  *           MXGG_FP8_128x128: 128x128 blocks (rows % 128 == 0, cols % 128 == 0).
+ *           MXGG_INT8: whole rows (cols % 16 == 0, cols < 2^17).
  *   flags   MXGG_POW2_SCALES for the blockwise formats (ignored for MX).
  *   q       MXFP4: u8 [rows, cols/2]; MXFP8: u8 [rows, cols]; blockwise: E4M3
  *           codes u8 [cols/64, rows, 64] (64-byte blocks along cols).
  *   scales  MX: u8 [cols/32, R4] (block-major, R4 = mxgg_mx_scale_stride(rows)),
  *           or with MXGG_LAYOUT_MFMA u8 [cols/128, R32/32, 64, 2];
  *           FP8_1x128: f32 [cols/128, rows] (block-major);
- *           FP8_128x128: f32 [rows/128, cols/128].
+ *           FP8_128x128: f32 [rows/128, cols/128]; INT8: f32 [rows].
  * rows == 0 returns MXGG_OK with no launch. Errors: NULL, SHAPE, FORMAT,
  * ALIGN, DEVICE, ARCH, HIP.
  */
@@ -341,11 +351,15 @@ mxgg_status mxgg_transpose_128x128(const void* w_q, const void* w_s, int32_t G, 
  *             64, 2] (K % 128 == 0); or MXGG_FP8_128x128: u8 [K/64, G*N, 64]
  *             + f32 [G*N/128, K/128] (G*N < 2^25).
  *   format pairs (a_fmt, w_fmt): (MXFP4, MXFP4) a4w4, (MXFP8, MXFP4) a8w4,
- *             (FP8_1x128, FP8_128x128) blockwise FP8. a_fmt takes no layout
- *             bits other than block-major.
+ *             (FP8_1x128, FP8_128x128) blockwise FP8, (INT8, INT8). a_fmt takes
+ *             no layout bits other than block-major.
+ *             INT8: a_q i8 [M, K] + f32 [M], w_q i8 [G*N, K] + f32 [G*N]; the
+ *             sum over k is exact (32-bit integers), then
+ *             out = bf16(fp32(sum) * a_s[r] * w_s[g*N + n]).
  *   m_splits  host int64 [G]; sum == M.
  *   M, N, K   K % 32 == 0 and N % 32 == 0 (MX); K % 128 == 0 and N % 128 == 0
- *             (blockwise); M < 2^31; N, K < 2^23.
+ *             (blockwise); M < 2^31; N, K < 2^23. INT8: K % 16 == 0, K < 2^17,
+ *             any N < 2^23.
  *   out       bf16 [M, N] (dense), written with round-to-nearest-even.
  *   ws        workspace of at least mxgg_workspace_size(G) bytes (may be NULL
  *             when that is 0).
@@ -584,6 +598,110 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
                            size_t ws_bytes, hipStream_t stream);
 /* 0 for sizes that the call refuses. */
 size_t mxgg_moe_layer_workspace(int64_t tokens, int64_t experts, int64_t top_k, int64_t inner);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Tokens to their experts and back, around the grouped GEMMs. A choice (t, j) is
+ * the j-th expert of token t; its number is t * top_k + j. Pointers are
+ * element-aligned and leading dimensions any number of elements from the row
+ * length up.
+ * ---------------------------------------------------------------------------
+ */
+
+/* integer types of a router's choices */
+typedef enum mxgg_itype { MXGG_I32 = 0, MXGG_I64 = 1 } mxgg_itype;
+
+/*
+ * The choices in the order of their experts, those of one expert in rising
+ * order of their numbers (stable). A choice outside [0, experts) (-1 from
+ * mxgg_moe_layer, an expert that lives elsewhere) is dropped: it goes behind all
+ * others.
+ *   ids      [tokens, top_k] of `itype`, leading dimension ldi; the same expert
+ *            may come up twice.
+ *   rows     int32 [tokens, top_k], written: the place of each choice, ~place
+ *            (which is negative) of a dropped one.
+ *   choices  int32 [tokens * top_k], written: the choice at each place (its
+ *            token is choice / top_k).
+ *   counts   int32 [experts], written: the rows of each expert, whose sum is
+ *            the number of choices that were not dropped (on the host they are
+ *            the m_splits of the grouped GEMMs).
+ *   ws       mxgg_moe_sort_workspace(...) bytes, 16-byte aligned (NULL when 0).
+ * tokens >= 0, tokens * top_k < 2^31, top_k in [1, 16], experts in [1, 512].
+ * tokens == 0 clears the counts. Errors: NULL, SHAPE, FORMAT, ALIGN, WORKSPACE,
+ * DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_moe_sort(const void* ids, mxgg_itype itype, int64_t ldi, int64_t tokens, int64_t top_k,
+                          int64_t experts, int32_t* rows, int32_t* choices, int32_t* counts, void* ws,
+                          size_t ws_bytes, hipStream_t stream);
+/* 0 for sizes that the call refuses, and where none is needed. */
+size_t mxgg_moe_sort_workspace(int64_t tokens, int64_t top_k, int64_t experts);
+
+/*
+ * Tokens' rows to the places of their choices: out[rows[t, j]] = x[t], and zeros
+ * at the place of a dropped choice.
+ *   x     [tokens, cols] of `dtype`, leading dimension ldx.
+ *   rows  int32 [tokens, top_k], as mxgg_moe_sort writes it: no place twice.
+ *   out   [expert_rows, cols] of `dtype`, leading dimension ldo. Places from
+ *         expert_rows on are left out (with expert_rows the sum of the counts,
+ *         just the dropped ones), rows that no place names stay as they were.
+ * Its gradient is mxgg_moe_combine without weights. cols in [1, 2^24].
+ * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_moe_dispatch(const void* x, int64_t ldx, mxgg_dtype dtype, int64_t tokens, int64_t cols,
+                              const int32_t* rows, int64_t top_k, void* out, int64_t ldo, int64_t expert_rows,
+                              hipStream_t stream);
+
+/*
+ * Experts' rows back to their tokens: out[t] = sum_j weights[t, j] y[rows[t, j]]
+ * over the choices of t that are not dropped, in fp32, j rising, rounded once;
+ * zeros where all are. What lies at a dropped choice's place does not matter.
+ *   y        [expert_rows, cols] of `dtype`, leading dimension ldy. A place from
+ *            expert_rows on counts as dropped.
+ *   weights  fp32 [tokens, top_k] or NULL (1).
+ *   out      [tokens, cols] of `dtype`, leading dimension ldo; not y.
+ * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_moe_combine(const void* y, int64_t ldy, mxgg_dtype dtype, int64_t expert_rows, int64_t cols,
+                             const int32_t* rows, const float* weights, int64_t tokens, int64_t top_k, void* out,
+                             int64_t ldo, hipStream_t stream);
+
+/*
+ * The gradients of mxgg_moe_combine with weights:
+ *   dy[rows[t, j]] = weights[t, j] dout[t], zeros at the place of a dropped choice
+ *   dweights[t, j] = sum_c dout[t, c] y[rows[t, j], c] in fp32 (one fixed order),
+ *                    0 for a dropped choice
+ *   dy       [expert_rows, cols] of `dtype`, leading dimension lddy; may be y.
+ *            Rows that no place names stay as they were.
+ * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_moe_combine_bwd(const void* dout, int64_t lddo, const void* y, int64_t ldy, mxgg_dtype dtype,
+                                 int64_t expert_rows, int64_t cols, const int32_t* rows, const float* weights,
+                                 int64_t tokens, int64_t top_k, void* dy, int64_t lddy, float* dweights,
+                                 hipStream_t stream);
+
+/*
+ * Dropout with a mask that is never stored, and a residual:
+ *   out = residual + (kept ? x / (1 - p') : 0)
+ * with p' = p rounded to a multiple of 2^-16. A dropped x is not looked at (NaN
+ * and infinity do not pass). Without a residual the same call on the gradient of
+ * out is the gradient of x.
+ *   Element (r, c) is dropped when the 16-bit number below is less than p' 2^16.
+ *   With ng = ceil(cols / 8) and b = r * ng + c / 8, the four 32-bit words are
+ *   Philox4x32-10 of the counter (b mod 2^32, b / 2^32, call, step mod 2^32)
+ *   under the key (seed mod 2^32, seed / 2^32), the seed taken as unsigned; the
+ *   number is the half (c % 2) of word (c % 8) / 2, the low half first.
+ *   x, residual, out  [rows, cols] of `dtype`, leading dimensions ldx, ldr, ldo;
+ *            residual may be NULL (0); out may be x or residual.
+ *   p        in [0, 1]; 1: all dropped.
+ *   state    int64 [2] on the device: seed and step, read on `stream` (so a
+ *            captured call draws new numbers when the step was advanced before a
+ *            replay).
+ *   call     tells apart the calls of one step.
+ * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
+ */
+mxgg_status mxgg_dropout(const void* x, int64_t ldx, mxgg_dtype dtype, int64_t rows, int64_t cols, float p,
+                         const int64_t* state, uint32_t call, const void* residual, int64_t ldr, void* out,
+                         int64_t ldo, hipStream_t stream);
 
 /* Static text for a status code. */
 const char* mxgg_status_string(mxgg_status status);

@@ -19,13 +19,14 @@ LIB_PATH = os.path.join(PKG, "libmxgg.so")
 HEADER = os.path.join(ROOT, "include", "mxgg.h")
 
 # mxgg_format
-MXFP4, MXFP8, FP8_1x128, FP8_128x128, FP8_1x128_P2, FP8_128x128_P2 = 0, 1, 2, 3, 4, 5
+MXFP4, MXFP8, FP8_1x128, FP8_128x128, FP8_1x128_P2, FP8_128x128_P2, INT8 = 0, 1, 2, 3, 4, 5, 6
 FORMATS = {"mxfp4": MXFP4, "mxfp8": MXFP8, "fp8_1x128": FP8_1x128, "fp8_128x128": FP8_128x128,
-           "fp8_1x128_p2": FP8_1x128_P2, "fp8_128x128_p2": FP8_128x128_P2}
+           "fp8_1x128_p2": FP8_1x128_P2, "fp8_128x128_p2": FP8_128x128_P2, "int8": INT8}
 POW2_SCALES = 1
 MAX_EXPERTS = 512
 # mxgg_dtype, mxgg_norm and the limits and flags of mxgg_moe_layer
 BF16, F32 = 0, 1
+I32, I64 = 0, 1   # mxgg_itype
 NORM_L2, NORM_MAX = 0, 1
 MOE_MAX_TOKENS, MOE_MAX_TOP_K, MOE_RENORMALIZE, MOE_W13_KBLOCK, MOE_W2_KBLOCK = 64, 16, 1, 4, 8
 # mxgg_scale_layout: OR-ed into an MX format to state the layout of its scales
@@ -69,12 +70,18 @@ _SIGS = {
     "mxgg_clip_grads_with_norm": [_vpp, _i64p, _i32p, _i64, _f32, _vp, _vp],
     "mxgg_moe_layer": [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _i32, _u32, _vp,
                        _vp, _vp, _vp, _sz, _vp],
+    "mxgg_moe_sort": [_vp, _i32, _i64, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp],
+    "mxgg_moe_dispatch": [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp],
+    "mxgg_moe_combine": [_vp, _i64, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp],
+    "mxgg_moe_combine_bwd": [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _vp, _vp],
+    "mxgg_dropout": [_vp, _i64, _i32, _i64, _i64, _f32, _vp, _u32, _vp, _i64, _vp, _i64, _vp],
 }
 # functions that return a size
 _SIZES = {
     "mxgg_layer_norm_bwd_workspace": [_i64, _i64],
     "mxgg_grad_norm_workspace": [_i64],
     "mxgg_moe_layer_workspace": [_i64, _i64, _i64, _i64],
+    "mxgg_moe_sort_workspace": [_i64, _i64, _i64],
 }
 
 
@@ -208,7 +215,9 @@ def _code_bytes(f, n):
 def _q_shape(f, rows, cols):
     """Codes of a [rows, cols] operand quantized along cols: rows of codes,
     or 64-byte blocks along cols, u8 [bytes per row / 64, rows, 64]
-    (blockwise formats always, MX with KBLOCK_ROWS)."""
+    (blockwise formats always, MX with KBLOCK_ROWS; int8 never)."""
+    if (f & 0xFF) == INT8:
+        return (rows, cols)
     if not _is_mx(f) or (f & KBLOCK_ROWS):
         return (_code_bytes(f, cols) // 64, rows, 64)
     return (rows, _code_bytes(f, cols))
@@ -217,7 +226,7 @@ def _q_shape(f, rows, cols):
 def _q_rows(q, f):
     """Row count of a code tensor laid out as _q_shape gives it (a tensor of
     another rank then fails the shape check that follows)."""
-    if _is_mx(f) and not (f & KBLOCK_ROWS):
+    if (_is_mx(f) and not (f & KBLOCK_ROWS)) or (f & 0xFF) == INT8:
         return q.shape[0] if q.dim() >= 1 else 0
     return q.shape[1] if q.dim() >= 2 else 0
 
@@ -233,7 +242,9 @@ def _col_q_shape(f, cols, mpad):
 def _row_scale_shape(f, rows, cols):
     """Scales of a [rows, cols] operand quantized along cols (row-major scales
     when the format says so: the library refuses them, never misreads them).
-    1x128 fp32 scales are block-major [cols/128, rows]."""
+    1x128 fp32 scales are block-major [cols/128, rows], int8 ones [rows]."""
+    if (f & 0xFF) == INT8:
+        return (rows,)
     if _is_mx(f):
         return _layout_shape(f & LAYOUT_MASK, rows, cols // 32)
     if (f & 0xFF) in (FP8_1x128, FP8_1x128_P2):
@@ -252,6 +263,11 @@ def _col_scale_shape(f, cols, mpad):
 def _sdtype(f):
     torch = _torch()
     return torch.uint8 if _is_mx(f) else torch.float32
+
+
+def _qdtype(f):
+    torch = _torch()
+    return torch.int8 if (f & 0xFF) == INT8 else torch.uint8
 
 
 def mxgg_workspace_size(G: int) -> int:
@@ -296,18 +312,20 @@ def mxgg_mx_scale_stride(rows):
 
 def mxgg_quantize_rowwise(x, fmt="mxfp4", flags=None, q=None, scales=None):
     """x: bf16 [rows, cols] (row stride may exceed cols). Returns (q, scales).
-    flags: None = default (MXGG_POW2_SCALES for the blockwise formats)."""
+    flags: None = default (MXGG_POW2_SCALES for the blockwise formats).
+    "int8": codes int8 [rows, cols], one scale a row (a token, or a weight's
+    channel)."""
     torch = _torch()
     f = _fmt(fmt)
     flags = _flags(flags, f)
     rows, cols = x.shape
     _check_bf16_2d(x)
     if q is None:
-        q = torch.empty(_q_shape(f, rows, cols), dtype=torch.uint8, device=x.device)
+        q = torch.empty(_q_shape(f, rows, cols), dtype=_qdtype(f), device=x.device)
     if scales is None:
         # MX: block-major, block stride = rows rounded up to a multiple of 4
         scales = torch.empty(_row_scale_shape(f, rows, cols), dtype=_sdtype(f), device=x.device)
-    _expect(q, "q", _q_shape(f, rows, cols), torch.uint8)
+    _expect(q, "q", _q_shape(f, rows, cols), _qdtype(f))
     _expect(scales, "scales", _row_scale_shape(f, rows, cols), _sdtype(f))
     _check(lib.mxgg_quantize_rowwise(_ptr(x), rows, cols, _ld(x), f, flags, _ptr(q), _ptr(scales),
                                      _stream(x)))
@@ -374,9 +392,9 @@ def mxgg_grouped_fwd(a_q, a_s, w_q, w_s, m_splits, N, K, a_fmt="mxfp4", w_fmt="m
     arr, G = _splits(m_splits)
     af, wf = _fmt(a_fmt), _fmt(w_fmt)
     M = _q_rows(a_q, af)
-    _expect(a_q, "a_q", _q_shape(af, M, K), torch.uint8)
+    _expect(a_q, "a_q", _q_shape(af, M, K), _qdtype(af))
     _expect(a_s, "a_s", _row_scale_shape(af, M, K), _sdtype(af))
-    _expect(w_q, "w_q", _q_shape(wf, G * N, K), torch.uint8)
+    _expect(w_q, "w_q", _q_shape(wf, G * N, K), _qdtype(wf))
     _expect(w_s, "w_s", _row_scale_shape(wf, G * N, K), _sdtype(wf))
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a_q.device)
@@ -693,6 +711,128 @@ def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", reno
     return out, ids, weights
 
 
+def _rows_index(rows):
+    """(tokens, top_k) of the places that moe_sort writes."""
+    if rows.dim() != 2 or rows.dtype is not _i32_t or not rows.is_contiguous():
+        raise ValueError(f"rows must be a contiguous int32 tensor [tokens, top_k], got "
+                         f"{str(rows.dtype).replace('torch.', '')} {tuple(rows.shape)}")
+    return rows.shape
+
+
+def _like_rows(t, name, n, x):
+    """[n, cols] beside x, the caller's or a new one, and its leading dimension."""
+    cols = x.shape[1]
+    if t is None:
+        return x.new_empty((n, cols)), cols
+    if t.dim() != 2 or (n is not None and t.shape[0] != n) or t.shape[1] != cols or t.dtype is not x.dtype:
+        raise ValueError(f"{name} must be a {str(x.dtype).replace('torch.', '')} tensor [{'rows' if n is None else n}, "
+                         f"{cols}], got {str(t.dtype).replace('torch.', '')} {tuple(t.shape)}")
+    return t, _rows2d(_on(t, x, name), name)
+
+
+def mxgg_moe_sort(ids, experts, rows=None, choices=None, counts=None, ws=None):
+    """A router's choices in the order of their experts (stable). ids: int32 or
+    int64 [tokens, top_k]; a choice outside [0, experts) is dropped. Returns
+    (rows, choices, counts), int32: the place of each choice [tokens, top_k]
+    (~place, behind all others, of a dropped one), the choice at each place
+    [tokens * top_k], the rows of each expert [experts]: counts.tolist() are the
+    grouped GEMMs' m_splits."""
+    torch = _torch()
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"ids must be int32 or int64, got {str(ids.dtype).replace('torch.', '')}")
+    ldi = _rows2d(ids, "ids")
+    T, k = ids.shape
+    rows = ids.new_empty((T, k), dtype=_i32_t) if rows is None else _on(_expect(rows, "rows", (T, k), _i32_t), ids, "rows")
+    choices = ids.new_empty(T * k, dtype=_i32_t) if choices is None \
+        else _on(_expect(choices, "choices", (T * k,), _i32_t), ids, "choices")
+    counts = ids.new_empty(experts, dtype=_i32_t) if counts is None \
+        else _on(_expect(counts, "counts", (experts,), _i32_t), ids, "counts")
+    need = int(lib.mxgg_moe_sort_workspace(T, k, experts))
+    at, ws_bytes = None, 0
+    if need or ws is not None:
+        ws, ws_bytes = _ws(ws, need, ids)
+        at = ws.data_ptr()
+    _check(lib.mxgg_moe_sort(ids.data_ptr(), I64 if ids.dtype is torch.int64 else I32, ldi, T, k, experts,
+                             rows.data_ptr(), choices.data_ptr(), counts.data_ptr(), at, ws_bytes, _stream_of(ids)))
+    return rows, choices, counts
+
+
+def mxgg_moe_dispatch(x, rows, expert_rows=None, out=None):
+    """Tokens' rows to the places of their choices: out[rows[t, j]] = x[t], zeros
+    at the places of dropped ones. x: bf16 or fp32 [tokens, cols] (any row
+    stride); rows from moe_sort; expert_rows: the rows of out (tokens * top_k, or
+    sum(m_splits) to leave the dropped ones out)."""
+    dt, ldx = _dtype(x, "x"), _rows2d(x, "x")
+    T, k = _rows_index(_on(rows, x, "rows"))
+    if x.shape[0] != T:
+        raise ValueError(f"x has {x.shape[0]} rows, rows is of {T} tokens")
+    if expert_rows is None:
+        expert_rows = T * k if out is None else out.shape[0]
+    out, ldo = _like_rows(out, "out", expert_rows, x)
+    _check(lib.mxgg_moe_dispatch(x.data_ptr(), ldx, dt, T, x.shape[1], rows.data_ptr(), k, out.data_ptr(), ldo,
+                                 expert_rows, _stream_of(x)))
+    return out
+
+
+def _token_weights(weights, rows):
+    return _on(_expect(weights, "weights", rows.shape, _f32_t), rows, "weights")
+
+
+def mxgg_moe_combine(y, rows, weights=None, out=None):
+    """Experts' rows back to their tokens: out[t] = sum_j weights[t, j] y[rows[t,
+    j]] over the choices that are not dropped, summed in fp32. y: bf16 or fp32
+    [expert rows, cols] (any row stride); weights: fp32 [tokens, top_k], None for
+    1 (then it is the gradient of moe_dispatch)."""
+    dt, ldy = _dtype(y, "y"), _rows2d(y, "y")
+    T, k = _rows_index(_on(rows, y, "rows"))
+    if weights is not None:
+        _token_weights(weights, rows)
+    out, ldo = _like_rows(out, "out", T, y)
+    _check(lib.mxgg_moe_combine(y.data_ptr(), ldy, dt, y.shape[0], y.shape[1], rows.data_ptr(), _at(weights), T, k,
+                                out.data_ptr(), ldo, _stream_of(y)))
+    return out
+
+
+def mxgg_moe_combine_bwd(dout, y, rows, weights, dy=None, dweights=None):
+    """The gradients of moe_combine: (dy, dweights), dy like y (zeros at the
+    places of dropped choices), dweights fp32 [tokens, top_k]."""
+    dt, ldy = _dtype(y, "y"), _rows2d(y, "y")
+    T, k = _rows_index(_on(rows, y, "rows"))
+    if dout is None:
+        raise ValueError("dout is required")
+    dout, lddo = _like_rows(dout, "dout", T, y)
+    _token_weights(weights, rows)
+    dy, lddy = _like_rows(dy, "dy", y.shape[0], y)
+    dweights = y.new_empty((T, k), dtype=_f32_t) if dweights is None \
+        else _on(_expect(dweights, "dweights", (T, k), _f32_t), y, "dweights")
+    _check(lib.mxgg_moe_combine_bwd(dout.data_ptr(), lddo, y.data_ptr(), ldy, dt, y.shape[0], y.shape[1],
+                                    rows.data_ptr(), weights.data_ptr(), T, k, dy.data_ptr(), lddy,
+                                    dweights.data_ptr(), _stream_of(y)))
+    return dy, dweights
+
+
+def mxgg_dropout(x, p, state, stream=0, residual=None, out=None):
+    """residual + x / (1 - p) where kept, residual where dropped; the mask is a
+    function of state (int64 [2] on the device: seed and step), of `stream` (an
+    int that tells the calls of a step apart) and of the element's row and column,
+    so the same call on the gradient of out, without residual, is the gradient of
+    x. x: bf16 or fp32 [rows, cols] (any row stride), residual and out like it; out
+    may be x or residual."""
+    dt, ldx = _dtype(x, "x"), _rows2d(x, "x")
+    rows, cols = x.shape
+    _on(_expect(state, "state", (2,), _torch().int64), x, "state")
+    if not 0 <= stream < 1 << 32:
+        raise ValueError(f"stream={stream} outside [0, 2^32)")
+    ldr = cols if residual is None else _rows_like(residual, x, "residual")
+    if out is None:
+        out, ldo = x.new_empty((rows, cols)), cols
+    else:
+        ldo = _rows_like(out, x, "out")
+    _check(lib.mxgg_dropout(x.data_ptr(), ldx, dt, rows, cols, p, state.data_ptr(), stream, _at(residual), ldr,
+                            out.data_ptr(), ldo, _stream_of(x)))
+    return out
+
+
 # short names
 quantize_rowwise = mxgg_quantize_rowwise
 quantize_colwise_segpad = mxgg_quantize_colwise_segpad
@@ -711,3 +851,8 @@ grad_norm = mxgg_grad_norm
 clip_grad_norm = mxgg_clip_grad_norm
 clip_grads_with_norm = mxgg_clip_grads_with_norm
 moe_layer = mxgg_moe_layer
+moe_sort = mxgg_moe_sort
+moe_dispatch = mxgg_moe_dispatch
+moe_combine = mxgg_moe_combine
+moe_combine_bwd = mxgg_moe_combine_bwd
+dropout = mxgg_dropout

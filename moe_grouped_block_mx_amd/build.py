@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmxgg.so")
 
 SOURCES = ["api.cpp", "quant_mx.hip", "quant_blockwise.hip", "gemm_mx.hip", "layer_norm.hip", "grad_clip.hip",
-           "moe_layer.hip"]
+           "moe_layer.hip", "moe_dispatch.hip", "gemm_int8.hip", "dropout.hip"]
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.
 HIP_FLAGS = [

@@ -12,6 +12,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstring>
 #include <mutex>
 #include <numeric>
@@ -21,8 +22,10 @@
 #include "../../include/mxgg.h"
 #include "block_launch.hpp"
 #include "launch.hpp"
+#include "token_launch.hpp"
 #include "validate.hpp"
 #include "validate_block.hpp"
+#include "validate_token.hpp"
 
 namespace mxgg {
 namespace {
@@ -202,6 +205,40 @@ Check grad_norm_and_clip(void* const* grads, const int64_t* numels, const int32_
   return Check{};
 }
 
+mxgg_status quantize_int8(const void* x, int64_t rows, int64_t cols, int64_t ldx, int fmt, void* q, void* scales,
+                          hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_quantize_int8(x, rows, cols, ldx, fmt, q, scales));
+    if (rows == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{x, "x"}, {q, "q"}, {scales, "scales"}}, &cus));
+    return hip_status(launch_quant_int8(static_cast<const uint16_t*>(x), rows, cols, ldx, static_cast<int8_t*>(q),
+                                        static_cast<float*>(scales), stream),
+                      "int8 quantizer launch");
+  });
+}
+
+mxgg_status grouped_fwd_int8(const void* a_q, const void* a_s, int a_fmt, const void* w_q, const void* w_s, int w_fmt,
+                             const int64_t* m_splits, int32_t G, int64_t M, int64_t N, int64_t K, void* out,
+                             hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_fwd_int8(a_q, a_s, a_fmt, w_q, w_s, w_fmt, m_splits, G, M, N, K, out));
+    if (M == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{a_q, "a_q"}, {a_s, "a_s"}, {w_q, "w_q"}, {w_s, "w_s"}, {out, "out"}}, &cus));
+    Int8Params p;
+    p.a = static_cast<const uint8_t*>(a_q);
+    p.as = static_cast<const float*>(a_s);
+    p.w = static_cast<const uint8_t*>(w_q);
+    p.ws = static_cast<const float*>(w_s);
+    p.out = static_cast<uint16_t*>(out);
+    p.n = N;
+    p.k = (int32_t)K;
+    p.sp = make_splits(m_splits, G);
+    return hip_status(launch_grouped_int8(p, cus, stream), "int8 forward launch");
+  });
+}
+
 }  // namespace
 }  // namespace mxgg
 
@@ -259,6 +296,7 @@ mxgg_status mxgg_mx_scales_relayout(const void* src, mxgg_scale_layout src_layou
 
 mxgg_status mxgg_quantize_rowwise(const void* x, int64_t rows, int64_t cols, int64_t ldx, mxgg_format fmt,
                                   uint32_t flags, void* q, void* scales, hipStream_t stream) {
+  if (format_bits(fmt) == MXGG_INT8) return quantize_int8(x, rows, cols, ldx, (int)fmt, q, scales, stream);
   if (is_p2(fmt)) flags |= MXGG_POW2_SCALES;
   fmt = (mxgg_format)base_format(fmt);
   Check c = validate_quantize_rowwise(x, rows, cols, ldx, (int)fmt, q, scales);
@@ -354,6 +392,8 @@ mxgg_status mxgg_transpose_128x128(const void* w_q, const void* w_s, int32_t G, 
 mxgg_status mxgg_grouped_fwd(const void* a_q, const void* a_s, mxgg_format a_fmt, const void* w_q, const void* w_s,
                              mxgg_format w_fmt, const int64_t* m_splits, int32_t G, int64_t M, int64_t N, int64_t K,
                              void* out, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (format_bits(a_fmt) == MXGG_INT8 && format_bits(w_fmt) == MXGG_INT8)
+    return grouped_fwd_int8(a_q, a_s, (int)a_fmt, w_q, w_s, (int)w_fmt, m_splits, G, M, N, K, out, stream);
   // power-of-two blockwise scales on both sides: the MFMA applies them
   const bool p2 = is_p2(a_fmt) && is_p2(w_fmt);
   a_fmt = (mxgg_format)base_format(a_fmt);
@@ -668,6 +708,134 @@ mxgg_status mxgg_moe_layer(const void* x, int64_t ldx, const void* logits, int64
     const MoeFormat mf = f == MXGG_MXFP4 ? kMoeFp4 : f == MXGG_MXFP8 ? kMoeFp8 : kMoeBlock;
     return hip_status(launch_moe_layer(p, mf, cus, stream),
                       "expert layer launch");
+  });
+}
+
+size_t mxgg_moe_sort_workspace(int64_t tokens, int64_t top_k, int64_t experts) {
+  if (!check_choices(tokens, top_k).ok() || experts < 1 || experts > MXGG_MAX_EXPERTS) return 0;
+  return sort_workspace(tokens * top_k, experts);
+}
+
+mxgg_status mxgg_moe_sort(const void* ids, mxgg_itype itype, int64_t ldi, int64_t tokens, int64_t top_k, int64_t experts,
+                          int32_t* rows, int32_t* choices, int32_t* counts, void* ws, size_t ws_bytes,
+                          hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_moe_sort(ids, (int)itype, ldi, tokens, top_k, experts, rows, choices, counts));
+    MXGG_TRY(check_workspace(ws, ws_bytes, sort_workspace(tokens * top_k, experts)));
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{ids, "ids"}, {rows, "rows"}, {choices, "choices"}, {counts, "counts"}, {ws, "ws"}},
+                           &cus));
+    SortParams p;
+    p.ids = ids;
+    p.rows = rows;
+    p.choices = choices;
+    p.counts = counts;
+    p.table = static_cast<int32_t*>(ws);
+    p.ldi = ldi;
+    p.n = (int32_t)(tokens * top_k);
+    p.top_k = (int32_t)top_k;
+    p.experts = (int32_t)experts;
+    return hip_status(launch_moe_sort(p, itype == MXGG_I64, stream), "sort launch");
+  });
+}
+
+mxgg_status mxgg_moe_dispatch(const void* x, int64_t ldx, mxgg_dtype dtype, int64_t tokens, int64_t cols,
+                              const int32_t* rows, int64_t top_k, void* out, int64_t ldo, int64_t expert_rows,
+                              hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_moe_dispatch(x, ldx, (int)dtype, tokens, cols, rows, top_k, out, ldo, expert_rows));
+    if (tokens == 0 || expert_rows == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{x, "x"}, {rows, "rows"}, {out, "out"}}, &cus));
+    TokenParams p{};
+    p.x = x;
+    p.out = out;
+    p.rows = rows;
+    p.tokens = tokens;
+    p.expert_rows = expert_rows;
+    p.ldx = ldx;
+    p.ldo = ldo;
+    p.top_k = (int32_t)top_k;
+    p.cols = (int32_t)cols;
+    return hip_status(launch_moe_dispatch(p, dtype == MXGG_F32, stream), "dispatch launch");
+  });
+}
+
+mxgg_status mxgg_moe_combine(const void* y, int64_t ldy, mxgg_dtype dtype, int64_t expert_rows, int64_t cols,
+                             const int32_t* rows, const float* weights, int64_t tokens, int64_t top_k, void* out,
+                             int64_t ldo, hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_moe_combine(y, ldy, (int)dtype, expert_rows, cols, rows, weights, tokens, top_k, out, ldo));
+    if (tokens == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{expert_rows ? y : nullptr, "y"}, {rows, "rows"}, {weights, "weights"}, {out, "out"}},
+                           &cus));
+    TokenParams p{};
+    p.y = y;
+    p.out = out;
+    p.rows = rows;
+    p.weights = weights;
+    p.tokens = tokens;
+    p.expert_rows = expert_rows;
+    p.ldy = ldy;
+    p.ldo = ldo;
+    p.top_k = (int32_t)top_k;
+    p.cols = (int32_t)cols;
+    return hip_status(launch_moe_combine(p, dtype == MXGG_F32, stream), "combine launch");
+  });
+}
+
+mxgg_status mxgg_moe_combine_bwd(const void* dout, int64_t lddo, const void* y, int64_t ldy, mxgg_dtype dtype,
+                                 int64_t expert_rows, int64_t cols, const int32_t* rows, const float* weights,
+                                 int64_t tokens, int64_t top_k, void* dy, int64_t lddy, float* dweights,
+                                 hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_moe_combine_bwd(dout, lddo, y, ldy, (int)dtype, expert_rows, cols, rows, weights, tokens, top_k, dy,
+                                      lddy, dweights));
+    if (tokens == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{dout, "dout"}, {expert_rows ? y : nullptr, "y"}, {rows, "rows"}, {weights, "weights"},
+                                    {expert_rows ? dy : nullptr, "dy"}, {dweights, "dweights"}}, &cus));
+    TokenParams p{};
+    p.x = dout;
+    p.y = y;
+    p.out = dy;
+    p.rows = rows;
+    p.weights = weights;
+    p.dweights = dweights;
+    p.tokens = tokens;
+    p.expert_rows = expert_rows;
+    p.ldx = lddo;
+    p.ldy = ldy;
+    p.ldo = lddy;
+    p.top_k = (int32_t)top_k;
+    p.cols = (int32_t)cols;
+    return hip_status(launch_moe_combine_bwd(p, dtype == MXGG_F32, stream), "combine backward launch");
+  });
+}
+
+mxgg_status mxgg_dropout(const void* x, int64_t ldx, mxgg_dtype dtype, int64_t rows, int64_t cols, float p,
+                         const int64_t* state, uint32_t call, const void* residual, int64_t ldr, void* out, int64_t ldo,
+                         hipStream_t stream) {
+  return guarded([&]() -> Check {
+    MXGG_TRY(validate_dropout(x, ldx, (int)dtype, rows, cols, p, state, residual, ldr, out, ldo));
+    if (rows == 0) return Check{};
+    int cus = 0;
+    MXGG_TRY(device_checks(stream, {{x, "x"}, {residual, "residual"}, {out, "out"}, {state, "state"}}, &cus));
+    DropoutParams d;
+    d.x = x;
+    d.residual = residual;
+    d.out = out;
+    d.state = state;
+    d.rows = rows;
+    d.ldx = ldx;
+    d.ldr = ldr;
+    d.ldo = ldo;
+    d.cols = (int32_t)cols;
+    d.stream = call;
+    d.limit = (uint32_t)std::nearbyint((double)p * 65536.0);
+    d.scale = d.limit < 65536 ? (float)(65536.0 / (65536.0 - d.limit)) : 0.f;
+    return hip_status(launch_dropout(d, dtype == MXGG_F32, stream), "dropout launch");
   });
 }
 
