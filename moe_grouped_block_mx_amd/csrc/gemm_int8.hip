@@ -130,6 +130,12 @@ hipError_t quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx
 // Weights are the MFMA's first operand, tokens the second: register i of a
 // 32x32 result is then channel 8 (i/4) + 4 (lane/32) + i%4 of token lane%32, four
 // neighbouring channels of one row.
+//
+// A workgroup has 256 channels and 256 tokens at a time, and its eight waves 128 x
+// 64 of them each. Stages of 64 codes of every row come to LDS by DMA, four slots in
+// a ring that runs on over the workgroup's tiles. The two waves of a SIMD take
+// turns: while one reads a stage's operands from LDS and issues loads, the other
+// has the matrix unit to itself, and a barrier swaps them.
 
 #define MXGG_LDS __attribute__((address_space(3)))
 
@@ -138,22 +144,30 @@ __device__ __forceinline__ void wait_vmcnt() {
   static_assert(N >= 0 && N < 64, "vmcnt range");
   __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
+// all reads from LDS
+__device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xF | (3 << 14) | (0x7 << 4)); }
 // Workgroup barrier without a memory fence (which would wait for every load to
-// LDS in flight)
+// LDS in flight); nothing moves across it.
 __device__ __forceinline__ void raw_barrier() {
+  __builtin_amdgcn_sched_barrier(0);
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
 }
-__device__ __forceinline__ void dma16(const uint8_t* src, uint8_t* lds) {
-  __builtin_amdgcn_global_load_lds((const void*)src, (MXGG_LDS void*)lds, 16, 0, 0);
+// A buffer from a wave-uniform base: reads past its end give zeros
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void* base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), 0,
+                                           (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
-// what stands in for the codes behind the contraction's end
-static __device__ __attribute__((aligned(64))) uint32_t g_zeros[16];
+constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's end
 
 constexpr int kTile = 256;            // channels and tokens of a tile
-constexpr int kStageK = 128;          // codes of a row in a stage
-constexpr int kOperand = kTile * kStageK, kStage = 2 * kOperand, kSlots = 2;
+constexpr int kStageK = 64;           // codes of a row in a stage
+constexpr int kOperand = kTile * kStageK, kStage = 2 * kOperand, kSlots = 4;
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kWaveN = 128, kWaveM = 64;      // 2 x 4 waves
 constexpr int kFN = kWaveN / 32, kFM = kWaveM / 32;
@@ -161,15 +175,20 @@ constexpr int kLoads = kOperand / (kWaves * 1024);   // 1 KiB loads of an operan
 constexpr int kTileGroup = 4;
 
 struct Tile {
-  const uint8_t* w;       // first channel's codes
-  const uint8_t* a;       // first token's
-  int64_t row0;
-  int g, col0, rows, cols;
+  int row0, g, col0, rows, cols;
 };
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-struct Offsets {
-  uint32_t w[kLoads], a[kLoads];
-};
+// The first `left` (1 to 7) of eight bf16
+__device__ __forceinline__ void store_some(uint16_t* out, uint32_t d0, uint32_t d1, uint32_t d2, uint32_t d3, int left) {
+  if (left & 4) {
+    const uint64_t v = d0 | (uint64_t)d1 << 32;
+    memcpy(out, &v, 8);
+  }
+  const uint32_t a = left & 4 ? d2 : d0, b = left & 4 ? d3 : d1;
+  if (left & 2) memcpy(out + (left & 4), &a, 4);
+  if (left & 1) out[left & 6] = (uint16_t)(left & 2 ? b : a);
+}
 
 __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Params p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -182,8 +201,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
   __syncthreads();
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wn = w / 4, wm = w % 4, h = lane >> 5, l32 = lane & 31;
-  const int total = offs[G], stages = (p.k + kStageK - 1) / kStageK;
+  const int turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4, h = lane >> 5, l32 = lane & 31;
+  const int K = p.k, total = __builtin_amdgcn_readfirstlane(offs[G]), stages = (K + kStageK - 1) / kStageK;
   const int nb = gridDim.x, b = blockIdx.x;
   // neighbouring tiles on one XCD (workgroups are dealt round the 8 of them):
   // they share operands in its L2
@@ -191,109 +210,148 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
 
   const auto find = [&](int t) {
     Tile o;
-    o.g = upper_bound_i32(offs, G + 1, t) - 1;
-    const int mt = (offs[o.g + 1] - offs[o.g]) / nt, local = t - offs[o.g];
+    o.g = uniform(upper_bound_i32(offs, G + 1, t) - 1);
+    const int o0 = uniform(offs[o.g]), mt = (uniform(offs[o.g + 1]) - o0) / nt, local = t - o0;
     const int r0 = local / (kTileGroup * nt) * kTileGroup, hgt = min(mt - r0, kTileGroup), in = local - r0 * nt;
     const int ct = in / hgt, rt = r0 + in % hgt;
-    o.row0 = pref[o.g] + (int64_t)rt * kTile;
+    o.row0 = uniform((int)pref[o.g]) + rt * kTile;
     o.col0 = ct * kTile;
     o.rows = min(p.sp.m[o.g] - rt * kTile, kTile);
     o.cols = (int)min(p.n - o.col0, (int64_t)kTile);
-    o.w = p.w + ((int64_t)o.g * p.n + o.col0) * p.k;
-    o.a = p.a + o.row0 * p.k;
     return o;
   };
-  // chunk c of row r lies at c ^ (r/2 % 8): the fragments' reads are then
-  // without bank conflicts
-  const int lr = lane / 8, lc = lane % 8;
-  const auto plan = [&](const Tile& o) {
-    Offsets f;
-#pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int r = (i * kWaves + w) * 8 + lr, c = lc ^ ((r >> 1) & 7);
-      f.w[i] = (uint32_t)(min(r, o.cols - 1) * p.k + c * 16);
-      f.a[i] = (uint32_t)(min(r, o.rows - 1) * p.k + c * 16);
-    }
-    return f;
+
+  // Issuing side. A load brings 16 rows; chunk c of row r lies at c ^ (r/4 % 4)
+  // of the row's four: the fragments' reads are then without bank conflicts.
+  const int lr = w * 16 + lane / 4, lc = (lane % 4) ^ (lane / 16);
+  const uint32_t lane_off = (uint32_t)(lr * K + lc * 16);
+  const int last_k = K - (stages - 1) * kStageK;          // codes of the last stage
+  const bool lane_in_last = lc * 16 < last_k;
+  int it = first, is = 0, slot_issue = 0;
+  const uint8_t *base_w = p.w, *base_a = p.a;
+  uint32_t size_w = 0, size_a = 0;
+  const auto aim = [&]() {
+    size_w = size_a = 0;                                  // nothing left: zeros, that the counts go on
+    if (it >= total) return;
+    const Tile o = find(it);
+    base_w = p.w + ((int64_t)o.g * p.n + o.col0) * K;
+    base_a = p.a + (int64_t)o.row0 * K;
+    size_w = (uint32_t)(o.cols * K);
+    size_a = (uint32_t)(o.rows * K);
   };
-  const auto issue = [&](const Tile& o, const Offsets& f, int s, int slot) {
-    uint8_t* at = smem + slot * kStage;
-    const uint8_t* zero = reinterpret_cast<const uint8_t*>(g_zeros);
+  const auto issue = [&]() {
+    uint8_t* at = smem + slot_issue * kStage + w * 1024;
+    const __amdgpu_buffer_rsrc_t bw = uniform_buffer(base_w, size_w), ba = uniform_buffer(base_a, size_a);
+    // zeros behind the contraction's end, of the tokens (the weights may be anything)
+    const uint32_t wo = lane_off + (uint32_t)(is * kStageK);
+    const uint32_t ao = is + 1 < stages || lane_in_last ? wo : kOutside;
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int r = (i * kWaves + w) * 8 + lr, c = lc ^ ((r >> 1) & 7);
-      const bool in = s * kStageK + c * 16 < p.k;
-      dma16(in ? o.w + s * kStageK + f.w[i] : zero, at + (i * kWaves + w) * 1024);
-      dma16(in ? o.a + s * kStageK + f.a[i] : zero, at + kOperand + (i * kWaves + w) * 1024);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, (MXGG_LDS void*)(at + i * (kWaves * 1024)), 16,
+                                               wo + (uint32_t)(i * 128 * K), 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba, (MXGG_LDS void*)(at + kOperand + i * (kWaves * 1024)), 16,
+                                               ao + (uint32_t)(i * 128 * K), 0, 0, 0);
+    }
+  };
+  const auto advance = [&]() {
+    slot_issue = (slot_issue + 1) & (kSlots - 1);
+    if (++is == stages) {
+      is = 0;
+      it += nb;
+      aim();
     }
   };
 
   if (first >= total) return;
-  Tile cur = find(first);
-  Offsets f = plan(cur);
+  aim();
+#pragma unroll
+  for (int s = 0; s < kSlots - 1; ++s) {
+    issue();
+    advance();
+  }
+  constexpr int kAhead = 2 * 2 * kLoads;                  // loads of the two stages behind the awaited one
+  wait_vmcnt<kAhead>();
+  raw_barrier();
+  if (turn) raw_barrier();                                // the second four waves are one turn behind
   int slot = 0;
-  issue(cur, f, 0, 0);
+  // a lane's pieces: codes 16 (2u + h) .. of row l32 of a fragment
+  const int piece0 = l32 * kStageK + (h ^ ((l32 >> 2) & 3)) * 16, piece1 = piece0 ^ 32;
+  const int at_w = wn * kWaveN * kStageK, at_a = kOperand + wm * kWaveM * kStageK;
   for (int t = first; t < total; t += nb) {
+    const Tile cur = find(t);
+    const bool busy = wn * kWaveN < cur.cols && wm * kWaveM < cur.rows;   // else nothing of the wave's is stored
     v16i acc[kFN][kFM];
 #pragma unroll
     for (int i = 0; i < kFN; ++i)
 #pragma unroll
       for (int j = 0; j < kFM; ++j) acc[i][j] = v16i{};
-    Tile next = cur;
     for (int s = 0; s < stages; ++s) {
-      wait_vmcnt<0>();
+      v4i wf[2][kFN], af[2][kFM];
+      if (busy) {
+        const uint8_t* st = smem + slot * kStage;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* pw = st + at_w + (u ? piece1 : piece0);
+          const uint8_t* pa = st + at_a + (u ? piece1 : piece0);
+#pragma unroll
+          for (int i = 0; i < kFN; ++i) wf[u][i] = *reinterpret_cast<const v4i*>(pw + i * 32 * kStageK);
+#pragma unroll
+          for (int j = 0; j < kFM; ++j) af[u][j] = *reinterpret_cast<const v4i*>(pa + j * 32 * kStageK);
+        }
+      }
+      slot = (slot + 1) & (kSlots - 1);
+      issue();
+      advance();
+      wait_lds();
+      if (turn) wait_vmcnt<kAhead>();
       raw_barrier();
-      if (s + 1 < stages) {
-        issue(cur, f, s + 1, slot ^ 1);
-      } else if (t + nb < total) {
-        next = find(t + nb);
-        f = plan(next);
-        issue(next, f, 0, slot ^ 1);
+      if (busy) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int i = 0; i < kFN; ++i)
+#pragma unroll
+            for (int j = 0; j < kFM; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][i], af[u][j], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
       }
-      const uint8_t* wt = smem + slot * kStage + wn * kWaveN * kStageK;
-      const uint8_t* at = smem + slot * kStage + kOperand + wm * kWaveM * kStageK;
-#pragma unroll
-      for (int u = 0; u < kStageK / 32; ++u) {
-        v4i wf[kFN], af[kFM];
-#pragma unroll
-        for (int i = 0; i < kFN; ++i) {
-          const int r = i * 32 + l32;
-          wf[i] = *reinterpret_cast<const v4i*>(wt + r * kStageK + ((2 * u + h) ^ ((r >> 1) & 7)) * 16);
-        }
-#pragma unroll
-        for (int j = 0; j < kFM; ++j) {
-          const int r = j * 32 + l32;
-          af[j] = *reinterpret_cast<const v4i*>(at + r * kStageK + ((2 * u + h) ^ ((r >> 1) & 7)) * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < kFN; ++i)
-#pragma unroll
-          for (int j = 0; j < kFM; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[i], af[j], acc[i][j], 0, 0, 0);
-      }
-      slot ^= 1;
+      if (!turn) wait_vmcnt<kAhead>();
+      raw_barrier();
     }
     // Epilogue: a lane has channels 8q + 4h .. +3 of token l32 in registers 4q ..
     // 4q + 3; the two halves of a wave exchange every other group, so that each
     // lane stores eight neighbouring channels.
+    if (!busy) continue;
+    const __amdgpu_buffer_rsrc_t scales =
+        uniform_buffer(p.ws + (int64_t)cur.g * p.n + cur.col0, (uint32_t)cur.cols * 4);
+    uint16_t* row[kFM];
+    float sa[kFM];
+    bool have[kFM];
 #pragma unroll
     for (int j = 0; j < kFM; ++j) {
       const int m = wm * kWaveM + j * 32 + l32;
-      const float sa = p.as[cur.row0 + min(m, cur.rows - 1)];
+      have[j] = m < cur.rows;
+      sa[j] = p.as[cur.row0 + min(m, cur.rows - 1)];
+      row[j] = p.out + (int64_t)(cur.row0 + m) * p.n + cur.col0;
+    }
 #pragma unroll
-      for (int i = 0; i < kFN; ++i)
+    for (int i = 0; i < kFN; ++i) {
+      const int n0 = wn * kWaveN + i * 32;
+      v4f sw[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        sw[q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(scales, (n0 + 8 * q + 4 * h) * 4, 0, 0));
+#pragma unroll
+      for (int j = 0; j < kFM; ++j)
 #pragma unroll
         for (int q = 0; q < 4; q += 2) {
           uint32_t v[4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int n0 = wn * kWaveN + i * 32 + 8 * (q + e) + 4 * h;
             float o[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int n = min(n0 + c, cur.cols - 1);
-              o[c] = (float)acc[i][j][4 * (q + e) + c] * sa * p.ws[(int64_t)cur.g * p.n + cur.col0 + n];
-            }
+            for (int c = 0; c < 4; ++c) o[c] = (float)acc[i][j][4 * (q + e) + c] * sa[j] * sw[q + e][c];
             v[2 * e] = bf16_pair(o[0], o[1]);
             v[2 * e + 1] = bf16_pair(o[2], o[3]);
           }
@@ -301,18 +359,14 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
           const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
           const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
           const uint32_t d[4] = {lo[0], hi[0], lo[1], hi[1]};
-          const int n0 = wn * kWaveN + i * 32 + 8 * (q + h);
-          if (m < cur.rows) {
-            uint16_t* out = p.out + (cur.row0 + m) * p.n + cur.col0 + n0;
-            if (n0 + 8 <= cur.cols) memcpy(out, d, 16);
-            else
-              for (int c = 0; c < 8; ++c)
-                if (n0 + c < cur.cols) out[c] = (uint16_t)(d[c / 2] >> (16 * (c % 2)));
-          }
+          const int n = n0 + 8 * (q + h), left = cur.cols - n;
+          if (have[j] && left >= 8) memcpy(row[j] + n, d, 16);
+          if (cur.cols % 8 && have[j] && left > 0 && left < 8) store_some(row[j] + n, d[0], d[1], d[2], d[3], left);
         }
     }
-    cur = next;
   }
+  if (!turn) raw_barrier();
+  wait_vmcnt<0>();
 }
 
 }  // namespace
