@@ -155,6 +155,11 @@ __device__ __forceinline__ void raw_barrier() {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_sched_barrier(0);
 }
+// Between a wave's lanes that meet in LDS (its accesses are done in order)
+__device__ __forceinline__ void wave_fence() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
 // A buffer from a wave-uniform base: reads past its end give zeros
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void* base, uint32_t bytes) {
   const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -165,14 +170,22 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void* bas
 }
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's end
 
-constexpr int kTile = 256;            // channels and tokens of a tile
 constexpr int kStageK = 64;           // codes of a row in a stage
-constexpr int kOperand = kTile * kStageK, kStage = 2 * kOperand, kSlots = 4;
 constexpr int kThreads = 512, kWaves = kThreads / 64;
-constexpr int kWaveN = 128, kWaveM = 64;      // 2 x 4 waves
-constexpr int kFN = kWaveN / 32, kFM = kWaveM / 32;
-constexpr int kLoads = kOperand / (kWaves * 1024);   // 1 KiB loads of an operand, a wave and stage
 constexpr int kTileGroup = 4;
+
+// FN fragments of 32 channels and FM of 32 tokens for each of 2 x 4 waves
+template <int FN, int FM, int SLOTS>
+struct Int8Tile {
+  static constexpr int TN = 64 * FN, TM = 128 * FM, WN = 32 * FN, WM = 32 * FM;
+  static constexpr int W_BYTES = TN * kStageK, STAGE = (TN + TM) * kStageK, LDS = SLOTS * STAGE;
+  // a wave's way out: 16 tokens of 64 channels, rows 16 bytes apart more
+  static constexpr int OUT_PITCH = 144, OUT_BYTES = 16 * OUT_PITCH, STORES = FM * FN * 2;
+  static constexpr int SMEM = LDS + kWaves * OUT_BYTES;
+  // 1 KiB loads of a wave and stage
+  static constexpr int LW = W_BYTES / (kWaves * 1024), LA = TM * kStageK / (kWaves * 1024);
+  static_assert(SMEM <= 154 * 1024 && LW >= 1 && LA >= 1 && FN % 2 == 0, "LDS: the ring beside the tables; whole loads");
+};
 
 struct Tile {
   int row0, g, col0, rows, cols;
@@ -190,15 +203,23 @@ __device__ __forceinline__ void store_some(uint16_t* out, uint32_t d0, uint32_t 
   if (left & 1) out[left & 6] = (uint16_t)(left & 2 ? b : a);
 }
 
+template <int FN, int FM, int SLOTS>
 __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Params p) {
+  using T = Int8Tile<FN, FM, SLOTS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int64_t pref[kMaxExperts + 1], tpref[kMaxExperts + 1], wtot[kWaves];
-  __shared__ int32_t offs[kMaxExperts + 1];
-  const int G = p.sp.G, nt = (int)((p.n + kTile - 1) / kTile);
-  block_prefix64<kThreads>(G, [&](int g) { return (int64_t)p.sp.m[g]; }, pref, wtot);
-  block_prefix64<kThreads>(G, [&](int g) { return (int64_t)((p.sp.m[g] + kTile - 1) / kTile); }, tpref, wtot);
-  for (int g = threadIdx.x; g <= G; g += kThreads) offs[g] = (int32_t)tpref[g] * nt;
-  __syncthreads();
+  __shared__ int32_t pref[kMaxExperts + 1], offs[kMaxExperts + 1];   // an expert's first row, and first tile
+  const int G = p.sp.G, nt = (int)((p.n + T::TN - 1) / T::TN);
+  {
+    int64_t* both = reinterpret_cast<int64_t*>(smem);                // the ring is not in use yet
+    block_prefix64<kThreads>(G, [&](int g) {
+      return (int64_t)((p.sp.m[g] + T::TM - 1) / T::TM) << 32 | p.sp.m[g];
+    }, both, both + kMaxExperts + 1);
+    for (int g = threadIdx.x; g <= G; g += kThreads) {
+      pref[g] = (int32_t)both[g];
+      offs[g] = (int32_t)(both[g] >> 32) * nt;
+    }
+    __syncthreads();
+  }
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4, h = lane >> 5, l32 = lane & 31;
@@ -214,10 +235,10 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
     const int o0 = uniform(offs[o.g]), mt = (uniform(offs[o.g + 1]) - o0) / nt, local = t - o0;
     const int r0 = local / (kTileGroup * nt) * kTileGroup, hgt = min(mt - r0, kTileGroup), in = local - r0 * nt;
     const int ct = in / hgt, rt = r0 + in % hgt;
-    o.row0 = uniform((int)pref[o.g]) + rt * kTile;
-    o.col0 = ct * kTile;
-    o.rows = min(p.sp.m[o.g] - rt * kTile, kTile);
-    o.cols = (int)min(p.n - o.col0, (int64_t)kTile);
+    o.row0 = uniform(pref[o.g]) + rt * T::TM;
+    o.col0 = ct * T::TN;
+    o.rows = min(p.sp.m[o.g] - rt * T::TM, T::TM);
+    o.cols = (int)min(p.n - o.col0, (int64_t)T::TN);
     return o;
   };
 
@@ -240,21 +261,22 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
     size_a = (uint32_t)(o.rows * K);
   };
   const auto issue = [&]() {
-    uint8_t* at = smem + slot_issue * kStage + w * 1024;
+    uint8_t* at = smem + slot_issue * T::STAGE + w * 1024;
     const __amdgpu_buffer_rsrc_t bw = uniform_buffer(base_w, size_w), ba = uniform_buffer(base_a, size_a);
     // zeros behind the contraction's end, of the tokens (the weights may be anything)
     const uint32_t wo = lane_off + (uint32_t)(is * kStageK);
     const uint32_t ao = is + 1 < stages || lane_in_last ? wo : kOutside;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
+    for (int i = 0; i < T::LW; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, (MXGG_LDS void*)(at + i * (kWaves * 1024)), 16,
                                                wo + (uint32_t)(i * 128 * K), 0, 0, 0);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba, (MXGG_LDS void*)(at + kOperand + i * (kWaves * 1024)), 16,
+#pragma unroll
+    for (int i = 0; i < T::LA; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba, (MXGG_LDS void*)(at + T::W_BYTES + i * (kWaves * 1024)), 16,
                                                ao + (uint32_t)(i * 128 * K), 0, 0, 0);
-    }
   };
   const auto advance = [&]() {
-    slot_issue = (slot_issue + 1) & (kSlots - 1);
+    slot_issue = slot_issue + 1 == SLOTS ? 0 : slot_issue + 1;
     if (++is == stages) {
       is = 0;
       it += nb;
@@ -264,42 +286,41 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
 
   if (first >= total) return;
   aim();
-#pragma unroll
-  for (int s = 0; s < kSlots - 1; ++s) {
+  for (int s = 0; s < SLOTS - 1; ++s) {
     issue();
     advance();
   }
-  constexpr int kAhead = 2 * 2 * kLoads;                  // loads of the two stages behind the awaited one
+  constexpr int kAhead = (SLOTS - 2) * (T::LW + T::LA);   // loads of the stages behind the awaited one
   wait_vmcnt<kAhead>();
   raw_barrier();
   if (turn) raw_barrier();                                // the second four waves are one turn behind
   int slot = 0;
   // a lane's pieces: codes 16 (2u + h) .. of row l32 of a fragment
   const int piece0 = l32 * kStageK + (h ^ ((l32 >> 2) & 3)) * 16, piece1 = piece0 ^ 32;
-  const int at_w = wn * kWaveN * kStageK, at_a = kOperand + wm * kWaveM * kStageK;
+  const int at_w = wn * T::WN * kStageK, at_a = T::W_BYTES + wm * T::WM * kStageK;
   for (int t = first; t < total; t += nb) {
     const Tile cur = find(t);
-    const bool busy = wn * kWaveN < cur.cols && wm * kWaveM < cur.rows;   // else nothing of the wave's is stored
-    v16i acc[kFN][kFM];
+    const bool busy = wn * T::WN < cur.cols && wm * T::WM < cur.rows;   // else nothing of the wave's is stored
+    v16i acc[FN][FM];
 #pragma unroll
-    for (int i = 0; i < kFN; ++i)
+    for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int j = 0; j < kFM; ++j) acc[i][j] = v16i{};
+      for (int j = 0; j < FM; ++j) acc[i][j] = v16i{};
     for (int s = 0; s < stages; ++s) {
-      v4i wf[2][kFN], af[2][kFM];
+      v4i wf[2][FN], af[2][FM];
       if (busy) {
-        const uint8_t* st = smem + slot * kStage;
+        const uint8_t* st = smem + slot * T::STAGE;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const uint8_t* pw = st + at_w + (u ? piece1 : piece0);
           const uint8_t* pa = st + at_a + (u ? piece1 : piece0);
 #pragma unroll
-          for (int i = 0; i < kFN; ++i) wf[u][i] = *reinterpret_cast<const v4i*>(pw + i * 32 * kStageK);
+          for (int i = 0; i < FN; ++i) wf[u][i] = *reinterpret_cast<const v4i*>(pw + i * 32 * kStageK);
 #pragma unroll
-          for (int j = 0; j < kFM; ++j) af[u][j] = *reinterpret_cast<const v4i*>(pa + j * 32 * kStageK);
+          for (int j = 0; j < FM; ++j) af[u][j] = *reinterpret_cast<const v4i*>(pa + j * 32 * kStageK);
         }
       }
-      slot = (slot + 1) & (kSlots - 1);
+      slot = slot + 1 == SLOTS ? 0 : slot + 1;
       issue();
       advance();
       wait_lds();
@@ -310,9 +331,9 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int i = 0; i < kFN; ++i)
+          for (int i = 0; i < FN; ++i)
 #pragma unroll
-            for (int j = 0; j < kFM; ++j)
+            for (int j = 0; j < FM; ++j)
               acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][i], af[u][j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
       }
@@ -320,53 +341,241 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
       raw_barrier();
     }
     // Epilogue: a lane has channels 8q + 4h .. +3 of token l32 in registers 4q ..
-    // 4q + 3; the two halves of a wave exchange every other group, so that each
-    // lane stores eight neighbouring channels.
+    // 4q + 3. The two halves of a wave exchange every other group, so that each
+    // lane has eight neighbouring channels; 16 tokens of 64 channels go through LDS
+    // and leave as whole lines.
     if (!busy) continue;
     const __amdgpu_buffer_rsrc_t scales =
         uniform_buffer(p.ws + (int64_t)cur.g * p.n + cur.col0, (uint32_t)cur.cols * 4);
-    uint16_t* row[kFM];
-    float sa[kFM];
-    bool have[kFM];
+    float sa[FM];
 #pragma unroll
-    for (int j = 0; j < kFM; ++j) {
-      const int m = wm * kWaveM + j * 32 + l32;
-      have[j] = m < cur.rows;
-      sa[j] = p.as[cur.row0 + min(m, cur.rows - 1)];
-      row[j] = p.out + (int64_t)(cur.row0 + m) * p.n + cur.col0;
-    }
+    for (int j = 0; j < FM; ++j) sa[j] = p.as[cur.row0 + min(wm * T::WM + j * 32 + l32, cur.rows - 1)];
+    uint8_t* scr = smem + T::LDS + w * T::OUT_BYTES;
+    const int m_out = wm * T::WM + lane / 8, n_out = wn * T::WN + lane % 8 * 8;
+    uint16_t* out = p.out + (int64_t)(cur.row0 + m_out) * p.n + cur.col0 + n_out;
 #pragma unroll
-    for (int i = 0; i < kFN; ++i) {
-      const int n0 = wn * kWaveN + i * 32;
-      v4f sw[4];
+    for (int c = 0; c < FN / 2; ++c) {
+      v4f sw[2][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        sw[q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(scales, (n0 + 8 * q + 4 * h) * 4, 0, 0));
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < kFM; ++j)
+        for (int q = 0; q < 4; ++q)
+          sw[i][q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
+                                                 scales, (wn * T::WN + c * 64 + i * 32 + 8 * q + 4 * h) * 4, 0, 0));
 #pragma unroll
-        for (int q = 0; q < 4; q += 2) {
-          uint32_t v[4];
+      for (int j = 0; j < FM; ++j) {
+        uint32_t d[2][2][4];                              // 16 channels of each fragment and pair of groups
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float o[4];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) o[c] = (float)acc[i][j][4 * (q + e) + c] * sa[j] * sw[q + e][c];
-            v[2 * e] = bf16_pair(o[0], o[1]);
-            v[2 * e + 1] = bf16_pair(o[2], o[3]);
+          for (int q = 0; q < 4; q += 2) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float o[4];
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[r] = (float)acc[2 * c + i][j][4 * (q + e) + r] * sa[j] * sw[i][q + e][r];
+              v[2 * e] = bf16_pair(o[0], o[1]);
+              v[2 * e + 1] = bf16_pair(o[2], o[3]);
+            }
+            // lower half: group q of both halves; upper half: group q + 1
+            const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
+            d[i][q / 2][0] = lo[0];
+            d[i][q / 2][1] = hi[0];
+            d[i][q / 2][2] = lo[1];
+            d[i][q / 2][3] = hi[1];
           }
-          // lower half: group q of both halves; upper half: group q + 1
-          const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-          const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-          const uint32_t d[4] = {lo[0], hi[0], lo[1], hi[1]};
-          const int n = n0 + 8 * (q + h), left = cur.cols - n;
-          if (have[j] && left >= 8) memcpy(row[j] + n, d, 16);
-          if (cur.cols % 8 && have[j] && left > 0 && left < 8) store_some(row[j] + n, d[0], d[1], d[2], d[3], left);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          wave_fence();
+          if (l32 / 16 == t) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<v4i*>(scr + l32 % 16 * T::OUT_PITCH + (i * 32 + 8 * (2 * q + h)) * 2) =
+                    v4i{(int)d[i][q][0], (int)d[i][q][1], (int)d[i][q][2], (int)d[i][q][3]};
+          }
+          wave_fence();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const v4i o = *reinterpret_cast<const v4i*>(scr + (lane / 8 + 8 * k) * T::OUT_PITCH + lane % 8 * 16);
+            const int down = j * 32 + t * 16 + k * 8, left = cur.cols - n_out - c * 64;
+            uint16_t* to = out + (int64_t)down * p.n + c * 64;
+            if (m_out + down < cur.rows) {
+              if (left >= 8) memcpy(to, &o, 16);
+              else if (left > 0) store_some(to, o[0], o[1], o[2], o[3], left);
+            }
+          }
         }
+      }
     }
   }
   if (!turn) raw_barrier();
   wait_vmcnt<0>();
+}
+
+// ---------------------------------------------------------------------------
+// Product of few tokens
+//
+// A workgroup has NF fragments of 16 channels and up to MF fragments of 16 tokens of
+// one expert; its eight waves split the contraction and meet in LDS at the end.
+// 32-bit sums are whole numbers, so their order does not matter. A wave brings its
+// 64-code steps to a ring of its own in LDS and waits for its own loads only.
+// (Straight to registers a lane would load 16 bytes of another row than its
+// neighbour does, which takes the address unit a cycle a lane.)
+
+constexpr int kFewWaves = 8;
+constexpr int few_slots(int nf, int mf) { return nf + mf <= 2 ? 4 : nf + mf <= 3 ? 3 : nf + mf <= 4 ? 4 : nf + mf <= 6 ? 3 : 2; }
+constexpr int few_lds(int nf, int mf) { return kFewWaves * few_slots(nf, mf) * (nf + mf) * 1024; }
+
+// Expert and rows of piece `seg`, when an expert's tokens go `each` at a time
+struct Piece {
+  int g, row0, rows;
+};
+__device__ __forceinline__ Piece find_piece(const SplitArgs& sp, int seg, int each) {
+  if (sp.G == 1) return Piece{0, seg * each, min(sp.m[0] - seg * each, each)};
+  const int lane = threadIdx.x & 63, per = (sp.G + 63) / 64;
+  // pieces (high half) and rows of the lane's experts, then of those before
+  uint64_t sum = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i, m = e < sp.G ? sp.m[e] : 0;
+    sum += (uint64_t)((m + each - 1) / each) << 32 | (uint32_t)m;
+  }
+  uint64_t upto = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint64_t o = __shfl_up((unsigned long long)upto, d, 64);
+    if (lane >= d) upto += o;
+  }
+  const int owner = __popcll(__ballot((int)(upto >> 32) <= seg));   // lanes whose pieces all come before
+  const uint64_t before = __shfl((unsigned long long)(upto - sum), owner, 64);
+  Piece p;
+  int left = uniform(seg - (int)(before >> 32)), row = uniform((int)(uint32_t)before);
+  p.g = uniform(owner) * per;
+  for (; p.g < sp.G; ++p.g) {
+    const int n = (sp.m[p.g] + each - 1) / each;
+    if (left < n) break;
+    left -= n;
+    row += sp.m[p.g];
+  }
+  p.row0 = row + left * each;
+  p.rows = min(sp.m[p.g] - left * each, each);
+  return p;
+}
+
+template <int NF, int MF>
+__global__ __launch_bounds__(kFewWaves * 64) void few_int8_kernel(const Int8Params p) {
+  constexpr int S = few_slots(NF, MF), LOADS = NF + MF, SLOT = LOADS * 1024;
+  static_assert(S * LOADS >= NF * MF, "a wave's sums fit in its ring");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  uint8_t* ring = smem + w * (S * SLOT);
+  const Piece pc = find_piece(p.sp, blockIdx.y, 16 * MF);
+  const int K = p.k, col0 = (int)blockIdx.x * (16 * NF), cols = (int)min(p.n - col0, (int64_t)(16 * NF));
+  const __amdgpu_buffer_rsrc_t bw = uniform_buffer(p.w + ((int64_t)pc.g * p.n + col0) * K, (uint32_t)(cols * K));
+  const __amdgpu_buffer_rsrc_t ba = uniform_buffer(p.a + (int64_t)pc.row0 * K, (uint32_t)(pc.rows * K));
+  const int steps = (K + 63) / 64, per = (steps + kFewWaves - 1) / kFewWaves;
+  const int begin = min(w * per, steps), end = min(begin + per, steps);
+  // chunk c of row r lies at c ^ (r/4 % 4), as in the stages above
+  const int lc = ((lane % 4) ^ (lane / 16)) * 16;
+  const uint32_t row = (uint32_t)(lane / 4 * K + lc);
+  const auto issue = [&](int s, int slot) {
+    // past the wave's part or the contraction's end: zeros
+    const uint32_t off = s < end && s * 64 + lc < K ? row + (uint32_t)(s * 64) : kOutside;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, (MXGG_LDS void*)(ring + slot * SLOT + i * 1024), 16,
+                                               off + (uint32_t)(i * 16 * K), 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < MF; ++j)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ba, (MXGG_LDS void*)(ring + slot * SLOT + (NF + j) * 1024), 16,
+                                               off + (uint32_t)(j * 16 * K), 0, 0, 0);
+  };
+  // Scales of the fragments that this wave will store: register c of lane l of
+  // fragment (i, j) is channel 16 i + 4 (l / 16) + c of token 16 j + l % 16.
+  constexpr int PER = (NF * MF + kFewWaves - 1) / kFewWaves;
+  const __amdgpu_buffer_rsrc_t bs = uniform_buffer(p.ws + (int64_t)pc.g * p.n + col0, (uint32_t)cols * 4);
+  float sa[PER];
+  v4f sw[PER];
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int f = w + q * kFewWaves, n = f / MF * 16 + lane / 16 * 4, m = f % MF * 16 + lane % 16;
+    sa[q] = p.as[pc.row0 + min(m, pc.rows - 1)];
+    sw[q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(bs, n * 4, 0, 0));
+  }
+  v4i acc[NF][MF];
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) acc[i][j] = v4i{};
+#pragma unroll
+  for (int s = 0; s < S; ++s) issue(begin + s, s);
+  const uint8_t* mine = ring + lane % 16 * 64 + ((lane / 16) ^ (lane / 4 % 4)) * 16;
+  int slot = 0;
+  for (int s = begin; s < end; ++s) {
+    wait_vmcnt<(S - 1) * LOADS>();
+    __builtin_amdgcn_sched_barrier(0);
+    v4i wf[NF], af[MF];
+#pragma unroll
+    for (int i = 0; i < NF; ++i) wf[i] = *reinterpret_cast<const v4i*>(mine + slot * SLOT + i * 1024);
+#pragma unroll
+    for (int j = 0; j < MF; ++j) af[j] = *reinterpret_cast<const v4i*>(mine + slot * SLOT + (NF + j) * 1024);
+    wait_lds();
+    __builtin_amdgcn_sched_barrier(0);
+    issue(s + S, slot);
+    slot = slot + 1 == S ? 0 : slot + 1;
+#pragma unroll
+    for (int i = 0; i < NF; ++i)
+#pragma unroll
+      for (int j = 0; j < MF; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i], af[j], acc[i][j], 0, 0, 0);
+  }
+  wait_vmcnt<0>();                                       // zeros still on their way to the ring
+  const auto sums_of = [&](int v) { return reinterpret_cast<v4i*>(smem + v * (S * SLOT)) + lane; };
+#pragma unroll
+  for (int i = 0; i < NF; ++i)
+#pragma unroll
+    for (int j = 0; j < MF; ++j) sums_of(w)[(i * MF + j) * 64] = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int q = 0; q < PER; ++q) {
+    const int f = w + q * kFewWaves;
+    if (f >= NF * MF) break;
+    v4i sum = sums_of(0)[f * 64];
+#pragma unroll
+    for (int v = 1; v < kFewWaves; ++v) sum += sums_of(v)[f * 64];
+    const int n = f / MF * 16 + lane / 16 * 4, m = f % MF * 16 + lane % 16, left = cols - n;
+    if (m >= pc.rows) continue;
+    float o[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[c] = (float)sum[c] * sa[q] * sw[q][c];
+    uint16_t* out = p.out + (int64_t)(pc.row0 + m) * p.n + col0 + n;
+    const uint32_t d[2] = {bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
+    if (left >= 4) memcpy(out, d, 8);
+    else if (left > 0) store_some(out, d[0], d[1], 0, 0, left);
+  }
+}
+
+template <int NF, int MF>
+hipError_t few_int8(const Int8Params& p, int pieces, hipStream_t st) {
+  const hipError_t e = ensure_dynamic_lds((const void*)few_int8_kernel<NF, MF>, few_lds(NF, MF), st);
+  if (e != hipSuccess) return e;
+  const dim3 grid((uint32_t)((p.n + 16 * NF - 1) / (16 * NF)), (uint32_t)pieces);
+  few_int8_kernel<NF, MF><<<grid, kFewWaves * 64, few_lds(NF, MF), st>>>(p);
+  return hipGetLastError();
+}
+
+template <int FN, int FM, int SLOTS>
+hipError_t tile_int8(const Int8Params& p, int num_cus, hipStream_t st) {
+  using T = Int8Tile<FN, FM, SLOTS>;
+  const hipError_t e = ensure_dynamic_lds((const void*)grouped_int8_kernel<FN, FM, SLOTS>, T::SMEM, st);
+  if (e != hipSuccess) return e;
+  int64_t tiles = 0;
+  for (int g = 0; g < p.sp.G; ++g) tiles += (p.sp.m[g] + T::TM - 1) / T::TM;
+  tiles *= (p.n + T::TN - 1) / T::TN;
+  grouped_int8_kernel<FN, FM, SLOTS><<<(uint32_t)(tiles < num_cus ? tiles : num_cus), kThreads, T::SMEM, st>>>(p);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -382,14 +591,33 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int6
 }
 
 hipError_t launch_grouped_int8(const Int8Params& p, int num_cus, hipStream_t st) {
-  const hipError_t e = ensure_dynamic_lds((const void*)grouped_int8_kernel, kSlots * kStage, st);
-  if (e != hipSuccess) return e;
-  int64_t tiles = 0;
-  for (int g = 0; g < p.sp.G; ++g) tiles += (p.sp.m[g] + kTile - 1) / kTile;
-  tiles *= (p.n + kTile - 1) / kTile;
-  const uint32_t grid = (uint32_t)(tiles < num_cus ? tiles : num_cus);
-  grouped_int8_kernel<<<grid, kThreads, kSlots * kStage, st>>>(p);
-  return hipGetLastError();
+  int most = 0;
+  for (int g = 0; g < p.sp.G; ++g) most = p.sp.m[g] > most ? p.sp.m[g] : most;
+  const char* form = getenv("FORM");
+  if (form && form[0] == 'b') return tile_int8<4, 2, 4>(p, num_cus, st);
+  if (form && form[0] == 'm') return tile_int8<4, 1, 5>(p, num_cus, st);
+  if (form && form[0] == 's') return tile_int8<2, 1, 8>(p, num_cus, st);
+  if (most <= 64 || form) {
+    int mf = most <= 16 ? 1 : most <= 32 ? 2 : 4;
+    if (form) mf = form[2] - '0';
+    int pieces = 0;
+    for (int g = 0; g < p.sp.G; ++g) pieces += (p.sp.m[g] + 16 * mf - 1) / (16 * mf);
+    int nf = mf == 1 ? 2 : 4;
+    if (form) nf = form[1] - '0';
+    else while (nf > 1 && (p.n + 16 * nf - 1) / (16 * nf) * pieces < num_cus) nf /= 2;
+    switch (mf * 10 + nf) {
+      case 11: return few_int8<1, 1>(p, pieces, st);
+      case 12: return few_int8<2, 1>(p, pieces, st);
+      case 14: return few_int8<4, 1>(p, pieces, st);
+      case 21: return few_int8<1, 2>(p, pieces, st);
+      case 22: return few_int8<2, 2>(p, pieces, st);
+      case 24: return few_int8<4, 2>(p, pieces, st);
+      case 41: return few_int8<1, 4>(p, pieces, st);
+      case 42: return few_int8<2, 4>(p, pieces, st);
+      default: return few_int8<4, 4>(p, pieces, st);
+    }
+  }
+  return tile_int8<4, 2, 4>(p, num_cus, st);
 }
 
 }  // namespace mxgg
