@@ -13,7 +13,7 @@
 namespace mxgg {
 namespace {
 
-typedef int v16i __attribute__((ext_vector_type(16)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 
 // ---------------------------------------------------------------------------
 // Quantizer
@@ -174,17 +174,17 @@ constexpr int kStageK = 64;           // codes of a row in a stage
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kTileGroup = 4;
 
-// FN fragments of 32 channels and FM of 32 tokens for each of 2 x 4 waves
+// FN fragments of 16 channels and FM of 16 tokens for each of 2 x 4 waves
 template <int FN, int FM, int SLOTS>
 struct Int8Tile {
-  static constexpr int TN = 64 * FN, TM = 128 * FM, WN = 32 * FN, WM = 32 * FM;
+  static constexpr int TN = 32 * FN, TM = 64 * FM, WN = 16 * FN, WM = 16 * FM;
   static constexpr int W_BYTES = TN * kStageK, STAGE = (TN + TM) * kStageK, LDS = SLOTS * STAGE;
   // a wave's way out: 16 tokens of 64 channels, rows 16 bytes apart more
-  static constexpr int OUT_PITCH = 144, OUT_BYTES = 16 * OUT_PITCH, STORES = FM * FN * 2;
+  static constexpr int OUT_PITCH = 144, OUT_BYTES = 16 * OUT_PITCH, STORES = FM * FN / 2;
   static constexpr int SMEM = LDS + kWaves * OUT_BYTES;
   // 1 KiB loads of a wave and stage
   static constexpr int LW = W_BYTES / (kWaves * 1024), LA = TM * kStageK / (kWaves * 1024);
-  static_assert(SMEM <= 154 * 1024 && LW >= 1 && LA >= 1 && FN % 2 == 0, "LDS: the ring beside the tables; whole loads");
+  static_assert(SMEM <= 154 * 1024 && LW >= 1 && LA >= 1 && FN % 4 == 0, "LDS: the ring beside the tables; whole loads");
 };
 
 struct Tile {
@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
   }
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4, h = lane >> 5, l32 = lane & 31;
+  const int turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4, h = lane / 16, l16 = lane % 16;
   const int K = p.k, total = __builtin_amdgcn_readfirstlane(offs[G]), stages = (K + kStageK - 1) / kStageK;
   const int nb = gridDim.x, b = blockIdx.x;
   // neighbouring tiles on one XCD (workgroups are dealt round the 8 of them):
@@ -295,30 +295,25 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
   raw_barrier();
   if (turn) raw_barrier();                                // the second four waves are one turn behind
   int slot = 0;
-  // a lane's pieces: codes 16 (2u + h) .. of row l32 of a fragment
-  const int piece0 = l32 * kStageK + (h ^ ((l32 >> 2) & 3)) * 16, piece1 = piece0 ^ 32;
-  const int at_w = wn * T::WN * kStageK, at_a = T::W_BYTES + wm * T::WM * kStageK;
+  // a lane's piece of a fragment of 16 rows: codes 16 (lane / 16) .. of row lane % 16
+  const int piece = l16 * kStageK + (h ^ (l16 / 4)) * 16;
+  const int at_w = wn * T::WN * kStageK + piece, at_a = T::W_BYTES + wm * T::WM * kStageK + piece;
   for (int t = first; t < total; t += nb) {
     const Tile cur = find(t);
     const bool busy = wn * T::WN < cur.cols && wm * T::WM < cur.rows;   // else nothing of the wave's is stored
-    v16i acc[FN][FM];
+    v4i acc[FN][FM];
 #pragma unroll
     for (int i = 0; i < FN; ++i)
 #pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = v16i{};
+      for (int j = 0; j < FM; ++j) acc[i][j] = v4i{};
     for (int s = 0; s < stages; ++s) {
-      v4i wf[2][FN], af[2][FM];
+      v4i wf[FN], af[FM];
       if (busy) {
         const uint8_t* st = smem + slot * T::STAGE;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint8_t* pw = st + at_w + (u ? piece1 : piece0);
-          const uint8_t* pa = st + at_a + (u ? piece1 : piece0);
+        for (int i = 0; i < FN; ++i) wf[i] = *reinterpret_cast<const v4i*>(st + at_w + i * 16 * kStageK);
 #pragma unroll
-          for (int i = 0; i < FN; ++i) wf[u][i] = *reinterpret_cast<const v4i*>(pw + i * 32 * kStageK);
-#pragma unroll
-          for (int j = 0; j < FM; ++j) af[u][j] = *reinterpret_cast<const v4i*>(pa + j * 32 * kStageK);
-        }
+        for (int j = 0; j < FM; ++j) af[j] = *reinterpret_cast<const v4i*>(st + at_a + j * 16 * kStageK);
       }
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
       issue();
@@ -329,84 +324,52 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
       if (busy) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int i = 0; i < FN; ++i)
 #pragma unroll
-          for (int i = 0; i < FN; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wf[u][i], af[u][j], acc[i][j], 0, 0, 0);
+          for (int j = 0; j < FM; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i], af[j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
       }
       if (!turn) wait_vmcnt<kAhead>();
       raw_barrier();
     }
-    // Epilogue: a lane has channels 8q + 4h .. +3 of token l32 in registers 4q ..
-    // 4q + 3. The two halves of a wave exchange every other group, so that each
-    // lane has eight neighbouring channels; 16 tokens of 64 channels go through LDS
-    // and leave as whole lines.
+    // Epilogue: 16 tokens of 64 channels go through LDS and leave as whole lines.
     if (!busy) continue;
     const __amdgpu_buffer_rsrc_t scales =
         uniform_buffer(p.ws + (int64_t)cur.g * p.n + cur.col0, (uint32_t)cur.cols * 4);
     float sa[FM];
 #pragma unroll
-    for (int j = 0; j < FM; ++j) sa[j] = p.as[cur.row0 + min(wm * T::WM + j * 32 + l32, cur.rows - 1)];
+    for (int j = 0; j < FM; ++j) sa[j] = p.as[cur.row0 + min(wm * T::WM + j * 16 + l16, cur.rows - 1)];
     uint8_t* scr = smem + T::LDS + w * T::OUT_BYTES;
     const int m_out = wm * T::WM + lane / 8, n_out = wn * T::WN + lane % 8 * 8;
     uint16_t* out = p.out + (int64_t)(cur.row0 + m_out) * p.n + cur.col0 + n_out;
 #pragma unroll
-    for (int c = 0; c < FN / 2; ++c) {
-      v4f sw[2][4];
+    for (int c = 0; c < FN / 4; ++c) {
+      v4f sw[4];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          sw[i][q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(
-                                                 scales, (wn * T::WN + c * 64 + i * 32 + 8 * q + 4 * h) * 4, 0, 0));
+      for (int i = 0; i < 4; ++i)
+        sw[i] = __builtin_bit_cast(
+            v4f, __builtin_amdgcn_raw_buffer_load_b128(scales, (wn * T::WN + c * 64 + i * 16 + 4 * h) * 4, 0, 0));
 #pragma unroll
       for (int j = 0; j < FM; ++j) {
-        uint32_t d[2][2][4];                              // 16 channels of each fragment and pair of groups
+        wave_fence();
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 4; ++i) {
+          float o[4];
 #pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            uint32_t v[4];
+          for (int r = 0; r < 4; ++r) o[r] = (float)acc[4 * c + i][j][r] * sa[j] * sw[i][r];
+          *reinterpret_cast<v2i*>(scr + l16 * T::OUT_PITCH + (i * 16 + 4 * h) * 2) =
+              v2i{(int)bf16_pair(o[0], o[1]), (int)bf16_pair(o[2], o[3])};
+        }
+        wave_fence();
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float o[4];
-#pragma unroll
-              for (int r = 0; r < 4; ++r) o[r] = (float)acc[2 * c + i][j][4 * (q + e) + r] * sa[j] * sw[i][q + e][r];
-              v[2 * e] = bf16_pair(o[0], o[1]);
-              v[2 * e + 1] = bf16_pair(o[2], o[3]);
-            }
-            // lower half: group q of both halves; upper half: group q + 1
-            const auto lo = __builtin_amdgcn_permlane32_swap(v[0], v[2], false, false);
-            const auto hi = __builtin_amdgcn_permlane32_swap(v[1], v[3], false, false);
-            d[i][q / 2][0] = lo[0];
-            d[i][q / 2][1] = hi[0];
-            d[i][q / 2][2] = lo[1];
-            d[i][q / 2][3] = hi[1];
-          }
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          wave_fence();
-          if (l32 / 16 == t) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-#pragma unroll
-              for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<v4i*>(scr + l32 % 16 * T::OUT_PITCH + (i * 32 + 8 * (2 * q + h)) * 2) =
-                    v4i{(int)d[i][q][0], (int)d[i][q][1], (int)d[i][q][2], (int)d[i][q][3]};
-          }
-          wave_fence();
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const v4i o = *reinterpret_cast<const v4i*>(scr + (lane / 8 + 8 * k) * T::OUT_PITCH + lane % 8 * 16);
-            const int down = j * 32 + t * 16 + k * 8, left = cur.cols - n_out - c * 64;
-            uint16_t* to = out + (int64_t)down * p.n + c * 64;
-            if (m_out + down < cur.rows) {
-              if (left >= 8) memcpy(to, &o, 16);
-              else if (left > 0) store_some(to, o[0], o[1], o[2], o[3], left);
-            }
+        for (int k = 0; k < 2; ++k) {
+          const v4i o = *reinterpret_cast<const v4i*>(scr + (lane / 8 + 8 * k) * T::OUT_PITCH + lane % 8 * 16);
+          const int down = j * 16 + k * 8, left = cur.cols - n_out - c * 64;
+          uint16_t* to = out + (int64_t)down * p.n + c * 64;
+          if (m_out + down < cur.rows) {
+            if (left >= 8) memcpy(to, &o, 16);
+            else if (left > 0) store_some(to, o[0], o[1], o[2], o[3], left);
           }
         }
       }
@@ -594,9 +557,9 @@ hipError_t launch_grouped_int8(const Int8Params& p, int num_cus, hipStream_t st)
   int most = 0;
   for (int g = 0; g < p.sp.G; ++g) most = p.sp.m[g] > most ? p.sp.m[g] : most;
   const char* form = getenv("FORM");
-  if (form && form[0] == 'b') return tile_int8<4, 2, 4>(p, num_cus, st);
-  if (form && form[0] == 'm') return tile_int8<4, 1, 5>(p, num_cus, st);
-  if (form && form[0] == 's') return tile_int8<2, 1, 8>(p, num_cus, st);
+  if (form && form[0] == 'b') return tile_int8<8, 4, 4>(p, num_cus, st);
+  if (form && form[0] == 'm') return tile_int8<8, 2, 5>(p, num_cus, st);
+  if (form && form[0] == 's') return tile_int8<4, 2, 8>(p, num_cus, st);
   if (most <= 64 || form) {
     int mf = most <= 16 ? 1 : most <= 32 ? 2 : 4;
     if (form) mf = form[2] - '0';
@@ -617,7 +580,7 @@ hipError_t launch_grouped_int8(const Int8Params& p, int num_cus, hipStream_t st)
       default: return few_int8<4, 4>(p, pieces, st);
     }
   }
-  return tile_int8<4, 2, 4>(p, num_cus, st);
+  return tile_int8<8, 4, 4>(p, num_cus, st);
 }
 
 }  // namespace mxgg
