@@ -170,20 +170,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void* bas
 }
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's end
 
-constexpr int kStageK = 64;           // codes of a row in a stage
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kTileGroup = 4;
 
-// FN fragments of 16 channels and FM of 16 tokens for each of 2 x 4 waves
-template <int FN, int FM, int SLOTS>
+// FN fragments of 16 channels and FM of 16 tokens for each of 2 x 4 waves; 64 KU
+// codes of a row in a stage
+template <int FN, int FM, int KU, int SLOTS>
 struct Int8Tile {
+  static constexpr int K = 64 * KU, CHUNKS = 4 * KU;
   static constexpr int TN = 32 * FN, TM = 64 * FM, WN = 16 * FN, WM = 16 * FM;
-  static constexpr int W_BYTES = TN * kStageK, STAGE = (TN + TM) * kStageK, LDS = SLOTS * STAGE;
+  static constexpr int W_BYTES = TN * K, STAGE = (TN + TM) * K, LDS = SLOTS * STAGE;
   // a wave's way out: 16 tokens of 64 channels, rows 16 bytes apart more
   static constexpr int OUT_PITCH = 144, OUT_BYTES = 16 * OUT_PITCH, STORES = FM * FN / 2;
   static constexpr int SMEM = LDS + kWaves * OUT_BYTES;
   // 1 KiB loads of a wave and stage
-  static constexpr int LW = W_BYTES / (kWaves * 1024), LA = TM * kStageK / (kWaves * 1024);
+  static constexpr int LW = W_BYTES / (kWaves * 1024), LA = TM * K / (kWaves * 1024);
+  // rows of a load, and of a load of all waves
+  static constexpr int LOAD_ROWS = 16 / KU, ROUND_ROWS = kWaves * LOAD_ROWS;
   static_assert(SMEM <= 154 * 1024 && LW >= 1 && LA >= 1 && FN % 4 == 0, "LDS: the ring beside the tables; whole loads");
 };
 
@@ -203,9 +206,9 @@ __device__ __forceinline__ void store_some(uint16_t* out, uint32_t d0, uint32_t 
   if (left & 1) out[left & 6] = (uint16_t)(left & 2 ? b : a);
 }
 
-template <int FN, int FM, int SLOTS>
+template <int FN, int FM, int KU, int SLOTS>
 __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Params p) {
-  using T = Int8Tile<FN, FM, SLOTS>;
+  using T = Int8Tile<FN, FM, KU, SLOTS>;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int32_t pref[kMaxExperts + 1], offs[kMaxExperts + 1];   // an expert's first row, and first tile
   const int G = p.sp.G, nt = (int)((p.n + T::TN - 1) / T::TN);
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
 
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4, h = lane / 16, l16 = lane % 16;
-  const int K = p.k, total = __builtin_amdgcn_readfirstlane(offs[G]), stages = (K + kStageK - 1) / kStageK;
+  const int K = p.k, total = __builtin_amdgcn_readfirstlane(offs[G]), stages = (K + T::K - 1) / T::K;
   const int nb = gridDim.x, b = blockIdx.x;
   // neighbouring tiles on one XCD (workgroups are dealt round the 8 of them):
   // they share operands in its L2
@@ -242,11 +245,12 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
     return o;
   };
 
-  // Issuing side. A load brings 16 rows; chunk c of row r lies at c ^ (r/4 % 4)
-  // of the row's four: the fragments' reads are then without bank conflicts.
-  const int lr = w * 16 + lane / 4, lc = (lane % 4) ^ (lane / 16);
+  // Issuing side. Chunk c of a row lies at c ^ swizzle(row): the 16 rows of a
+  // fragment's read are then spread over all banks.
+  const auto swizzle = [](int row) { return KU == 1 ? row / 4 % 4 : row / 2 % 8; };
+  const int lr = w * T::LOAD_ROWS + lane / T::CHUNKS, lc = (lane % T::CHUNKS) ^ swizzle(lr);
   const uint32_t lane_off = (uint32_t)(lr * K + lc * 16);
-  const int last_k = K - (stages - 1) * kStageK;          // codes of the last stage
+  const int last_k = K - (stages - 1) * T::K;             // codes of the last stage
   const bool lane_in_last = lc * 16 < last_k;
   int it = first, is = 0, slot_issue = 0;
   const uint8_t *base_w = p.w, *base_a = p.a;
@@ -264,16 +268,16 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
     uint8_t* at = smem + slot_issue * T::STAGE + w * 1024;
     const __amdgpu_buffer_rsrc_t bw = uniform_buffer(base_w, size_w), ba = uniform_buffer(base_a, size_a);
     // zeros behind the contraction's end, of the tokens (the weights may be anything)
-    const uint32_t wo = lane_off + (uint32_t)(is * kStageK);
+    const uint32_t wo = lane_off + (uint32_t)(is * T::K);
     const uint32_t ao = is + 1 < stages || lane_in_last ? wo : kOutside;
 #pragma unroll
     for (int i = 0; i < T::LW; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, (MXGG_LDS void*)(at + i * (kWaves * 1024)), 16,
-                                               wo + (uint32_t)(i * 128 * K), 0, 0, 0);
+                                               wo + (uint32_t)(i * T::ROUND_ROWS * K), 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < T::LA; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ba, (MXGG_LDS void*)(at + T::W_BYTES + i * (kWaves * 1024)), 16,
-                                               ao + (uint32_t)(i * 128 * K), 0, 0, 0);
+                                               ao + (uint32_t)(i * T::ROUND_ROWS * K), 0, 0, 0);
   };
   const auto advance = [&]() {
     slot_issue = slot_issue + 1 == SLOTS ? 0 : slot_issue + 1;
@@ -295,9 +299,14 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
   raw_barrier();
   if (turn) raw_barrier();                                // the second four waves are one turn behind
   int slot = 0;
-  // a lane's piece of a fragment of 16 rows: codes 16 (lane / 16) .. of row lane % 16
-  const int piece = l16 * kStageK + (h ^ (l16 / 4)) * 16;
-  const int at_w = wn * T::WN * kStageK + piece, at_a = T::W_BYTES + wm * T::WM * kStageK + piece;
+  // a lane's piece u of a fragment of 16 rows: codes 64 u + 16 (lane / 16) .. of row lane % 16
+  int at_w[KU], at_a[KU];
+#pragma unroll
+  for (int u = 0; u < KU; ++u) {
+    const int piece = l16 * T::K + ((4 * u + h) ^ swizzle(l16)) * 16;
+    at_w[u] = wn * T::WN * T::K + piece;
+    at_a[u] = T::W_BYTES + wm * T::WM * T::K + piece;
+  }
   for (int t = first; t < total; t += nb) {
     const Tile cur = find(t);
     const bool busy = wn * T::WN < cur.cols && wm * T::WM < cur.rows;   // else nothing of the wave's is stored
@@ -307,13 +316,16 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
 #pragma unroll
       for (int j = 0; j < FM; ++j) acc[i][j] = v4i{};
     for (int s = 0; s < stages; ++s) {
-      v4i wf[FN], af[FM];
+      v4i wf[KU][FN], af[KU][FM];
       if (busy) {
         const uint8_t* st = smem + slot * T::STAGE;
 #pragma unroll
-        for (int i = 0; i < FN; ++i) wf[i] = *reinterpret_cast<const v4i*>(st + at_w + i * 16 * kStageK);
+        for (int u = 0; u < KU; ++u) {
 #pragma unroll
-        for (int j = 0; j < FM; ++j) af[j] = *reinterpret_cast<const v4i*>(st + at_a + j * 16 * kStageK);
+          for (int i = 0; i < FN; ++i) wf[u][i] = *reinterpret_cast<const v4i*>(st + at_w[u] + i * 16 * T::K);
+#pragma unroll
+          for (int j = 0; j < FM; ++j) af[u][j] = *reinterpret_cast<const v4i*>(st + at_a[u] + j * 16 * T::K);
+        }
       }
       slot = slot + 1 == SLOTS ? 0 : slot + 1;
       issue();
@@ -324,10 +336,12 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
       if (busy) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 0; i < FN; ++i)
+        for (int u = 0; u < KU; ++u)
 #pragma unroll
-          for (int j = 0; j < FM; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[i], af[j], acc[i][j], 0, 0, 0);
+          for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[u][i], af[u][j], acc[i][j], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
       }
       if (!turn) wait_vmcnt<kAhead>();
@@ -521,23 +535,21 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_int8_kernel(const Int8Para
 }
 
 template <int NF, int MF>
-hipError_t few_int8(const Int8Params& p, int pieces, hipStream_t st) {
+hipError_t few_int8(const Int8Params& p, hipStream_t st) {
   const hipError_t e = ensure_dynamic_lds((const void*)few_int8_kernel<NF, MF>, few_lds(NF, MF), st);
   if (e != hipSuccess) return e;
-  const dim3 grid((uint32_t)((p.n + 16 * NF - 1) / (16 * NF)), (uint32_t)pieces);
+  const dim3 grid((uint32_t)((p.n + 16 * NF - 1) / (16 * NF)), (uint32_t)int8_pieces(p.sp, 16 * MF));
   few_int8_kernel<NF, MF><<<grid, kFewWaves * 64, few_lds(NF, MF), st>>>(p);
   return hipGetLastError();
 }
 
-template <int FN, int FM, int SLOTS>
+template <int FN, int FM, int KU, int SLOTS>
 hipError_t tile_int8(const Int8Params& p, int num_cus, hipStream_t st) {
-  using T = Int8Tile<FN, FM, SLOTS>;
-  const hipError_t e = ensure_dynamic_lds((const void*)grouped_int8_kernel<FN, FM, SLOTS>, T::SMEM, st);
+  using T = Int8Tile<FN, FM, KU, SLOTS>;
+  const hipError_t e = ensure_dynamic_lds((const void*)grouped_int8_kernel<FN, FM, KU, SLOTS>, T::SMEM, st);
   if (e != hipSuccess) return e;
-  int64_t tiles = 0;
-  for (int g = 0; g < p.sp.G; ++g) tiles += (p.sp.m[g] + T::TM - 1) / T::TM;
-  tiles *= (p.n + T::TN - 1) / T::TN;
-  grouped_int8_kernel<FN, FM, SLOTS><<<(uint32_t)(tiles < num_cus ? tiles : num_cus), kThreads, T::SMEM, st>>>(p);
+  const int64_t tiles = int8_pieces(p.sp, T::TM) * ((p.n + T::TN - 1) / T::TN);
+  grouped_int8_kernel<FN, FM, KU, SLOTS><<<(uint32_t)(tiles < num_cus ? tiles : num_cus), kThreads, T::SMEM, st>>>(p);
   return hipGetLastError();
 }
 
@@ -554,33 +566,18 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int6
 }
 
 hipError_t launch_grouped_int8(const Int8Params& p, int num_cus, hipStream_t st) {
-  int most = 0;
-  for (int g = 0; g < p.sp.G; ++g) most = p.sp.m[g] > most ? p.sp.m[g] : most;
-  const char* form = getenv("FORM");
-  if (form && form[0] == 'b') return tile_int8<8, 4, 4>(p, num_cus, st);
-  if (form && form[0] == 'm') return tile_int8<8, 2, 5>(p, num_cus, st);
-  if (form && form[0] == 's') return tile_int8<4, 2, 8>(p, num_cus, st);
-  if (most <= 64 || form) {
-    int mf = most <= 16 ? 1 : most <= 32 ? 2 : 4;
-    if (form) mf = form[2] - '0';
-    int pieces = 0;
-    for (int g = 0; g < p.sp.G; ++g) pieces += (p.sp.m[g] + 16 * mf - 1) / (16 * mf);
-    int nf = mf == 1 ? 2 : 4;
-    if (form) nf = form[1] - '0';
-    else while (nf > 1 && (p.n + 16 * nf - 1) / (16 * nf) * pieces < num_cus) nf /= 2;
-    switch (mf * 10 + nf) {
-      case 11: return few_int8<1, 1>(p, pieces, st);
-      case 12: return few_int8<2, 1>(p, pieces, st);
-      case 14: return few_int8<4, 1>(p, pieces, st);
-      case 21: return few_int8<1, 2>(p, pieces, st);
-      case 22: return few_int8<2, 2>(p, pieces, st);
-      case 24: return few_int8<4, 2>(p, pieces, st);
-      case 41: return few_int8<1, 4>(p, pieces, st);
-      case 42: return few_int8<2, 4>(p, pieces, st);
-      default: return few_int8<4, 4>(p, pieces, st);
-    }
+  switch (int8_form(p.sp, p.n, p.k, num_cus)) {
+    case kInt8Big: return tile_int8<8, 4, 1, 4>(p, num_cus, st);
+    case kInt8Small: return tile_int8<4, 2, 2, 4>(p, num_cus, st);
+    case kInt8Few11: return few_int8<1, 1>(p, st);
+    case kInt8Few12: return few_int8<1, 2>(p, st);
+    case kInt8Few21: return few_int8<2, 1>(p, st);
+    case kInt8Few22: return few_int8<2, 2>(p, st);
+    case kInt8Few24: return few_int8<2, 4>(p, st);
+    case kInt8Few42: return few_int8<4, 2>(p, st);
+    case kInt8Few44: return few_int8<4, 4>(p, st);
   }
-  return tile_int8<8, 4, 4>(p, num_cus, st);
+  return hipErrorInvalidValue;
 }
 
 }  // namespace mxgg

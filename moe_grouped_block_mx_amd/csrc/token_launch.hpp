@@ -78,6 +78,69 @@ struct Int8Params {
   int32_t k;
   SplitArgs sp;
 };
+// Pieces of at most `each` tokens of one expert
+inline int64_t int8_pieces(const SplitArgs& sp, int each) {
+  int64_t n = 0;
+  for (int g = 0; g < sp.G; ++g) n += ((int64_t)sp.m[g] + each - 1) / each;
+  return n;
+}
+// The forms of the product: tiles of 256 channels x 256 tokens, of 128 x 128, and
+// for few tokens 16 i channels x 16 j tokens (kInt8Few<i><j>) with the
+// contraction split over a workgroup's waves.
+enum Int8Form { kInt8Big, kInt8Small, kInt8Few11, kInt8Few12, kInt8Few21, kInt8Few22, kInt8Few24, kInt8Few42, kInt8Few44 };
+// Every form's time is its rounds of one workgroup a CU, times what one takes: a
+// part that grows with K, in units of 16 rows of codes brought to a CU (at K = 4096
+// 1.5 us), and one that does not (start, results, the wait for the first loads),
+// which is less where two workgroups fit on a CU. The forms of few tokens bring the
+// rows of their channels and tokens; a 128 x 128 tile's loads overlap more (12.3
+// units for 16), a 256 x 256 tile's time is its MFMAs'.
+// Measured, us (one expert unless said; tokens, channels, K):
+//                                   256    128    64 x 64   32 x 32
+//   64, 4096, 4096                   51     25      16        10
+//   256, 4096, 4096                  58     25      16        27
+//   512, 4096, 4096                  56     25      29        50
+//   512, 1111, 2000                  35     16      10        16
+//   1024, 1024, 8192                 82     37      23
+//   1024, 8192, 1024                 23     20      39
+//   2048, 4096, 4096                 56     45      92
+//   2048, 8192, 1024                 25     34      77
+//   4096, 4096, 4096                 65     83     179
+//   1024 of 32 experts, 4096, 4096  138    125     144
+//   4096 of 32                      187    152     266
+//   8192 of 32                      203    225     446
+//   8192 of 64, 4096, 7168          504    476     844
+//   16384 of 64                     620    739
+// and for the fewest tokens, 16 x 16, 32 x 16 (channels x tokens):
+//   1, 4096, 7168                   7.9   11.3
+//   1, 8192, 1024                   4.4    4.1
+//   64 of 128 experts, 2048, 7168   142    134
+//   256 of 32, 4096, 4096           126    105
+inline Int8Form int8_form(const SplitArgs& sp, int64_t n, int64_t k, int num_cus) {
+  struct Option {
+    Int8Form form;
+    int channels, tokens;
+    float units, fixed;   // units 0: the rows that a workgroup brings
+  };
+  static constexpr Option options[] = {
+      {kInt8Big, 256, 256, 29.f, 8.f},     {kInt8Small, 128, 128, 12.3f, 2.3f}, {kInt8Few11, 16, 16, 0, 0.5f},
+      {kInt8Few21, 32, 16, 0, 0.5f},       {kInt8Few12, 16, 32, 0, 0.5f},       {kInt8Few22, 32, 32, 0, 1.3f},
+      {kInt8Few24, 32, 64, 0, 1.3f},       {kInt8Few42, 64, 32, 0, 1.3f},       {kInt8Few44, 64, 64, 0, 1.3f}};
+  int64_t rows = 0;
+  for (int g = 0; g < sp.G; ++g) rows += sp.m[g];
+  Int8Form best = kInt8Big;
+  float least = 0;
+  for (const Option& o : options) {
+    const int64_t pieces = int8_pieces(sp, o.tokens), groups = pieces * ((n + o.channels - 1) / o.channels);
+    if (o.units == 0 && pieces > 65535) continue;      // the grid's y axis
+    const float units = o.units > 0 ? o.units : (float)o.channels / 16 + (float)rows / (float)pieces / 16;
+    const float cost = (float)((groups + num_cus - 1) / num_cus) * (units + o.fixed * 4096 / (float)k);
+    if (o.form == kInt8Big || cost < least) {
+      least = cost;
+      best = o.form;
+    }
+  }
+  return best;
+}
 hipError_t launch_grouped_int8(const Int8Params& p, int num_cus, hipStream_t st);
 
 }  // namespace mxgg

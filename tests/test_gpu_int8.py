@@ -90,9 +90,32 @@ def check(splits, N, K, seed=0):
     ([1], 1, 16), ([1], 64, 64), ([3], 33, 48), ([16], 16, 128), ([17], 257, 144), ([64], 256, 256), ([65], 100, 272),
     ([1, 0, 2], 48, 64), ([0, 0, 5, 0], 130, 1040), ([31, 33, 0, 1], 96, 512), ([255, 256, 257], 255, 112),
     ([300, 0, 7], 515, 400), ([1] * 40, 72, 192), ([2000], 1111, 2000), ([513, 1, 700], 520, 4096),
-    ([128, 129, 60], 1, 64), ([1], 4096, 7168), ([8], 2048, 8208), ([48, 3, 64], 264, 4112)])
+    ([128, 129, 60], 1, 64), ([1], 4096, 7168), ([8], 2048, 8208), ([48, 3, 64], 264, 4112),
+    # one shape at least for every form of the kernel: few tokens ...
+    ([1], 4100, 160), ([3, 1], 9000, 96), ([30], 1500, 2064), ([64], 4096, 272), ([40], 8200, 80), ([60, 50], 5000, 144),
+    ([250], 4100, 96), ([33] * 9, 1030, 592), ([16], 16000, 4096), ([48], 4100, 4096), ([24], 4099, 4096), ([60], 4095, 2000),
+    # ... 128 x 128 tiles, and 256 x 256, with rounds of both
+    ([1024], 4096, 144), ([700, 0, 1300, 77], 3001, 272), ([100] * 20, 2000, 64), ([4096], 4096, 144),
+    ([1300, 0, 2900, 77], 4004, 208), ([257] * 12, 4099, 80), ([9000], 2050, 336)])
 def test_product(splits, N, K):
     check(splits, N, K)
+
+
+OPTIONS = [(256, 256, 29, 8), (128, 128, 12.3, 2.3), (16, 16, 0, .5), (32, 16, 0, .5), (16, 32, 0, .5), (32, 32, 0, 1.3),
+           (32, 64, 0, 1.3), (64, 32, 0, 1.3), (64, 64, 0, 1.3)]
+
+
+def form(splits, N, K):
+    """int8_form restated: the least of rounds times what a workgroup takes."""
+    def cost(o):
+        pieces = sum(-(-m // o[1]) for m in splits)
+        return -(-pieces * -(-N // o[0]) // 256) * ((o[2] or o[0] / 16 + sum(splits) / pieces / 16) + o[3] * 4096 / K)
+    return min(OPTIONS, key=cost)[:2]
+
+
+def test_every_form_is_chosen():
+    marks = [m for m in test_product.pytestmark if m.name == "parametrize"][0].args[1]
+    assert {form(*m) for m in marks} == {o[:2] for o in OPTIONS}
 
 
 def test_many_experts():
