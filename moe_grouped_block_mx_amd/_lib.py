@@ -317,6 +317,8 @@ def mxgg_quantize_rowwise(x, fmt="mxfp4", flags=None, q=None, scales=None):
     channel)."""
     torch = _torch()
     f = _fmt(fmt)
+    if f == INT8:
+        return _quantize_int8(x, flags, q, scales)
     flags = _flags(flags, f)
     rows, cols = x.shape
     _check_bf16_2d(x)
@@ -389,8 +391,10 @@ def mxgg_quantize_dual(x, m_splits, fmt="mxfp4", flags=None, q_row=None, s_row=N
 def mxgg_grouped_fwd(a_q, a_s, w_q, w_s, m_splits, N, K, a_fmt="mxfp4", w_fmt="mxfp4", out=None, ws=None):
     """out[M, N] (bf16) = per-expert A . W_g^T; W packed [G*N, ...]."""
     torch = _torch()
-    arr, G = _splits(m_splits)
     af, wf = _fmt(a_fmt), _fmt(w_fmt)
+    if af == wf == INT8:
+        return _grouped_fwd_int8(a_q, a_s, w_q, w_s, m_splits, N, K, out, ws)
+    arr, G = _splits(m_splits)
     M = _q_rows(a_q, af)
     _expect(a_q, "a_q", _q_shape(af, M, K), _qdtype(af))
     _expect(a_s, "a_s", _row_scale_shape(af, M, K), _sdtype(af))
@@ -471,6 +475,7 @@ def mxgg_grouped_wgrad(dycol_q, dycol_s, xcol_q, xcol_s, m_splits, N, K, mpad, m
 # few microseconds: their bindings pass addresses as plain ints and look a
 # caller's buffer over only where one was given.
 _f32_t, _u8_t, _i32_t = _torch().float32, _torch().uint8, _torch().int32
+_bf16_t, _i8_t = _torch().bfloat16, _torch().int8
 _KINDS = {_torch().bfloat16: BF16, _f32_t: F32}
 _raw_stream = _torch()._C._cuda_getCurrentRawStream
 
@@ -613,6 +618,31 @@ def _grad_list(grads, total):
                                  f"{str(g.dtype).replace('torch.', '')} {tuple(g.shape)} with strides {g.stride()}")
     return (n, _host_array(ctypes.c_void_p, "Q", map(T.data_ptr, grads), n),
             _host_array(ctypes.c_int64, "q", map(T.numel, grads), n), _host_array(ctypes.c_int32, "i", dtypes, n), like)
+
+
+def _quantize_int8(x, flags, q, scales):
+    _check_bf16_2d(x)
+    rows, cols = x.shape
+    q = x.new_empty((rows, cols), dtype=_i8_t) if q is None else _on(_expect(q, "q", (rows, cols), _i8_t), x, "q")
+    scales = _f32_out(scales, "scales", rows, x)
+    _check(lib.mxgg_quantize_rowwise(x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols, INT8, flags or 0,
+                                     q.data_ptr(), scales.data_ptr(), _stream_of(x)))
+    return q, scales
+
+
+def _grouped_fwd_int8(a_q, a_s, w_q, w_s, m_splits, N, K, out, ws):
+    G = len(m_splits)
+    M = a_q.shape[0] if a_q.dim() else 0
+    _expect(a_q, "a_q", (M, K), _i8_t)
+    _on(_expect(a_s, "a_s", (M,), _f32_t), a_q, "a_s")
+    _on(_expect(w_q, "w_q", (G * N, K), _i8_t), a_q, "w_q")
+    _on(_expect(w_s, "w_s", (G * N,), _f32_t), a_q, "w_s")
+    out = a_q.new_empty((M, N), dtype=_bf16_t) if out is None else _on(_expect(out, "out", (M, N), _bf16_t), a_q, "out")
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib.mxgg_grouped_fwd(a_q.data_ptr(), a_s.data_ptr(), INT8, w_q.data_ptr(), w_s.data_ptr(), INT8,
+                                _host_array(ctypes.c_int64, "q", m_splits, G), G, M, N, K, out.data_ptr(), _at(ws),
+                                ws_bytes, _stream_of(a_q)))
+    return out
 
 
 def _norm_kind(norm_type):

@@ -39,20 +39,33 @@ __device__ __forceinline__ int sort_key(const SortParams& p, int c) {
   return id >= 0 && id < (I)p.experts ? (int)id : p.experts;
 }
 
-// Counts the `have` lanes' keys into cnt; a lane's place among them and what
-// cnt held.
-__device__ __forceinline__ int count_keys(int32_t* cnt, int key, bool have, int bits) {
-  uint64_t same = __ballot(have);
-  for (int b = 0; b < bits; ++b) {
-    const uint64_t set = __ballot((key >> b) & 1);
-    same &= (key >> b) & 1 ? set : ~set;
-  }
+// Counts PER keys a lane into cnt (those with `have`), 64 neighbouring choices
+// at a time; place: a lane's among its wave's choices of the same key. One step for
+// all PER before the next, so that their latencies overlap.
+template <int PER>
+__device__ __forceinline__ void count_keys(int32_t* cnt, const int (&key)[PER], const bool (&have)[PER], int bits,
+                                           int (&place)[PER]) {
   const int lane = threadIdx.x & 63;
-  const int first = have ? __ffsll((unsigned long long)same) - 1 : lane;
-  int before = 0;
-  if (have && lane == first) before = atomicAdd(cnt + key, (int32_t)__popcll(same));
-  before = __shfl(before, first, 64);
-  return before + (int)__popcll(same & ((1ull << lane) - 1));
+  uint64_t same[PER];
+  int first[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) same[i] = __ballot(have[i]);
+  for (int b = 0; b < bits; ++b)
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool set = (key[i] >> b) & 1;
+      const uint64_t with = __ballot(set);
+      same[i] &= set ? with : ~with;
+    }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    first[i] = have[i] ? __ffsll((unsigned long long)same[i]) - 1 : lane;
+    place[i] = 0;
+    if (have[i] && lane == first[i]) place[i] = atomicAdd(cnt + key[i], (int32_t)__popcll(same[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    place[i] = __shfl(place[i], first[i], 64) + (int)__popcll(same[i] & ((1ull << lane) - 1));
 }
 
 // Exclusive prefix sum over the block's threads.
@@ -73,26 +86,27 @@ __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part) {
 }
 
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
-constexpr int kSortPer = kSortChunk / kSortThreads;   // choices of a lane
 constexpr int kSortKeys = kMaxExperts + 1;
+constexpr int kSortPer = kSortChunk / kSortThreads;   // choices of a lane, of several workgroups
 static_assert(kSortKeys <= kSortThreads && kSortKeys <= 1 << kSortBits, "a thread for each key");
 
 // The chunk's choices: keys, and their places among those of the same key in
 // the chunk; thread e < experts + 1 gets key e's count.
-template <class I>
+template <class I, int PER>
 __device__ __forceinline__ int32_t sort_chunk(const SortParams& p, int first, int32_t (*cnt)[kSortKeys],
-                                              int (&key)[kSortPer], int (&place)[kSortPer]) {
+                                              int (&key)[PER], int (&place)[PER]) {
   const int keys = p.experts + 1, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int bits = 32 - __clz(p.experts);
   for (int e = lane; e < keys; e += 64) cnt[wave][e] = 0;
-  const int run = first + wave * (64 * kSortPer) + lane;
+  const int run = first + wave * (64 * PER) + lane;
+  bool have[PER];
 #pragma unroll
-  for (int i = 0; i < kSortPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int c = run + i * 64;
-    key[i] = c < p.n ? sort_key<I>(p, c) : p.experts;
+    have[i] = c < p.n;
+    key[i] = have[i] ? sort_key<I>(p, c) : p.experts;
   }
-#pragma unroll
-  for (int i = 0; i < kSortPer; ++i) place[i] = count_keys(cnt[wave], key[i], run + i * 64 < p.n, bits);
+  count_keys<PER>(cnt[wave], key, have, bits, place);
   __syncthreads();
   int32_t total = 0;
   if ((int)threadIdx.x < keys) {
@@ -105,7 +119,7 @@ __device__ __forceinline__ int32_t sort_chunk(const SortParams& p, int first, in
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSortPer; ++i) place[i] += cnt[wave][key[i]];
+  for (int i = 0; i < PER; ++i) place[i] += cnt[wave][key[i]];
   return total;
 }
 
@@ -114,20 +128,20 @@ __device__ __forceinline__ void store_place(const SortParams& p, int c, int key,
   p.choices[place] = c;
 }
 
-// One chunk: all in one workgroup.
-template <class I>
+// One workgroup for all, PER choices a lane.
+template <class I, int PER>
 __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams p) {
   __shared__ int32_t cnt[kSortWaves][kSortKeys];
   __shared__ int32_t base[kSortKeys], part[kSortWaves];
-  int key[kSortPer], place[kSortPer];
-  const int32_t total = sort_chunk<I>(p, 0, cnt, key, place);
+  int key[PER], place[PER];
+  const int32_t total = sort_chunk<I, PER>(p, 0, cnt, key, place);
   const int32_t at = block_exclusive<kSortThreads>(total, part);
   if ((int)threadIdx.x <= p.experts) base[threadIdx.x] = at;
   if ((int)threadIdx.x < p.experts) p.counts[threadIdx.x] = total;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSortPer; ++i) {
-    const int c = (int)(threadIdx.x >> 6) * (64 * kSortPer) + i * 64 + (threadIdx.x & 63);
+  for (int i = 0; i < PER; ++i) {
+    const int c = (int)(threadIdx.x >> 6) * (64 * PER) + i * 64 + (threadIdx.x & 63);
     if (c < p.n) store_place(p, c, key[i], base[key[i]] + place[i]);
   }
 }
@@ -138,7 +152,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams p) 
   __shared__ int32_t cnt[kSortWaves][kSortKeys];
   int key[kSortPer], place[kSortPer];
   const int first = (int)blockIdx.x * kSortChunk;
-  const int32_t total = sort_chunk<I>(p, first, cnt, key, place);
+  const int32_t total = sort_chunk<I, kSortPer>(p, first, cnt, key, place);
   if ((int)threadIdx.x <= p.experts) p.table[(int64_t)blockIdx.x * (p.experts + 1) + threadIdx.x] = total;
 #pragma unroll
   for (int i = 0; i < kSortPer; ++i) {
@@ -168,42 +182,54 @@ __global__ __launch_bounds__(64) void sort_scan_kernel(SortParams p, int chunks)
 }
 
 // ... and the places of all. SCANNED: the table holds what the launch above made
-// of it; else every workgroup adds its columns up.
+// of it; else every workgroup adds its columns up, `parts` threads a column.
 template <class I, bool SCANNED>
-__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p, int chunks) {
-  __shared__ int32_t base[kSortKeys], part[kSortWaves];
-  const int keys = p.experts + 1, e = threadIdx.x, mine = blockIdx.x;
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p, int chunks, int parts) {
+  __shared__ int32_t base[kSortKeys], part[kSortWaves], sums[2][kSortThreads];
+  const int keys = p.experts + 1, t = threadIdx.x, mine = blockIdx.x;
   const int first = mine * kSortChunk;
   int key[kSortPer], place[kSortPer];
 #pragma unroll
   for (int i = 0; i < kSortPer; ++i) {
-    const int c = first + i * kSortThreads + e;
+    const int c = first + i * kSortThreads + t;
     if (c < p.n) {
       key[i] = sort_key<I>(p, c);
       place[i] = p.rows[c];
     }
   }
   int32_t before = 0, total = 0;
-  if (e < keys) {
-    if constexpr (SCANNED) {
-      before = p.table[(int64_t)mine * keys + e];
-      total = p.table[(int64_t)chunks * keys + e];
-    } else {
+  if constexpr (SCANNED) {
+    if (t < keys) {
+      before = p.table[(int64_t)mine * keys + t];
+      total = p.table[(int64_t)chunks * keys + t];
+    }
+  } else {
+    const int width = kSortThreads / parts, e = t % width;
+    if (e < keys) {
 #pragma unroll 16
-      for (int b = 0; b < chunks; ++b) {
+      for (int b = t / width; b < chunks; b += parts) {
         const int32_t v = p.table[(int64_t)b * keys + e];
         before += b < mine ? v : 0;
         total += v;
       }
     }
+    sums[0][t] = before;
+    sums[1][t] = total;
+    __syncthreads();
+    before = total = 0;
+    if (t < keys)
+      for (int q = 0; q < parts; ++q) {
+        before += sums[0][q * width + t];
+        total += sums[1][q * width + t];
+      }
   }
   const int32_t at = block_exclusive<kSortThreads>(total, part);
-  if (e < keys) base[e] = at + before;
-  if (mine == 0 && e < p.experts) p.counts[e] = total;
+  if (t < keys) base[t] = at + before;
+  if (mine == 0 && t < p.experts) p.counts[t] = total;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSortPer; ++i) {
-    const int c = first + i * kSortThreads + e;
+    const int c = first + i * kSortThreads + t;
     if (c < p.n) store_place(p, c, key[i], base[key[i]] + place[i]);
   }
 }
@@ -212,19 +238,23 @@ template <class I>
 hipError_t sort_any(const SortParams& p, hipStream_t st) {
   const int64_t chunks = sort_chunks(p.n);
   if (chunks <= 1) {
-    sort_one_kernel<I><<<1, kSortThreads, 0, st>>>(p);
+    if (p.n <= kSortThreads) sort_one_kernel<I, 1><<<1, kSortThreads, 0, st>>>(p);
+    else if (p.n <= 2 * kSortThreads) sort_one_kernel<I, 2><<<1, kSortThreads, 0, st>>>(p);
+    else sort_one_kernel<I, kSortOne / kSortThreads><<<1, kSortThreads, 0, st>>>(p);
     return hipGetLastError();
   }
   sort_count_kernel<I><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (chunks <= kSortDirect) {
-    sort_place_kernel<I, false><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks);
+    int parts = 1;
+    while (parts * 2 * (p.experts + 1) <= kSortThreads) parts *= 2;
+    sort_place_kernel<I, false><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, parts);
     return hipGetLastError();
   }
   sort_scan_kernel<<<(uint32_t)p.experts + 1, 64, 0, st>>>(p, (int)chunks);
   if ((e = hipGetLastError()) != hipSuccess) return e;
-  sort_place_kernel<I, true><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks);
+  sort_place_kernel<I, true><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, 1);
   return hipGetLastError();
 }
 
@@ -235,7 +265,20 @@ hipError_t sort_any(const SortParams& p, hipStream_t st) {
 // takes 16-byte chunks L apart.
 
 constexpr int kRowThreads = 256;
-constexpr int64_t kRowGrid = 1 << 20;   // workgroups along the tokens at most; they stay for the rest
+constexpr int64_t kRowGrid = 1 << 20;   // workgroups at most; they stay for the rest
+
+// A thread's first token and chunk of the row: neighbouring workgroups have the
+// pieces of one row, which keeps a row's reads together.
+struct RowPlace {
+  int64_t token, step;
+  int chunk;
+  __device__ __forceinline__ RowPlace(int lanes, uint32_t pieces) {
+    const int per = kRowThreads / lanes;
+    token = (int64_t)(blockIdx.x / pieces) * per + threadIdx.x / lanes;
+    step = (int64_t)(gridDim.x / pieces) * per;
+    chunk = (int)(blockIdx.x % pieces) * lanes + threadIdx.x % lanes;
+  }
+};
 
 // The chunk at `col`, moved back to end with the row (its first elements are its
 // neighbour's then, and written twice with the same bits); a row shorter than a
@@ -259,13 +302,13 @@ struct RowChunk {
 };
 
 template <class E>
-__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(TokenParams p, int lanes) {
+__global__ __launch_bounds__(kRowThreads) void dispatch_kernel(TokenParams p, int lanes, uint32_t pieces) {
   constexpr int N = Chunk<E>::N;
-  const int per = kRowThreads / lanes, lane = threadIdx.x % lanes;
-  const int col = ((int)blockIdx.y * lanes + lane) * N;
+  const RowPlace pl(lanes, pieces);
+  const int col = pl.chunk * N;
   if (col >= p.cols) return;
   const RowChunk<E> at(col, p.cols);
-  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes; t < p.tokens; t += (int64_t)gridDim.x * per) {
+  for (int64_t t = pl.token; t < p.tokens; t += pl.step) {
     Chunk<E> c, zero{};
     at.load(c, static_cast<const E*>(p.x) + t * p.ldx);
     for (int j = 0; j < p.top_k; ++j) {
@@ -276,23 +319,42 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(TokenParams p, in
   }
 }
 
-template <class E, bool WEIGHTED>
-__global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int lanes) {
+// A token's choices j < K (at least top_k): rows that are kept and their weights. A
+// row that is not has weight 0 and is read at place 0, and what is read there is
+// not used: loads behind a branch would be waited for one after the other.
+template <int K>
+struct Choices {
+  int32_t row[K];
+  float weight[K];
+  bool kept[K];
+  __device__ __forceinline__ Choices(const TokenParams& p, int64_t t) {
+#pragma unroll
+    for (int j = 0; j < K; ++j) row[j] = p.rows[t * p.top_k + (j < p.top_k ? j : 0)];
+#pragma unroll
+    for (int j = 0; j < K; ++j) weight[j] = p.weights ? p.weights[t * p.top_k + (j < p.top_k ? j : 0)] : 1.f;
+#pragma unroll
+    for (int j = 0; j < K; ++j) kept[j] = j < p.top_k && row[j] >= 0 && row[j] < p.expert_rows;
+  }
+};
+
+template <class E, int K>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int lanes, uint32_t pieces) {
   constexpr int N = Chunk<E>::N;
-  const int per = kRowThreads / lanes, lane = threadIdx.x % lanes;
-  const int col = ((int)blockIdx.y * lanes + lane) * N;
+  const RowPlace pl(lanes, pieces);
+  const int col = pl.chunk * N;
   if (col >= p.cols) return;
   const RowChunk<E> at(col, p.cols);
-  for (int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / lanes; t < p.tokens; t += (int64_t)gridDim.x * per) {
+  for (int64_t t = pl.token; t < p.tokens; t += pl.step) {
     float sum[N] = {};
-    for (int j = 0; j < p.top_k; ++j) {
-      const int32_t r = p.rows[t * p.top_k + j];
-      if (r < 0 || r >= p.expert_rows) continue;
-      const float w = WEIGHTED ? p.weights[t * p.top_k + j] : 1.f;
-      Chunk<E> c;
-      at.load(c, static_cast<const E*>(p.y) + r * p.ldy);
+    if (p.expert_rows > 0) {
+      const Choices<K> ch(p, t);
+      Chunk<E> c[K];
 #pragma unroll
-      for (int i = 0; i < N; ++i) sum[i] += WEIGHTED ? w * c.get(i) : c.get(i);
+      for (int j = 0; j < K; ++j) at.load(c[j], static_cast<const E*>(p.y) + (ch.kept[j] ? ch.row[j] : 0) * p.ldy);
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+#pragma unroll
+        for (int i = 0; i < N; ++i) sum[i] = ch.kept[j] ? __builtin_fmaf(ch.weight[j], c[j].get(i), sum[i]) : sum[i];
     }
     Chunk<E> o;
     o.set(sum);
@@ -300,44 +362,64 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int
   }
 }
 
-// One workgroup a token: the weights' gradients are sums over the whole row.
-template <class E>
+// A token belongs to L lanes that go over the whole row: the weights' gradients
+// are sums over it.
+template <class E, int K, int L>
 __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p) {
-  constexpr int N = Chunk<E>::N;
-  __shared__ float part[kRowThreads / 64];
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    const E* d = static_cast<const E*>(p.x) + t * p.ldx;
-    for (int j = 0; j < p.top_k; ++j) {
-      const int32_t r = p.rows[t * p.top_k + j];
-      const int32_t to = r < 0 ? ~r : r;
-      const bool here = to < p.expert_rows, kept = r >= 0 && here;
-      const float w = kept ? p.weights[t * p.top_k + j] : 0.f;
-      float dot = 0.f;
-      if (here)
-        for (int col = (int)threadIdx.x * N; col < p.cols; col += kRowThreads * N) {
-          const RowChunk<E> at(col, p.cols);
-          Chunk<E> c, o{};
-          if (kept) {
-            Chunk<E> y;
-            at.load(c, d);
-            at.load(y, static_cast<const E*>(p.y) + r * p.ldy);
-            float v[N];
+  constexpr int N = Chunk<E>::N, PER = kRowThreads / L;
+  __shared__ float part[kRowThreads / 64][K];
+  const int lane = threadIdx.x % L;
+  for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < p.tokens; t0 += (int64_t)gridDim.x * PER) {
+    const bool here = t0 + threadIdx.x / L < p.tokens;
+    const int64_t t = here ? t0 + threadIdx.x / L : p.tokens - 1;
+    float dot[K] = {};
+    if (here && p.expert_rows > 0) {
+      const Choices<K> ch(p, t);
+      const E* d = static_cast<const E*>(p.x) + t * p.ldx;
+      for (int col = lane * N; col < p.cols; col += L * N) {
+        const RowChunk<E> at(col, p.cols);
+        Chunk<E> c, y[K];
+        at.load(c, d);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              // a moved chunk's first elements count in their own lane
-              if (at.start + i >= col && i < at.size) dot += c.get(i) * y.get(i);
-              v[i] = w * c.get(i);
-            }
-            o.set(v);
+        for (int j = 0; j < K; ++j) at.load(y[j], static_cast<const E*>(p.y) + (ch.kept[j] ? ch.row[j] : 0) * p.ldy);
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+          float v[N];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            // a moved chunk's first elements count in their own lane
+            const bool own = at.start + i >= col && i < at.size;
+            dot[j] = own ? __builtin_fmaf(c.get(i), y[j].get(i), dot[j]) : dot[j];
+            v[i] = ch.kept[j] ? ch.weight[j] * c.get(i) : 0.f;
           }
-          at.store(o, static_cast<E*>(p.out) + to * p.ldo);
+          Chunk<E> o;
+          o.set(v);
+          const int32_t to = ch.row[j] < 0 ? ~ch.row[j] : ch.row[j];
+          if (j < p.top_k && to < p.expert_rows) at.store(o, static_cast<E*>(p.out) + to * p.ldo);
         }
-      dot = lanes_sum<64>(dot);
-      if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = dot;
+      }
+#pragma unroll
+      for (int j = 0; j < K; ++j) dot[j] = ch.kept[j] ? dot[j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < K; ++j) dot[j] = lanes_sum<(L < 64 ? L : 64)>(dot[j]);
+    if constexpr (L > 64) {
+      if (threadIdx.x % 64 == 0)
+#pragma unroll
+        for (int j = 0; j < K; ++j) part[threadIdx.x / 64][j] = dot[j];
       __syncthreads();
-      if (threadIdx.x == 0) p.dweights[t * p.top_k + j] = kept ? part[0] + part[1] + part[2] + part[3] : 0.f;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (lane == j) {
+          float sum = part[threadIdx.x / L * (L / 64)][j];
+          for (int w = 1; w < L / 64; ++w) sum += part[threadIdx.x / L * (L / 64) + w][j];
+          dot[j] = sum;
+        }
       __syncthreads();
     }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (here && lane == j && j < p.top_k) p.dweights[t * p.top_k + j] = dot[j];
   }
 }
 
@@ -350,23 +432,52 @@ int row_lanes(int64_t chunks) {
 
 struct RowGrid {
   int lanes;
-  dim3 grid;
+  uint32_t pieces, grid;
 };
 RowGrid row_grid(const TokenParams& p, int n) {
   const int64_t chunks = (p.cols + n - 1) / n;
   RowGrid g;
   g.lanes = row_lanes(chunks);
-  const int64_t per = kRowThreads / g.lanes, blocks = (p.tokens + per - 1) / per;
-  g.grid = dim3((uint32_t)(blocks < kRowGrid ? blocks : kRowGrid), (uint32_t)((chunks + g.lanes - 1) / g.lanes));
+  g.pieces = (uint32_t)((chunks + g.lanes - 1) / g.lanes);
+  const int64_t per = kRowThreads / g.lanes, blocks = (p.tokens + per - 1) / per, most = kRowGrid / g.pieces;
+  g.grid = g.pieces * (uint32_t)(blocks < most ? blocks : most);
   return g;
 }
 
+template <class E, int K>
+hipError_t combine(const TokenParams& p, hipStream_t st) {
+  const RowGrid g = row_grid(p, Chunk<E>::N);
+  combine_kernel<E, K><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
+  return hipGetLastError();
+}
+template <class E, int K, int L>
+hipError_t combine_bwd(const TokenParams& p, hipStream_t st) {
+  const int64_t blocks = (p.tokens + kRowThreads / L - 1) / (kRowThreads / L);
+  combine_bwd_kernel<E, K, L><<<(uint32_t)(blocks < kRowGrid ? blocks : kRowGrid), kRowThreads, 0, st>>>(p);
+  return hipGetLastError();
+}
 template <class E>
 hipError_t combine_any(const TokenParams& p, hipStream_t st) {
-  const RowGrid g = row_grid(p, Chunk<E>::N);
-  if (p.weights) combine_kernel<E, true><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes);
-  else combine_kernel<E, false><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes);
-  return hipGetLastError();
+  if (p.top_k <= 1) return combine<E, 1>(p, st);
+  if (p.top_k <= 2) return combine<E, 2>(p, st);
+  if (p.top_k <= 4) return combine<E, 4>(p, st);
+  if (p.top_k <= 8) return combine<E, 8>(p, st);
+  return combine<E, 16>(p, st);
+}
+template <class E, int K>
+hipError_t combine_bwd_wide(const TokenParams& p, hipStream_t st) {
+  const int chunks = (p.cols + Chunk<E>::N - 1) / Chunk<E>::N;
+  if (chunks <= 16) return combine_bwd<E, K, 16>(p, st);
+  if (chunks <= 32) return combine_bwd<E, K, 32>(p, st);
+  return chunks <= 128 ? combine_bwd<E, K, 64>(p, st) : combine_bwd<E, K, 256>(p, st);
+}
+template <class E>
+hipError_t combine_bwd_any(const TokenParams& p, hipStream_t st) {
+  if (p.top_k <= 1) return combine_bwd_wide<E, 1>(p, st);
+  if (p.top_k <= 2) return combine_bwd_wide<E, 2>(p, st);
+  if (p.top_k <= 4) return combine_bwd_wide<E, 4>(p, st);
+  if (p.top_k <= 8) return combine_bwd_wide<E, 8>(p, st);
+  return combine_bwd_wide<E, 16>(p, st);
 }
 
 }  // namespace
@@ -377,8 +488,8 @@ hipError_t launch_moe_sort(const SortParams& p, bool i64, hipStream_t st) {
 
 hipError_t launch_moe_dispatch(const TokenParams& p, bool f32, hipStream_t st) {
   const RowGrid g = row_grid(p, f32 ? 4 : 8);
-  if (f32) dispatch_kernel<float><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes);
-  else dispatch_kernel<bf16_t><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes);
+  if (f32) dispatch_kernel<float><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
+  else dispatch_kernel<bf16_t><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
   return hipGetLastError();
 }
 
@@ -387,10 +498,7 @@ hipError_t launch_moe_combine(const TokenParams& p, bool f32, hipStream_t st) {
 }
 
 hipError_t launch_moe_combine_bwd(const TokenParams& p, bool f32, hipStream_t st) {
-  const uint32_t grid = (uint32_t)(p.tokens < kRowGrid ? p.tokens : kRowGrid);
-  if (f32) combine_bwd_kernel<float><<<grid, kRowThreads, 0, st>>>(p);
-  else combine_bwd_kernel<bf16_t><<<grid, kRowThreads, 0, st>>>(p);
-  return hipGetLastError();
+  return f32 ? combine_bwd_any<float>(p, st) : combine_bwd_any<bf16_t>(p, st);
 }
 
 }  // namespace mxgg

@@ -10,11 +10,13 @@
 namespace mxgg {
 
 // --- tokens to experts and back ---------------------------------------------
-// Choices that one workgroup sorts; a call of more than one of them goes over
-// a table of the workgroups' counts (in the workspace), one row of experts + 1
-// counts each (the last: dropped choices).
-constexpr int kSortChunk = 2048;
-inline int64_t sort_chunks(int64_t choices) { return (choices + kSortChunk - 1) / kSortChunk; }
+// Up to kSortOne choices are sorted by one workgroup in one launch. More are cut
+// into chunks of kSortChunk, a workgroup each, that meet in a table (in the
+// workspace): one row of experts + 1 counts a chunk (the last: dropped choices).
+constexpr int kSortOne = 4096, kSortChunk = 2048;
+inline int64_t sort_chunks(int64_t choices) {
+  return choices <= kSortOne ? 1 : (choices + kSortChunk - 1) / kSortChunk;
+}
 // Up to so many workgroups, each adds up the table's rows before its own
 // itself; beyond, a launch between does it for all.
 constexpr int64_t kSortDirect = 128;
