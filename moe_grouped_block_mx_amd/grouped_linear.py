@@ -173,6 +173,7 @@ class GroupedLinear(torch.nn.Module):
                                             device=device)
         self.weight.overwrite_main_grad = False
         self._cache = _WeightCache()
+        self._int8 = None
         self._pending = []
 
     def forward(self, x, m_splits, is_first_microbatch=None, out=None, dgrad_out=None):
@@ -197,6 +198,23 @@ class GroupedLinear(torch.nn.Module):
         (q, s), _ = self._cache.get(self.weight, self.recipe, self.num_experts, self.out_features, self.in_features)
         f = _formats(self.recipe, self.out_features, self.in_features)["fwd_w"]
         return q, s, L.FORMATS[f] if isinstance(f, str) else f
+
+    def int8_weight(self):
+        """(codes, scales) of the weight in 8-bit integers with a scale per output
+        channel, quantized again only when the weight changed."""
+        key = (self.weight.data_ptr(), self.weight._version)
+        if self._int8 is None or self._int8[0] != key:
+            self._int8 = (key, *L.mxgg_quantize_rowwise(self.weight.detach(), L.INT8))
+        return self._int8[1:]
+
+    @torch.no_grad()
+    def forward_int8(self, x, m_splits):
+        """The layer in 8-bit integers, for serving (no gradient): x bf16 [M, K]
+        quantized per token, times int8_weight(). in_features a multiple of 16."""
+        q, scales = L.mxgg_quantize_rowwise(x, L.INT8)
+        w_q, w_s = self.int8_weight()
+        return L.mxgg_grouped_fwd(q, scales, w_q, w_s, [int(m) for m in m_splits], self.out_features, self.in_features,
+                                  a_fmt=L.INT8, w_fmt=L.INT8)
 
     def _run_wgrad(self, job):
         dq, ds, xq, xs, m_splits, mpad, accumulate = job
