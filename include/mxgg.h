@@ -626,7 +626,7 @@ typedef enum mxgg_itype { MXGG_I32 = 0, MXGG_I64 = 1 } mxgg_itype;
  *            the number of choices that were not dropped (on the host they are
  *            the m_splits of the grouped GEMMs).
  *   ws       mxgg_moe_sort_workspace(...) bytes, 16-byte aligned (NULL when 0).
- * tokens >= 0, tokens * top_k < 2^31, top_k in [1, 16], experts in [1, 512].
+ * tokens >= 0, tokens * top_k <= 2^30, top_k in [1, 16], experts in [1, 512].
  * tokens == 0 clears the counts. Errors: NULL, SHAPE, FORMAT, ALIGN, WORKSPACE,
  * DEVICE, ARCH, HIP.
  */
@@ -644,7 +644,8 @@ size_t mxgg_moe_sort_workspace(int64_t tokens, int64_t top_k, int64_t experts);
  *   out   [expert_rows, cols] of `dtype`, leading dimension ldo. Places from
  *         expert_rows on are left out (with expert_rows the sum of the counts,
  *         just the dropped ones), rows that no place names stay as they were.
- * Its gradient is mxgg_moe_combine without weights. cols in [1, 2^24].
+ * Its gradient is mxgg_moe_combine without weights. out does not overlap x. cols
+ * in [1, 2^24].
  * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
  */
 mxgg_status mxgg_moe_dispatch(const void* x, int64_t ldx, mxgg_dtype dtype, int64_t tokens, int64_t cols,

@@ -475,8 +475,9 @@ def mxgg_grouped_wgrad(dycol_q, dycol_s, xcol_q, xcol_s, m_splits, N, K, mpad, m
 # few microseconds: their bindings pass addresses as plain ints and look a
 # caller's buffer over only where one was given.
 _f32_t, _u8_t, _i32_t = _torch().float32, _torch().uint8, _torch().int32
-_bf16_t, _i8_t = _torch().bfloat16, _torch().int8
-_KINDS = {_torch().bfloat16: BF16, _f32_t: F32}
+_bf16_t, _i8_t, _i64_t = _torch().bfloat16, _torch().int8, _torch().int64
+_KINDS = {_bf16_t: BF16, _f32_t: F32}
+_INTS = {_i32_t: I32, _i64_t: I64}
 _raw_stream = _torch()._C._cuda_getCurrentRawStream
 
 
@@ -623,8 +624,8 @@ def _grad_list(grads, total):
 def _quantize_int8(x, flags, q, scales):
     _check_bf16_2d(x)
     rows, cols = x.shape
-    q = x.new_empty((rows, cols), dtype=_i8_t) if q is None else _on(_expect(q, "q", (rows, cols), _i8_t), x, "q")
-    scales = _f32_out(scales, "scales", rows, x)
+    q = x.new_empty((rows, cols), dtype=_i8_t) if q is None else _expect(q, "q", (rows, cols), _i8_t)
+    scales = x.new_empty(rows, dtype=_f32_t) if scales is None else _expect(scales, "scales", (rows,), _f32_t)
     _check(lib.mxgg_quantize_rowwise(x.data_ptr(), rows, cols, x.stride(0) if rows > 1 else cols, INT8, flags or 0,
                                      q.data_ptr(), scales.data_ptr(), _stream_of(x)))
     return q, scales
@@ -634,10 +635,10 @@ def _grouped_fwd_int8(a_q, a_s, w_q, w_s, m_splits, N, K, out, ws):
     G = len(m_splits)
     M = a_q.shape[0] if a_q.dim() else 0
     _expect(a_q, "a_q", (M, K), _i8_t)
-    _on(_expect(a_s, "a_s", (M,), _f32_t), a_q, "a_s")
-    _on(_expect(w_q, "w_q", (G * N, K), _i8_t), a_q, "w_q")
-    _on(_expect(w_s, "w_s", (G * N,), _f32_t), a_q, "w_s")
-    out = a_q.new_empty((M, N), dtype=_bf16_t) if out is None else _on(_expect(out, "out", (M, N), _bf16_t), a_q, "out")
+    _expect(a_s, "a_s", (M,), _f32_t)
+    _expect(w_q, "w_q", (G * N, K), _i8_t)
+    _expect(w_s, "w_s", (G * N,), _f32_t)
+    out = a_q.new_empty((M, N), dtype=_bf16_t) if out is None else _expect(out, "out", (M, N), _bf16_t)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.mxgg_grouped_fwd(a_q.data_ptr(), a_s.data_ptr(), INT8, w_q.data_ptr(), w_s.data_ptr(), INT8,
                                 _host_array(ctypes.c_int64, "q", m_splits, G), G, M, N, K, out.data_ptr(), _at(ws),
@@ -741,23 +742,34 @@ def mxgg_moe_layer(x, logits, w13_q, w13_s, w2_q, w2_s, top_k, fmt="mxfp4", reno
     return out, ids, weights
 
 
+def _lead(t, name):
+    """Leading dimension of a 2-D tensor with unit inner stride (one look for the
+    common case)."""
+    return t.shape[1] if t.is_contiguous() and t.dim() == 2 else _rows2d(t, name)
+
+
 def _rows_index(rows):
     """(tokens, top_k) of the places that moe_sort writes."""
-    if rows.dim() != 2 or rows.dtype is not _i32_t or not rows.is_contiguous():
+    shape = rows.shape
+    if len(shape) != 2 or rows.dtype is not _i32_t or not rows.is_contiguous():
         raise ValueError(f"rows must be a contiguous int32 tensor [tokens, top_k], got "
-                         f"{str(rows.dtype).replace('torch.', '')} {tuple(rows.shape)}")
-    return rows.shape
+                         f"{str(rows.dtype).replace('torch.', '')} {tuple(shape)}")
+    return shape
 
 
-def _like_rows(t, name, n, x):
-    """[n, cols] beside x, the caller's or a new one, and its leading dimension."""
-    cols = x.shape[1]
+def _like_rows(t, name, n, cols, x):
+    """[n, cols] of x's type, the caller's or a new one, and its leading dimension.
+    (That it is on x's device the library checks, as of every pointer.)"""
     if t is None:
         return x.new_empty((n, cols)), cols
-    if t.dim() != 2 or (n is not None and t.shape[0] != n) or t.shape[1] != cols or t.dtype is not x.dtype:
-        raise ValueError(f"{name} must be a {str(x.dtype).replace('torch.', '')} tensor [{'rows' if n is None else n}, "
-                         f"{cols}], got {str(t.dtype).replace('torch.', '')} {tuple(t.shape)}")
-    return t, _rows2d(_on(t, x, name), name)
+    if t.shape != (n, cols) or t.dtype is not x.dtype:
+        raise ValueError(f"{name} must be a {str(x.dtype).replace('torch.', '')} tensor [{n}, {cols}], got "
+                         f"{str(t.dtype).replace('torch.', '')} {tuple(t.shape)}")
+    return t, _lead(t, name)
+
+
+def _i32_out(t, name, shape, like):
+    return like.new_empty(shape, dtype=_i32_t) if t is None else _expect(t, name, shape, _i32_t)
 
 
 def mxgg_moe_sort(ids, experts, rows=None, choices=None, counts=None, ws=None):
@@ -767,23 +779,21 @@ def mxgg_moe_sort(ids, experts, rows=None, choices=None, counts=None, ws=None):
     (~place, behind all others, of a dropped one), the choice at each place
     [tokens * top_k], the rows of each expert [experts]: counts.tolist() are the
     grouped GEMMs' m_splits."""
-    torch = _torch()
-    if ids.dtype not in (torch.int32, torch.int64):
+    kind = _INTS.get(ids.dtype)
+    if kind is None:
         raise ValueError(f"ids must be int32 or int64, got {str(ids.dtype).replace('torch.', '')}")
-    ldi = _rows2d(ids, "ids")
+    ldi = _lead(ids, "ids")
     T, k = ids.shape
-    rows = ids.new_empty((T, k), dtype=_i32_t) if rows is None else _on(_expect(rows, "rows", (T, k), _i32_t), ids, "rows")
-    choices = ids.new_empty(T * k, dtype=_i32_t) if choices is None \
-        else _on(_expect(choices, "choices", (T * k,), _i32_t), ids, "choices")
-    counts = ids.new_empty(experts, dtype=_i32_t) if counts is None \
-        else _on(_expect(counts, "counts", (experts,), _i32_t), ids, "counts")
-    need = int(lib.mxgg_moe_sort_workspace(T, k, experts))
+    rows = _i32_out(rows, "rows", (T, k), ids)
+    choices = _i32_out(choices, "choices", (T * k,), ids)
+    counts = _i32_out(counts, "counts", (experts,), ids)
+    need = lib.mxgg_moe_sort_workspace(T, k, experts)
     at, ws_bytes = None, 0
     if need or ws is not None:
         ws, ws_bytes = _ws(ws, need, ids)
         at = ws.data_ptr()
-    _check(lib.mxgg_moe_sort(ids.data_ptr(), I64 if ids.dtype is torch.int64 else I32, ldi, T, k, experts,
-                             rows.data_ptr(), choices.data_ptr(), counts.data_ptr(), at, ws_bytes, _stream_of(ids)))
+    _check(lib.mxgg_moe_sort(ids.data_ptr(), kind, ldi, T, k, experts, rows.data_ptr(), choices.data_ptr(),
+                             counts.data_ptr(), at, ws_bytes, _stream_of(ids)))
     return rows, choices, counts
 
 
@@ -792,20 +802,17 @@ def mxgg_moe_dispatch(x, rows, expert_rows=None, out=None):
     at the places of dropped ones. x: bf16 or fp32 [tokens, cols] (any row
     stride); rows from moe_sort; expert_rows: the rows of out (tokens * top_k, or
     sum(m_splits) to leave the dropped ones out)."""
-    dt, ldx = _dtype(x, "x"), _rows2d(x, "x")
-    T, k = _rows_index(_on(rows, x, "rows"))
-    if x.shape[0] != T:
-        raise ValueError(f"x has {x.shape[0]} rows, rows is of {T} tokens")
+    dt, ldx = _dtype(x, "x"), _lead(x, "x")
+    T, k = _rows_index(rows)
+    n, cols = x.shape
+    if n != T:
+        raise ValueError(f"x has {n} rows, rows is of {T} tokens")
     if expert_rows is None:
         expert_rows = T * k if out is None else out.shape[0]
-    out, ldo = _like_rows(out, "out", expert_rows, x)
-    _check(lib.mxgg_moe_dispatch(x.data_ptr(), ldx, dt, T, x.shape[1], rows.data_ptr(), k, out.data_ptr(), ldo,
-                                 expert_rows, _stream_of(x)))
+    out, ldo = _like_rows(out, "out", expert_rows, cols, x)
+    _check(lib.mxgg_moe_dispatch(x.data_ptr(), ldx, dt, T, cols, rows.data_ptr(), k, out.data_ptr(), ldo, expert_rows,
+                                 _stream_of(x)))
     return out
-
-
-def _token_weights(weights, rows):
-    return _on(_expect(weights, "weights", rows.shape, _f32_t), rows, "weights")
 
 
 def mxgg_moe_combine(y, rows, weights=None, out=None):
@@ -813,31 +820,31 @@ def mxgg_moe_combine(y, rows, weights=None, out=None):
     j]] over the choices that are not dropped, summed in fp32. y: bf16 or fp32
     [expert rows, cols] (any row stride); weights: fp32 [tokens, top_k], None for
     1 (then it is the gradient of moe_dispatch)."""
-    dt, ldy = _dtype(y, "y"), _rows2d(y, "y")
-    T, k = _rows_index(_on(rows, y, "rows"))
+    dt, ldy = _dtype(y, "y"), _lead(y, "y")
+    T, k = _rows_index(rows)
     if weights is not None:
-        _token_weights(weights, rows)
-    out, ldo = _like_rows(out, "out", T, y)
-    _check(lib.mxgg_moe_combine(y.data_ptr(), ldy, dt, y.shape[0], y.shape[1], rows.data_ptr(), _at(weights), T, k,
-                                out.data_ptr(), ldo, _stream_of(y)))
+        _expect(weights, "weights", (T, k), _f32_t)
+    n, cols = y.shape
+    out, ldo = _like_rows(out, "out", T, cols, y)
+    _check(lib.mxgg_moe_combine(y.data_ptr(), ldy, dt, n, cols, rows.data_ptr(), _at(weights), T, k, out.data_ptr(), ldo,
+                                _stream_of(y)))
     return out
 
 
 def mxgg_moe_combine_bwd(dout, y, rows, weights, dy=None, dweights=None):
     """The gradients of moe_combine: (dy, dweights), dy like y (zeros at the
     places of dropped choices), dweights fp32 [tokens, top_k]."""
-    dt, ldy = _dtype(y, "y"), _rows2d(y, "y")
-    T, k = _rows_index(_on(rows, y, "rows"))
+    dt, ldy = _dtype(y, "y"), _lead(y, "y")
+    T, k = _rows_index(rows)
     if dout is None:
         raise ValueError("dout is required")
-    dout, lddo = _like_rows(dout, "dout", T, y)
-    _token_weights(weights, rows)
-    dy, lddy = _like_rows(dy, "dy", y.shape[0], y)
-    dweights = y.new_empty((T, k), dtype=_f32_t) if dweights is None \
-        else _on(_expect(dweights, "dweights", (T, k), _f32_t), y, "dweights")
-    _check(lib.mxgg_moe_combine_bwd(dout.data_ptr(), lddo, y.data_ptr(), ldy, dt, y.shape[0], y.shape[1],
-                                    rows.data_ptr(), weights.data_ptr(), T, k, dy.data_ptr(), lddy,
-                                    dweights.data_ptr(), _stream_of(y)))
+    n, cols = y.shape
+    dout, lddo = _like_rows(dout, "dout", T, cols, y)
+    _expect(weights, "weights", (T, k), _f32_t)
+    dy, lddy = _like_rows(dy, "dy", n, cols, y)
+    dweights = y.new_empty((T, k), dtype=_f32_t) if dweights is None else _expect(dweights, "dweights", (T, k), _f32_t)
+    _check(lib.mxgg_moe_combine_bwd(dout.data_ptr(), lddo, y.data_ptr(), ldy, dt, n, cols, rows.data_ptr(),
+                                    weights.data_ptr(), T, k, dy.data_ptr(), lddy, dweights.data_ptr(), _stream_of(y)))
     return dy, dweights
 
 
@@ -848,16 +855,13 @@ def mxgg_dropout(x, p, state, stream=0, residual=None, out=None):
     so the same call on the gradient of out, without residual, is the gradient of
     x. x: bf16 or fp32 [rows, cols] (any row stride), residual and out like it; out
     may be x or residual."""
-    dt, ldx = _dtype(x, "x"), _rows2d(x, "x")
+    dt, ldx = _dtype(x, "x"), _lead(x, "x")
     rows, cols = x.shape
-    _on(_expect(state, "state", (2,), _torch().int64), x, "state")
+    _expect(state, "state", (2,), _i64_t)
     if not 0 <= stream < 1 << 32:
         raise ValueError(f"stream={stream} outside [0, 2^32)")
-    ldr = cols if residual is None else _rows_like(residual, x, "residual")
-    if out is None:
-        out, ldo = x.new_empty((rows, cols)), cols
-    else:
-        ldo = _rows_like(out, x, "out")
+    ldr = cols if residual is None else _like_rows(residual, "residual", rows, cols, x)[1]
+    out, ldo = _like_rows(out, "out", rows, cols, x)
     _check(lib.mxgg_dropout(x.data_ptr(), ldx, dt, rows, cols, p, state.data_ptr(), stream, _at(residual), ldr,
                             out.data_ptr(), ldo, _stream_of(x)))
     return out

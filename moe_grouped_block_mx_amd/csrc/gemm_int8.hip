@@ -67,60 +67,63 @@ __global__ __launch_bounds__(THREADS) void quant_int8_kernel(const uint16_t* x, 
   constexpr int PER = THREADS / L, WAVES = L > 64 ? L / 64 : 1;
   __shared__ uint32_t part[THREADS / 64];
   const int lane = threadIdx.x % L;
-  const int64_t r = (int64_t)blockIdx.x * PER + threadIdx.x / L;
-  const bool here = r < rows;
-  const bf16_t* row = reinterpret_cast<const bf16_t*>(x) + (here ? r : rows - 1) * ldx;
-  Chunk<bf16_t> c[NV];
-  uint32_t top = 0;
-  for (int base = 0; base < chunks; base += L * NV) {
+  for (int64_t r0 = (int64_t)blockIdx.x * PER; r0 < rows; r0 += (int64_t)gridDim.x * PER) {
+    const int64_t r = r0 + threadIdx.x / L;
+    const bool here = r < rows;
+    const bf16_t* row = reinterpret_cast<const bf16_t*>(x) + (here ? r : rows - 1) * ldx;
+    Chunk<bf16_t> c[NV];
+    uint32_t top = 0;
+    for (int base = 0; base < chunks; base += L * NV) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = base + i * L + lane;
-      c[i].load(row + (at < chunks ? at : chunks - 1) * 8);
+      for (int i = 0; i < NV; ++i) {
+        const int at = base + i * L + lane;
+        c[i].load(row + (at < chunks ? at : chunks - 1) * 8);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = max_u16x2(top, c[i].w[w] & 0x7FFF7FFFu);
+      if (STAY) break;
     }
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) top = max_u16x2(top, c[i].w[w] & 0x7FFF7FFFu);
-    if (STAY) break;
-  }
-  top = max(top & 0xFFFFu, top >> 16);
-  top = max(top, rotate<8>(top));
-  top = max(top, rotate<4>(top));
-  top = max(top, rotate<2>(top));
-  top = max(top, rotate<1>(top));
-  if constexpr (L >= 64) {
-    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-  }
-  if constexpr (L > 64) {
-    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w) top = max(top, part[threadIdx.x / L * WAVES + w]);
-  }
-  const Int8Row s(top);
-  if (!here) return;
-  if (lane == 0) scales[r] = s.scale;
-  int8_t* out = q + r * (int64_t)chunks * 8;
-  for (int base = 0; base < chunks; base += L * NV) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int at = base + i * L + lane;
-      if (at >= chunks) continue;
-      if (!STAY) c[i].load(row + at * 8);
-      const uint64_t v = s.codes8(c[i]);
-      memcpy(out + at * 8, &v, 8);
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, rotate<8>(top));
+    top = max(top, rotate<4>(top));
+    top = max(top, rotate<2>(top));
+    top = max(top, rotate<1>(top));
+    if constexpr (L >= 64) {
+      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     }
-    if (STAY) break;
+    if constexpr (L > 64) {
+      if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = max(top, part[threadIdx.x / L * WAVES + w]);
+      __syncthreads();   // the next row's are written after this
+    }
+    if (!here) continue;
+    const Int8Row s(top);
+    if (lane == 0) scales[r] = s.scale;
+    int8_t* out = q + r * (int64_t)chunks * 8;
+    for (int base = 0; base < chunks; base += L * NV) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int at = base + i * L + lane;
+        if (at >= chunks) continue;
+        if (!STAY) c[i].load(row + at * 8);
+        const uint64_t v = s.codes8(c[i]);
+        memcpy(out + at * 8, &v, 8);
+      }
+      if (STAY) break;
+    }
   }
 }
 
 template <int L, int NV, bool STAY = true>
 hipError_t quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, int8_t* q, float* scales, hipStream_t st) {
   constexpr int THREADS = L < 256 ? 256 : L, PER = THREADS / L;
-  const int64_t blocks = (rows + PER - 1) / PER;
-  quant_int8_kernel<L, NV, THREADS, STAY><<<(uint32_t)blocks, THREADS, 0, st>>>(x, rows, (int)(cols / 8), ldx, q, scales);
+  const int64_t blocks = (rows + PER - 1) / PER, most = 1 << 20;   // a launch has 2^32 threads at most
+  quant_int8_kernel<L, NV, THREADS, STAY><<<(uint32_t)(blocks < most ? blocks : most), THREADS, 0, st>>>(x, rows, (int)(cols / 8), ldx, q, scales);
   return hipGetLastError();
 }
 
@@ -356,7 +359,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
     for (int j = 0; j < FM; ++j) sa[j] = p.as[cur.row0 + min(wm * T::WM + j * 16 + l16, cur.rows - 1)];
     uint8_t* scr = smem + T::LDS + w * T::OUT_BYTES;
     const int m_out = wm * T::WM + lane / 8, n_out = wn * T::WN + lane % 8 * 8;
-    uint16_t* out = p.out + (int64_t)(cur.row0 + m_out) * p.n + cur.col0 + n_out;
+    uint16_t* out = p.out + ((int64_t)cur.row0 + m_out) * p.n + cur.col0 + n_out;
 #pragma unroll
     for (int c = 0; c < FN / 4; ++c) {
       v4f sw[4];
@@ -527,7 +530,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_int8_kernel(const Int8Para
     float o[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[c] = (float)sum[c] * sa[q] * sw[q][c];
-    uint16_t* out = p.out + (int64_t)(pc.row0 + m) * p.n + col0 + n;
+    uint16_t* out = p.out + ((int64_t)pc.row0 + m) * p.n + col0 + n;
     const uint32_t d[2] = {bf16_pair(o[0], o[1]), bf16_pair(o[2], o[3])};
     if (left >= 4) memcpy(out, d, 8);
     else if (left > 0) store_some(out, d[0], d[1], 0, 0, left);

@@ -14,8 +14,9 @@ constexpr int64_t kTokenMaxCols = (int64_t)1 << 24;
 
 inline Check check_choices(int64_t tokens, int64_t top_k) {
   if (top_k < 1 || top_k > MXGG_MOE_MAX_TOP_K) return fail(MXGG_ERR_SHAPE, "top_k=%lld outside [1, 16]", top_k);
-  if (tokens < 0 || tokens >= ((int64_t)1 << 31) / top_k)
-    return fail(MXGG_ERR_SHAPE, "tokens=%lld: negative, or tokens * top_k >= 2^31", tokens);
+  // (the kernels number choices, and what lies up to a chunk behind them, in 32 bits)
+  if (tokens < 0 || tokens > ((int64_t)1 << 30) / top_k)
+    return fail(MXGG_ERR_SHAPE, "tokens=%lld: negative, or tokens * top_k > 2^30", tokens);
   return Check{};
 }
 

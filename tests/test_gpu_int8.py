@@ -45,6 +45,17 @@ def test_quantizer(rows, cols, pad):
         assert mxg.quantize_rowwise(x, "int8")[0].shape == (0, cols)
 
 
+def test_quantizer_more_rows_than_workgroups():
+    """2^20 workgroups at most, which stay for the rows behind."""
+    R = (1 << 20) + 700
+    x = torch.empty((R, 1040), dtype=torch.bfloat16, device="cuda").normal_(generator=gen(3))
+    q, s = mxg.quantize_rowwise(x, "int8")
+    for at in (slice(0, 3), slice((1 << 20) - 2, (1 << 20) + 2), slice(R - 3, R)):
+        wq, ws = ot.quantize_int8(f64(x[at]))
+        assert np.array_equal(host(q[at]), wq) and np.array_equal(host(s[at]), ws)
+    assert bool((q.abs().amax(1) == 127).all())
+
+
 def test_quantizer_all_ratios():
     """Every mantissa of the largest element, at the ends and in the middle of the
     exponents, against every bf16 value of the 11 binades from it downward, of

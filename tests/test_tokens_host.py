@@ -29,7 +29,7 @@ def test_sort_rules():
     assert sort() == HIP                                   # valid; no GPU to run it on
     assert sort(it=1) == HIP and sort(ldi=9) == HIP and sort(E=512) == HIP
     assert sort(it=2) == FORMAT and sort(k=0) == SHAPE and sort(k=17, ldi=17) == SHAPE and sort(ldi=7) == SHAPE
-    assert sort(T=-1) == SHAPE and sort(T=BIG // 8) == SHAPE and sort(E=0) == SHAPE and sort(E=513) == SHAPE
+    assert sort(T=-1) == SHAPE and sort(T=(BIG >> 4) + 1) == SHAPE and sort(T=1 << 20, ws=P, ws_bytes=BIG) == HIP and sort(E=0) == SHAPE and sort(E=513) == SHAPE
     assert sort(ids=None) == NULL and sort(rows=None) == NULL and sort(choices=None) == NULL and sort(counts=None) == NULL
     assert sort(ids=WORD) == HIP and sort(ids=WORD, it=1) == ALIGN and sort(rows=HALF) == ALIGN
     need = L.mxgg_moe_sort_workspace(4096, 8, 16)
@@ -57,7 +57,7 @@ def test_row_rules():
         assert f() == HIP and f(dt=1) == HIP
         assert f(dt=2) == FORMAT and f(C=0) == SHAPE and f(C=9) == SHAPE and f(k=0) == SHAPE and f(k=17) == SHAPE
         assert f(C=(1 << 24) + 1) == SHAPE
-        assert f(T=-1) == SHAPE and f(T=BIG // 2) == SHAPE and f(R=-1) == SHAPE and f(R=BIG) == SHAPE
+        assert f(T=-1) == SHAPE and f(T=(BIG >> 2) + 1) == SHAPE and f(T=BIG >> 2) == HIP and f(R=-1) == SHAPE and f(R=BIG) == SHAPE
         assert f(rows=None) == NULL and f(rows=HALF) == ALIGN
         assert f(T=0, rows=None) == OK
     assert dispatch(ldx=7) == SHAPE and dispatch(ldo=7) == SHAPE and dispatch(ldo=BIG) == SHAPE
