@@ -130,15 +130,30 @@ hipError_t quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx
 // ---------------------------------------------------------------------------
 // Product
 //
-// Weights are the MFMA's first operand, tokens the second: register i of a
-// 32x32 result is then channel 8 (i/4) + 4 (lane/32) + i%4 of token lane%32, four
-// neighbouring channels of one row.
+// Weights are the MFMA's first operand, tokens the second: register c of lane l of
+// a 16x16 result is then channel 4 (l / 16) + c of token l % 16, four neighbouring
+// channels of one row.
 //
 // A workgroup has 256 channels and 256 tokens at a time, and its eight waves 128 x
 // 64 of them each. Stages of 64 codes of every row come to LDS by DMA, four slots in
 // a ring that runs on over the workgroup's tiles. The two waves of a SIMD take
 // turns: while one reads a stage's operands from LDS and issues loads, the other
-// has the matrix unit to itself, and a barrier swaps them.
+// has the matrix unit to itself, and a barrier swaps them. Loads are through
+// buffers that end with the tile's rows, so what lies past an end is zeros without
+// a comparison.
+//
+// 16x16x64 MFMAs, not 32x32x32: both do the same operations a cycle, but a 32x32
+// result moves twice the accumulators, and while one wave's MFMAs ran the other's
+// twelve reads of a turn took 770 cycles of the SIMD's (310 alone), with 16x16 510
+// (8192 x 8192 x 8192: 488 us and 440).
+//
+// What bounds it: large products of real codes the power of the card. 8192^3 in
+// 440 us is 2500 Tops (a bf16 product reaches half of that); with zeros for codes the
+// same launch takes 319 us, 3450 Tops. Issuing the loads between the MFMAs instead of
+// in the other turn, and letting a tile's stores run on into the next tile, changed
+// nothing (438 -> 444 us). Of 64 experts with 512 rows each on average (32768 x 4096
+// x 7168, 990 us) a quarter of the tiles' rows are past an expert's end. A 128 x 128
+// tile brings a byte for 128 operations and is bound by that: 52 bytes a ns and CU.
 
 #define MXGG_LDS __attribute__((address_space(3)))
 
@@ -171,32 +186,36 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_buffer(const void* bas
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(((uint64_t)hi << 32) | lo), 0,
                                            (int)__builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 constexpr uint32_t kOutside = 0x80000000u;   // an offset past every buffer's end
 
 constexpr int kThreads = 512, kWaves = kThreads / 64;
 constexpr int kTileGroup = 4;
 
-// FN fragments of 16 channels and FM of 16 tokens for each of 2 x 4 waves; 64 KU
-// codes of a row in a stage
-template <int FN, int FM, int KU, int SLOTS>
+// FN fragments of 16 channels and FM of 16 tokens a wave; 64 KU codes of a row in a
+// stage. The waves are 2 x 4 over the tile, or with SPLIT 2 x 2 twice: each half
+// then multiplies every other stage.
+template <int FN, int FM, int KU, int SLOTS, bool SPLIT>
 struct Int8Tile {
   static constexpr int K = 64 * KU, CHUNKS = 4 * KU;
-  static constexpr int TN = 32 * FN, TM = 64 * FM, WN = 16 * FN, WM = 16 * FM;
+  static constexpr int WN = 16 * FN, WM = 16 * FM, TN = 2 * WN, TM = (SPLIT ? 2 : 4) * WM;
   static constexpr int W_BYTES = TN * K, STAGE = (TN + TM) * K, LDS = SLOTS * STAGE;
   // a wave's way out: 16 tokens of 64 channels, rows 16 bytes apart more
-  static constexpr int OUT_PITCH = 144, OUT_BYTES = 16 * OUT_PITCH, STORES = FM * FN / 2;
+  static constexpr int OUT_PITCH = 144, OUT_BYTES = 16 * OUT_PITCH;
   static constexpr int SMEM = LDS + kWaves * OUT_BYTES;
   // 1 KiB loads of a wave and stage
   static constexpr int LW = W_BYTES / (kWaves * 1024), LA = TM * K / (kWaves * 1024);
+  // loads of the stages that are on their way behind the awaited one
+  static constexpr int AHEAD = (SLOTS - 2) * (LW + LA);
   // rows of a load, and of a load of all waves
   static constexpr int LOAD_ROWS = 16 / KU, ROUND_ROWS = kWaves * LOAD_ROWS;
+  static constexpr int MORE = SLOTS - 1;                  // stages issued ahead
   static_assert(SMEM <= 154 * 1024 && LW >= 1 && LA >= 1 && FN % 4 == 0, "LDS: the ring beside the tables; whole loads");
 };
 
 struct Tile {
   int row0, g, col0, rows, cols;
 };
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // The first `left` (1 to 7) of eight bf16
 __device__ __forceinline__ void store_some(uint16_t* out, uint32_t d0, uint32_t d1, uint32_t d2, uint32_t d3, int left) {
@@ -209,35 +228,59 @@ __device__ __forceinline__ void store_some(uint16_t* out, uint32_t d0, uint32_t 
   if (left & 1) out[left & 6] = (uint16_t)(left & 2 ? b : a);
 }
 
-template <int FN, int FM, int KU, int SLOTS>
-__global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Params p) {
-  using T = Int8Tile<FN, FM, KU, SLOTS>;
-  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
-  __shared__ int32_t pref[kMaxExperts + 1], offs[kMaxExperts + 1];   // an expert's first row, and first tile
-  const int G = p.sp.G, nt = (int)((p.n + T::TN - 1) / T::TN);
-  {
-    int64_t* both = reinterpret_cast<int64_t*>(smem);                // the ring is not in use yet
+// Chunk c of a row lies at c ^ swizzle(row): the 16 rows of a fragment's read are
+// then spread over all banks.
+template <class T>
+__device__ __forceinline__ int swizzle(int row) {
+  return T::CHUNKS == 4 ? row / 4 % 4 : row / 2 % 8;
+}
+
+// The workgroup's tiles and the stages on their way: every wave issues its share
+// of one stage after the other, from tile to tile.
+template <class T>
+struct Int8Stream {
+  const Int8Params& p;
+  uint8_t* smem;
+  const int32_t *pref, *offs;       // LDS: an expert's first row, and first tile
+  int w, lane, nt, total, nb, first;
+  int stages;                       // of a tile; the last ones may lie behind the contraction's end
+  int it, is = 0, slot = 0;         // what is issued next
+  uint32_t lane_off;
+  int lane_k;                       // codes of the lane's chunk begin here in a stage
+  const uint8_t *base_w, *base_a;
+  uint32_t size_w = 0, size_a = 0;
+
+  __device__ __forceinline__ Int8Stream(const Int8Params& q, uint8_t* lds, int32_t* rows_at, int32_t* tiles_at,
+                                        int stages_of_a_tile)
+      : p(q), smem(lds), pref(rows_at), offs(tiles_at), stages(stages_of_a_tile) {
+    const int G = p.sp.G;
+    nt = (int)((p.n + T::TN - 1) / T::TN);
+    int64_t* both = reinterpret_cast<int64_t*>(smem);     // the ring is not in use yet
     block_prefix64<kThreads>(G, [&](int g) {
       return (int64_t)((p.sp.m[g] + T::TM - 1) / T::TM) << 32 | p.sp.m[g];
     }, both, both + kMaxExperts + 1);
     for (int g = threadIdx.x; g <= G; g += kThreads) {
-      pref[g] = (int32_t)both[g];
-      offs[g] = (int32_t)(both[g] >> 32) * nt;
+      rows_at[g] = (int32_t)both[g];
+      tiles_at[g] = (int32_t)(both[g] >> 32) * nt;
     }
     __syncthreads();
+    lane = threadIdx.x & 63;
+    w = uniform(threadIdx.x >> 6);
+    total = uniform(offs[G]);
+    nb = gridDim.x;
+    // neighbouring tiles on one XCD (workgroups are dealt round the 8 of them):
+    // they share operands in its L2
+    const int b = blockIdx.x;
+    first = it = nb % 8 == 0 ? (b % 8) * (nb / 8) + b / 8 : b;
+    const int r = w * T::LOAD_ROWS + lane / T::CHUNKS;
+    lane_k = ((lane % T::CHUNKS) ^ swizzle<T>(r)) * 16;
+    lane_off = (uint32_t)(r * p.k + lane_k);
+    base_w = p.w;
+    base_a = p.a;
   }
-
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4, h = lane / 16, l16 = lane % 16;
-  const int K = p.k, total = __builtin_amdgcn_readfirstlane(offs[G]), stages = (K + T::K - 1) / T::K;
-  const int nb = gridDim.x, b = blockIdx.x;
-  // neighbouring tiles on one XCD (workgroups are dealt round the 8 of them):
-  // they share operands in its L2
-  const int first = nb % 8 == 0 ? (b % 8) * (nb / 8) + b / 8 : b;
-
-  const auto find = [&](int t) {
+  __device__ __forceinline__ Tile find(int t) const {
     Tile o;
-    o.g = uniform(upper_bound_i32(offs, G + 1, t) - 1);
+    o.g = uniform(upper_bound_i32(offs, p.sp.G + 1, t) - 1);
     const int o0 = uniform(offs[o.g]), mt = (uniform(offs[o.g + 1]) - o0) / nt, local = t - o0;
     const int r0 = local / (kTileGroup * nt) * kTileGroup, hgt = min(mt - r0, kTileGroup), in = local - r0 * nt;
     const int ct = in / hgt, rt = r0 + in % hgt;
@@ -246,153 +289,230 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Par
     o.rows = min(p.sp.m[o.g] - rt * T::TM, T::TM);
     o.cols = (int)min(p.n - o.col0, (int64_t)T::TN);
     return o;
-  };
-
-  // Issuing side. Chunk c of a row lies at c ^ swizzle(row): the 16 rows of a
-  // fragment's read are then spread over all banks.
-  const auto swizzle = [](int row) { return KU == 1 ? row / 4 % 4 : row / 2 % 8; };
-  const int lr = w * T::LOAD_ROWS + lane / T::CHUNKS, lc = (lane % T::CHUNKS) ^ swizzle(lr);
-  const uint32_t lane_off = (uint32_t)(lr * K + lc * 16);
-  const int last_k = K - (stages - 1) * T::K;             // codes of the last stage
-  const bool lane_in_last = lc * 16 < last_k;
-  int it = first, is = 0, slot_issue = 0;
-  const uint8_t *base_w = p.w, *base_a = p.a;
-  uint32_t size_w = 0, size_a = 0;
-  const auto aim = [&]() {
+  }
+  __device__ __forceinline__ void aim() {
     size_w = size_a = 0;                                  // nothing left: zeros, that the counts go on
     if (it >= total) return;
     const Tile o = find(it);
-    base_w = p.w + ((int64_t)o.g * p.n + o.col0) * K;
-    base_a = p.a + (int64_t)o.row0 * K;
-    size_w = (uint32_t)(o.cols * K);
-    size_a = (uint32_t)(o.rows * K);
-  };
-  const auto issue = [&]() {
-    uint8_t* at = smem + slot_issue * T::STAGE + w * 1024;
+    base_w = p.w + ((int64_t)o.g * p.n + o.col0) * p.k;
+    base_a = p.a + (int64_t)o.row0 * p.k;
+    size_w = (uint32_t)(o.cols * p.k);
+    size_a = (uint32_t)(o.rows * p.k);
+  }
+  __device__ __forceinline__ void issue() const {
+    uint8_t* at = smem + slot * T::STAGE + w * 1024;
     const __amdgpu_buffer_rsrc_t bw = uniform_buffer(base_w, size_w), ba = uniform_buffer(base_a, size_a);
     // zeros behind the contraction's end, of the tokens (the weights may be anything)
-    const uint32_t wo = lane_off + (uint32_t)(is * T::K);
-    const uint32_t ao = is + 1 < stages || lane_in_last ? wo : kOutside;
+    const uint32_t wo = lane_off + (uint32_t)(is * T::K), round = (uint32_t)(T::ROUND_ROWS * p.k);
+    const uint32_t ao = is * T::K + lane_k < p.k ? wo : kOutside;
 #pragma unroll
     for (int i = 0; i < T::LW; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bw, (MXGG_LDS void*)(at + i * (kWaves * 1024)), 16,
-                                               wo + (uint32_t)(i * T::ROUND_ROWS * K), 0, 0, 0);
+                                               wo + (uint32_t)i * round, 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < T::LA; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ba, (MXGG_LDS void*)(at + T::W_BYTES + i * (kWaves * 1024)), 16,
-                                               ao + (uint32_t)(i * T::ROUND_ROWS * K), 0, 0, 0);
-  };
-  const auto advance = [&]() {
-    slot_issue = slot_issue + 1 == SLOTS ? 0 : slot_issue + 1;
+                                               ao + (uint32_t)i * round, 0, 0, 0);
+  }
+  __device__ __forceinline__ void advance() {
+    slot = slot + 1 == T::MORE + 1 ? 0 : slot + 1;
     if (++is == stages) {
       is = 0;
       it += nb;
       aim();
     }
-  };
-
-  if (first >= total) return;
-  aim();
-  for (int s = 0; s < SLOTS - 1; ++s) {
-    issue();
-    advance();
   }
-  constexpr int kAhead = (SLOTS - 2) * (T::LW + T::LA);   // loads of the stages behind the awaited one
-  wait_vmcnt<kAhead>();
-  raw_barrier();
-  if (turn) raw_barrier();                                // the second four waves are one turn behind
-  int slot = 0;
-  // a lane's piece u of a fragment of 16 rows: codes 64 u + 16 (lane / 16) .. of row lane % 16
-  int at_w[KU], at_a[KU];
-#pragma unroll
-  for (int u = 0; u < KU; ++u) {
-    const int piece = l16 * T::K + ((4 * u + h) ^ swizzle(l16)) * 16;
-    at_w[u] = wn * T::WN * T::K + piece;
-    at_a[u] = T::W_BYTES + wm * T::WM * T::K + piece;
-  }
-  for (int t = first; t < total; t += nb) {
-    const Tile cur = find(t);
-    const bool busy = wn * T::WN < cur.cols && wm * T::WM < cur.rows;   // else nothing of the wave's is stored
-    v4i acc[FN][FM];
-#pragma unroll
-    for (int i = 0; i < FN; ++i)
-#pragma unroll
-      for (int j = 0; j < FM; ++j) acc[i][j] = v4i{};
-    for (int s = 0; s < stages; ++s) {
-      v4i wf[KU][FN], af[KU][FM];
-      if (busy) {
-        const uint8_t* st = smem + slot * T::STAGE;
-#pragma unroll
-        for (int u = 0; u < KU; ++u) {
-#pragma unroll
-          for (int i = 0; i < FN; ++i) wf[u][i] = *reinterpret_cast<const v4i*>(st + at_w[u] + i * 16 * T::K);
-#pragma unroll
-          for (int j = 0; j < FM; ++j) af[u][j] = *reinterpret_cast<const v4i*>(st + at_a[u] + j * 16 * T::K);
-        }
-      }
-      slot = slot + 1 == SLOTS ? 0 : slot + 1;
+  // the ring filled, its first stage landed
+  __device__ __forceinline__ void start() {
+    aim();
+    for (int s = 0; s < T::MORE; ++s) {
       issue();
       advance();
-      wait_lds();
-      if (turn) wait_vmcnt<kAhead>();
-      raw_barrier();
-      if (busy) {
-        __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-        for (int u = 0; u < KU; ++u)
-#pragma unroll
-          for (int i = 0; i < FN; ++i)
-#pragma unroll
-            for (int j = 0; j < FM; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wf[u][i], af[u][j], acc[i][j], 0, 0, 0);
-        __builtin_amdgcn_s_setprio(0);
-      }
-      if (!turn) wait_vmcnt<kAhead>();
-      raw_barrier();
     }
-    // Epilogue: 16 tokens of 64 channels go through LDS and leave as whole lines.
-    if (!busy) continue;
-    const __amdgpu_buffer_rsrc_t scales =
-        uniform_buffer(p.ws + (int64_t)cur.g * p.n + cur.col0, (uint32_t)cur.cols * 4);
-    float sa[FM];
+    wait_vmcnt<T::AHEAD>();
+    raw_barrier();
+  }
+};
+
+// Operands of a stage in a wave's registers: fragments of 16 rows, of which lane l
+// holds codes 64 u + 16 (l / 16) .. of row l % 16.
+template <int FN, int FM, int KU, class T>
+struct Int8Operands {
+  v4i w[KU][FN], a[KU][FM];
+  __device__ __forceinline__ void read(const uint8_t* st, int wn, int wm, int lane) {
 #pragma unroll
-    for (int j = 0; j < FM; ++j) sa[j] = p.as[cur.row0 + min(wm * T::WM + j * 16 + l16, cur.rows - 1)];
-    uint8_t* scr = smem + T::LDS + w * T::OUT_BYTES;
-    const int m_out = wm * T::WM + lane / 8, n_out = wn * T::WN + lane % 8 * 8;
-    uint16_t* out = p.out + ((int64_t)cur.row0 + m_out) * p.n + cur.col0 + n_out;
+    for (int u = 0; u < KU; ++u) {
+      const int l16 = lane % 16, piece = l16 * T::K + ((4 * u + lane / 16) ^ swizzle<T>(l16)) * 16;
 #pragma unroll
-    for (int c = 0; c < FN / 4; ++c) {
-      v4f sw[4];
+      for (int i = 0; i < FN; ++i) w[u][i] = *reinterpret_cast<const v4i*>(st + wn * T::WN * T::K + piece + i * 16 * T::K);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        sw[i] = __builtin_bit_cast(
-            v4f, __builtin_amdgcn_raw_buffer_load_b128(scales, (wn * T::WN + c * 64 + i * 16 + 4 * h) * 4, 0, 0));
+      for (int j = 0; j < FM; ++j)
+        a[u][j] = *reinterpret_cast<const v4i*>(st + T::W_BYTES + wm * T::WM * T::K + piece + j * 16 * T::K);
+    }
+  }
+  __device__ __forceinline__ void multiply(v4i (&acc)[FN][FM]) const {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        wave_fence();
+    for (int u = 0; u < KU; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float o[4];
+      for (int i = 0; i < FN; ++i)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) o[r] = (float)acc[4 * c + i][j][r] * sa[j] * sw[i][r];
-          *reinterpret_cast<v2i*>(scr + l16 * T::OUT_PITCH + (i * 16 + 4 * h) * 2) =
-              v2i{(int)bf16_pair(o[0], o[1]), (int)bf16_pair(o[2], o[3])};
-        }
-        wave_fence();
+        for (int j = 0; j < FM; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[u][i], a[u][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_s_setprio(0);
+  }
+};
+
+template <int FN, int FM>
+__device__ __forceinline__ void clear(v4i (&acc)[FN][FM]) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const v4i o = *reinterpret_cast<const v4i*>(scr + (lane / 8 + 8 * k) * T::OUT_PITCH + lane % 8 * 16);
-          const int down = j * 16 + k * 8, left = cur.cols - n_out - c * 64;
-          uint16_t* to = out + (int64_t)down * p.n + c * 64;
-          if (m_out + down < cur.rows) {
-            if (left >= 8) memcpy(to, &o, 16);
-            else if (left > 0) store_some(to, o[0], o[1], o[2], o[3], left);
-          }
+  for (int i = 0; i < FN; ++i)
+#pragma unroll
+    for (int j = 0; j < FM; ++j) acc[i][j] = v4i{};
+}
+
+// A wave's sums, of channels n0 .. and tokens m0 .. of the tile, scaled and stored:
+// 16 tokens of 64 channels go through LDS and leave as whole lines.
+template <int FN, int FM, class T>
+__device__ __forceinline__ void store_sums(const Int8Params& p, const Tile& cur, const v4i (&acc)[FN][FM], int n0, int m0,
+                                           uint8_t* scr, int lane) {
+  const int h = lane / 16, l16 = lane % 16;
+  const __amdgpu_buffer_rsrc_t scales = uniform_buffer(p.ws + (int64_t)cur.g * p.n + cur.col0, (uint32_t)cur.cols * 4);
+  float sa[FM];
+#pragma unroll
+  for (int j = 0; j < FM; ++j) sa[j] = p.as[cur.row0 + min(m0 + j * 16 + l16, cur.rows - 1)];
+  const int m_out = m0 + lane / 8, n_out = n0 + lane % 8 * 8;
+  uint16_t* out = p.out + ((int64_t)cur.row0 + m_out) * p.n + cur.col0 + n_out;
+#pragma unroll
+  for (int c = 0; c < FN / 4; ++c) {
+    v4f sw[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      sw[i] = __builtin_bit_cast(
+          v4f, __builtin_amdgcn_raw_buffer_load_b128(scales, (n0 + c * 64 + i * 16 + 4 * h) * 4, 0, 0));
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      wave_fence();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float o[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[r] = (float)acc[4 * c + i][j][r] * sa[j] * sw[i][r];
+        *reinterpret_cast<v2i*>(scr + l16 * T::OUT_PITCH + (i * 16 + 4 * h) * 2) =
+            v2i{(int)bf16_pair(o[0], o[1]), (int)bf16_pair(o[2], o[3])};
+      }
+      wave_fence();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const v4i o = *reinterpret_cast<const v4i*>(scr + (lane / 8 + 8 * k) * T::OUT_PITCH + lane % 8 * 16);
+        const int down = j * 16 + k * 8, left = cur.cols - n_out - c * 64;
+        uint16_t* to = out + (int64_t)down * p.n + c * 64;
+        if (m_out + down < cur.rows) {
+          if (left >= 8) memcpy(to, &o, 16);
+          else if (left > 0) store_some(to, o[0], o[1], o[2], o[3], left);
         }
       }
     }
   }
+}
+
+template <int FN, int FM, int KU, int SLOTS>
+__global__ __launch_bounds__(kThreads, 1) void grouped_int8_kernel(const Int8Params p) {
+  using T = Int8Tile<FN, FM, KU, SLOTS, false>;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int32_t pref[kMaxExperts + 1], offs[kMaxExperts + 1];
+  Int8Stream<T> in(p, smem, pref, offs, (p.k + T::K - 1) / T::K);
+  const int w = in.w, lane = in.lane, turn = w / 4, wn = turn, wm = turn ? 3 - w % 4 : w % 4;
+  if (in.first >= in.total) return;
+  in.start();
+  if (turn) raw_barrier();                                // the second four waves are one turn behind
+  int slot = 0;
+  for (int t = in.first; t < in.total; t += in.nb) {
+    const Tile cur = in.find(t);
+    const bool busy = wn * T::WN < cur.cols && wm * T::WM < cur.rows;   // else nothing of the wave's is stored
+    v4i acc[FN][FM];
+    clear(acc);
+    for (int s = 0; s < in.stages; ++s) {
+      Int8Operands<FN, FM, KU, T> f;
+      if (busy) f.read(smem + slot * T::STAGE, wn, wm, lane);
+      slot = slot + 1 == SLOTS ? 0 : slot + 1;
+      in.issue();
+      in.advance();
+      wait_lds();
+      if (turn) wait_vmcnt<T::AHEAD>();
+      raw_barrier();
+      if (busy) f.multiply(acc);
+      if (!turn) wait_vmcnt<T::AHEAD>();
+      raw_barrier();
+    }
+    if (busy) store_sums<FN, FM, T>(p, cur, acc, wn * T::WN, wm * T::WM, smem + T::LDS + w * T::OUT_BYTES, lane);
+  }
   if (!turn) raw_barrier();
+  wait_vmcnt<0>();
+}
+
+// The same for smaller tiles, where a turn of half the waves would have too few
+// MFMAs for its reads and barriers: the halves take every other stage, all of the
+// tile each, and a stage ends with every turn. At a tile's end each half has a sum of
+// its own; they give each other the sums of half the tokens, through the slot of the
+// last stage, which no load goes to meanwhile.
+template <int FN, int FM, int KU, int SLOTS>
+__global__ __launch_bounds__(kThreads, 1) void split_int8_kernel(const Int8Params p) {
+  using T = Int8Tile<FN, FM, KU, SLOTS, true>;
+  static_assert(FM % 2 == 0 && T::STAGE >= kWaves * FN * 1024, "exchange of 16 tokens a wave in a slot");
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int32_t pref[kMaxExperts + 1], offs[kMaxExperts + 1];
+  // an even number of stages (one may hold zeros only)
+  Int8Stream<T> in(p, smem, pref, offs, (p.k + 2 * T::K - 1) / (2 * T::K) * 2);
+  const int w = in.w, lane = in.lane, turn = w / 4, wn = w % 4 / 2, wm = w % 2;
+  if (in.first >= in.total) return;
+  in.start();
+  int slot = 0;                                           // of the stage that this turn reads
+  const auto turn_ends = [&](bool issued) {
+    if (issued) in.advance();
+    wait_lds();
+    if (issued) wait_vmcnt<T::AHEAD>();
+    raw_barrier();
+    slot = slot + 1 == SLOTS ? 0 : slot + 1;
+  };
+  for (int t = in.first; t < in.total; t += in.nb) {
+    const Tile cur = in.find(t);
+    v4i acc[FN][FM];
+    clear(acc);
+    if (turn) {
+      in.issue();
+      turn_ends(true);
+    }
+    for (int s = 0; s < in.stages; s += 2) {
+      Int8Operands<FN, FM, KU, T> f;
+      f.read(smem + slot * T::STAGE, wn, wm, lane);
+      in.issue();
+      turn_ends(true);
+      const bool more = !turn || s + 2 < in.stages;       // the tile's stages are as many as its turns that issue
+      if (more) in.issue();
+      f.multiply(acc);
+      if (more) turn_ends(true);
+    }
+    // (its last reads were done before the last barrier)
+    uint8_t* last = smem + (slot == 0 ? SLOTS - 1 : slot - 1) * T::STAGE;
+    v4i mine[FN][FM / 2];
+#pragma unroll
+    for (int j = 0; j < FM / 2; ++j) {
+      // wave w gives to w ^ 4 and takes what that gives
+      v4i* give = reinterpret_cast<v4i*>(last + w * (FN * 1024)) + lane;
+      const v4i* take = reinterpret_cast<const v4i*>(last + (w ^ 4) * (FN * 1024)) + lane;
+#pragma unroll
+      for (int i = 0; i < FN; ++i) give[i * 64] = turn ? acc[i][j] : acc[i][j + FM / 2];
+      wait_lds();
+      raw_barrier();
+#pragma unroll
+      for (int i = 0; i < FN; ++i) mine[i][j] = (turn ? acc[i][j + FM / 2] : acc[i][j]) + take[i * 64];
+      wait_lds();
+      raw_barrier();
+    }
+    const int m0 = wm * T::WM + turn * (T::WM / 2);
+    if (wn * T::WN < cur.cols && m0 < cur.rows)
+      store_sums<FN, FM / 2, T>(p, cur, mine, wn * T::WN, m0, smem + T::LDS + w * T::OUT_BYTES, lane);
+  }
   wait_vmcnt<0>();
 }
 
@@ -546,13 +666,12 @@ hipError_t few_int8(const Int8Params& p, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int FN, int FM, int KU, int SLOTS>
-hipError_t tile_int8(const Int8Params& p, int num_cus, hipStream_t st) {
-  using T = Int8Tile<FN, FM, KU, SLOTS>;
-  const hipError_t e = ensure_dynamic_lds((const void*)grouped_int8_kernel<FN, FM, KU, SLOTS>, T::SMEM, st);
+template <class T>
+hipError_t tile_int8(void (*kernel)(Int8Params), const Int8Params& p, int num_cus, hipStream_t st) {
+  const hipError_t e = ensure_dynamic_lds((const void*)kernel, T::SMEM, st);
   if (e != hipSuccess) return e;
   const int64_t tiles = int8_pieces(p.sp, T::TM) * ((p.n + T::TN - 1) / T::TN);
-  grouped_int8_kernel<FN, FM, KU, SLOTS><<<(uint32_t)(tiles < num_cus ? tiles : num_cus), kThreads, T::SMEM, st>>>(p);
+  kernel<<<(uint32_t)(tiles < num_cus ? tiles : num_cus), kThreads, T::SMEM, st>>>(p);
   return hipGetLastError();
 }
 
@@ -570,8 +689,8 @@ hipError_t launch_quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int6
 
 hipError_t launch_grouped_int8(const Int8Params& p, int num_cus, hipStream_t st) {
   switch (int8_form(p.sp, p.n, p.k, num_cus)) {
-    case kInt8Big: return tile_int8<8, 4, 1, 4>(p, num_cus, st);
-    case kInt8Small: return tile_int8<4, 2, 2, 4>(p, num_cus, st);
+    case kInt8Big: return tile_int8<Int8Tile<8, 4, 1, 4, false>>(grouped_int8_kernel<8, 4, 1, 4>, p, num_cus, st);
+    case kInt8Small: return tile_int8<Int8Tile<4, 4, 2, 4, true>>(split_int8_kernel<4, 4, 2, 4>, p, num_cus, st);
     case kInt8Few11: return few_int8<1, 1>(p, st);
     case kInt8Few12: return few_int8<1, 2>(p, st);
     case kInt8Few21: return few_int8<2, 1>(p, st);

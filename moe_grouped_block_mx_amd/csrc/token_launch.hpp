@@ -94,29 +94,31 @@ enum Int8Form { kInt8Big, kInt8Small, kInt8Few11, kInt8Few12, kInt8Few21, kInt8F
 // part that grows with K, in units of 16 rows of codes brought to a CU (at K = 4096
 // 1.5 us), and one that does not (start, results, the wait for the first loads),
 // which is less where two workgroups fit on a CU. The forms of few tokens bring the
-// rows of their channels and tokens; a 128 x 128 tile's loads overlap more (12.3
+// rows of their channels and tokens; a 128 x 128 tile's loads overlap more (11.5
 // units for 16), a 256 x 256 tile's time is its MFMAs'.
-// Measured, us (one expert unless said; tokens, channels, K):
-//                                   256    128    64 x 64   32 x 32
-//   64, 4096, 4096                   51     25      16        10
-//   256, 4096, 4096                  58     25      16        27
-//   512, 4096, 4096                  56     25      29        50
-//   512, 1111, 2000                  35     16      10        16
-//   1024, 1024, 8192                 82     37      23
-//   1024, 8192, 1024                 23     20      39
-//   2048, 4096, 4096                 56     45      92
-//   2048, 8192, 1024                 25     34      77
-//   4096, 4096, 4096                 65     83     179
-//   1024 of 32 experts, 4096, 4096  138    125     144
-//   4096 of 32                      187    152     266
-//   8192 of 32                      203    225     446
-//   8192 of 64, 4096, 7168          504    476     844
-//   16384 of 64                     620    739
-// and for the fewest tokens, 16 x 16, 32 x 16 (channels x tokens):
-//   1, 4096, 7168                   7.9   11.3
-//   1, 8192, 1024                   4.4    4.1
-//   64 of 128 experts, 2048, 7168   142    134
-//   256 of 32, 4096, 4096           126    105
+// Measured, us (one expert unless said; tokens, channels, K; medians of replays, the
+// weights of several layers in turn; the form that the rule takes is marked):
+//                                    256    128    64 x 64  64 x 32  32 x 32  32 x 16  16 x 16
+//   1, 4096, 7168                     71     32      21       19       12       12       8.2*
+//   1, 8192, 1024                     18     10      6.7      6.0      5.2      4.5*     4.8
+//   32, 4096, 4096                    43     20      12       10       8.2      7.1*     8.3
+//   64, 4096, 4096                    44     20      12       10       9.1*     11       13
+//   256, 4096, 4096                   48     21      15*      21       26       29       38
+//   512, 4096, 4096                   48     22*     27       40       48       53       70
+//   512, 1111, 2000                   36     16      9.9*     13       16       15       17
+//   1024, 1024, 8192                  84     35      23*      32       40       50       63
+//   1024, 8192, 1024                  23     19*     40       60       95       87       140
+//   2048, 4096, 4096                  51     43*     92       148
+//   2048, 8192, 1024                  26*    32      78       119
+//   4096, 4096, 4096                  62*    78
+//   64 of 128 experts, 2048, 7168     171    128     148      141      147      126*     132
+//   256 of 32, 4096, 4096             141    126     128      120      137      109*     132
+//   1024 of 32, 4096, 4096            143    125*    144      153      193      191      251
+//   4096 of 32, 4096, 4096            188    153*
+//   8192 of 32, 4096, 4096            204*   221
+//   8192 of 64, 4096, 7168            520    482*
+//   16384 of 64, 4096, 7168           640*   730
+// (32 x 64 and 16 x 32 are for the tokens in between, as 40 and 20.)
 inline Int8Form int8_form(const SplitArgs& sp, int64_t n, int64_t k, int num_cus) {
   struct Option {
     Int8Form form;
@@ -124,9 +126,9 @@ inline Int8Form int8_form(const SplitArgs& sp, int64_t n, int64_t k, int num_cus
     float units, fixed;   // units 0: the rows that a workgroup brings
   };
   static constexpr Option options[] = {
-      {kInt8Big, 256, 256, 29.f, 8.f},     {kInt8Small, 128, 128, 12.3f, 2.3f}, {kInt8Few11, 16, 16, 0, 0.5f},
-      {kInt8Few21, 32, 16, 0, 0.5f},       {kInt8Few12, 16, 32, 0, 0.5f},       {kInt8Few22, 32, 32, 0, 1.3f},
-      {kInt8Few24, 32, 64, 0, 1.3f},       {kInt8Few42, 64, 32, 0, 1.3f},       {kInt8Few44, 64, 64, 0, 1.3f}};
+      {kInt8Big, 256, 256, 29.f, 8.f},     {kInt8Small, 128, 128, 11.5f, 2.2f}, {kInt8Few11, 16, 16, 0, 0.5f},
+      {kInt8Few21, 32, 16, 0, 0.5f},       {kInt8Few12, 16, 32, 0, 0.5f},       {kInt8Few22, 32, 32, 0, 1.6f},
+      {kInt8Few24, 32, 64, 0, 1.6f},       {kInt8Few42, 64, 32, 0, 1.6f},       {kInt8Few44, 64, 64, 0, 1.6f}};
   int64_t rows = 0;
   for (int g = 0; g < sp.G; ++g) rows += sp.m[g];
   Int8Form best = kInt8Big;

@@ -107,13 +107,14 @@ def check(splits, N, K, seed=0):
     ([250], 4100, 96), ([33] * 9, 1030, 592), ([16], 16000, 4096), ([48], 4100, 4096), ([24], 4099, 4096), ([60], 4095, 2000),
     # ... 128 x 128 tiles, and 256 x 256, with rounds of both
     ([1024], 4096, 144), ([700, 0, 1300, 77], 3001, 272), ([100] * 20, 2000, 64), ([4096], 4096, 144),
-    ([1300, 0, 2900, 77], 4004, 208), ([257] * 12, 4099, 80), ([9000], 2050, 336)])
+    ([1300, 0, 2900, 77], 4004, 208), ([257] * 12, 4099, 80), ([9000], 2050, 336),
+    ([3000, 1500, 2500], 4099, 176)])
 def test_product(splits, N, K):
     check(splits, N, K)
 
 
-OPTIONS = [(256, 256, 29, 8), (128, 128, 12.3, 2.3), (16, 16, 0, .5), (32, 16, 0, .5), (16, 32, 0, .5), (32, 32, 0, 1.3),
-           (32, 64, 0, 1.3), (64, 32, 0, 1.3), (64, 64, 0, 1.3)]
+OPTIONS = [(256, 256, 29, 8), (128, 128, 11.5, 2.2), (16, 16, 0, .5), (32, 16, 0, .5), (16, 32, 0, .5), (32, 32, 0, 1.6),
+           (32, 64, 0, 1.6), (64, 32, 0, 1.6), (64, 64, 0, 1.6)]
 
 
 def form(splits, N, K):
