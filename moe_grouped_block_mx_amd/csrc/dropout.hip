@@ -11,6 +11,10 @@
 // 16 bits an element, so a group of eight columns takes one call of 20 wide
 // multiplications: p is rounded to 2^-16, and the scale is that of the rounded
 // one, so the expectation is exact.
+//
+// What bounds it: the bytes. bf16 16384 x 7168: 101 us without a residual (4.7 TB/s;
+// with 32 bits an element, two calls a group, 121), 138 us with one (5.1 TB/s; 142).
+// A plain copy reaches 5.1 TB/s. 8 x 4096 takes 5.5 us, a launch and two latencies.
 #include "block_common.hpp"
 #include "token_launch.hpp"
 

@@ -23,6 +23,9 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 // reciprocal and then corrected by its remainder, so a quotient half way between
 // two integers is seen as that and goes to the even one (any other is at least
 // 2^-9 away from half way, far more than the approximation is off).
+//
+// What bounds it: the bytes. 65536 x 512 22 us (4.6 TB/s), 16384 x 7168 63 us (5.6),
+// 4096 x 20480, read twice, 53 us (the second time from cache); 1 x 7168 2.6 us.
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   typedef uint16_t v2u __attribute__((ext_vector_type(2)));
@@ -525,6 +528,10 @@ __global__ __launch_bounds__(kThreads, 1) void split_int8_kernel(const Int8Param
 // 64-code steps to a ring of its own in LDS and waits for its own loads only.
 // (Straight to registers a lane would load 16 bytes of another row than its
 // neighbour does, which takes the address unit a cycle a lane.)
+//
+// What bounds it: reading the weights. 64 rows of 128 experts, 2048 x 7168: 110 us for
+// the 620 MB of the experts that have any (5.7 TB/s, as a plain read); one row, 4096 x
+// 7168: 7 us, of which 5.2 are for the 29 MB.
 
 constexpr int kFewWaves = 8;
 constexpr int few_slots(int nf, int mf) { return nf + mf <= 2 ? 4 : nf + mf <= 3 ? 3 : nf + mf <= 4 ? 4 : nf + mf <= 6 ? 3 : 2; }

@@ -13,12 +13,16 @@ namespace mxgg {
 // Up to kSortOne choices are sorted by one workgroup in one launch. More are cut
 // into chunks of kSortChunk, a workgroup each, that meet in a table (in the
 // workspace): one row of experts + 1 counts a chunk (the last: dropped choices).
+// Measured, us, one launch and chunks: 4096 choices of 8 experts 5.8 and 7.2, of 511
+// 7.9 and 8.2; 8192 of 8 experts 9.6 and 7.3, of 128 12.6 and 7.9.
 constexpr int kSortOne = 4096, kSortChunk = 2048;
 inline int64_t sort_chunks(int64_t choices) {
   return choices <= kSortOne ? 1 : (choices + kSortChunk - 1) / kSortChunk;
 }
 // Up to so many workgroups, each adds up the table's rows before its own
-// itself; beyond, a launch between does it for all.
+// itself; beyond, a launch between does it for all. Measured, us, without the launch
+// and with it: 16 chunks of 128 experts 9.0 and 9.7; 64 of 8 experts 8.0 and 8.8; 128
+// of 128 experts 11.5 and 11.6; 256 of 128 experts 15.5 and 14.1, of 511 22 and 17.
 constexpr int64_t kSortDirect = 128;
 inline size_t sort_workspace(int64_t choices, int64_t experts) {
   const int64_t chunks = sort_chunks(choices);
