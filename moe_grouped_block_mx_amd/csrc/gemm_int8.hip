@@ -678,7 +678,10 @@ hipError_t tile_int8(void (*kernel)(Int8Params), const Int8Params& p, int num_cu
   const hipError_t e = ensure_dynamic_lds((const void*)kernel, T::SMEM, st);
   if (e != hipSuccess) return e;
   const int64_t tiles = int8_pieces(p.sp, T::TM) * ((p.n + T::TN - 1) / T::TN);
-  kernel<<<(uint32_t)(tiles < num_cus ? tiles : num_cus), kThreads, T::SMEM, st>>>(p);
+  // Whole eights, so that neighbouring tiles meet on an XCD (a workgroup without a tile
+  // ends at once): 2999 rows of 5 experts, 1111 x 2000, 20.3 -> 18.1 us.
+  const int64_t grid = (tiles + 7) / 8 * 8;
+  kernel<<<(uint32_t)(grid < num_cus ? grid : num_cus), kThreads, T::SMEM, st>>>(p);
   return hipGetLastError();
 }
 
