@@ -60,15 +60,19 @@ class MoEBlock(torch.nn.Module):
         y, _, _ = mxg.moe_layer(n, n @ self.gate.t(), w13_q, w13_s, w2_q, w2_s, self.top_k, fmt=fmt, w2_fmt=w2_fmt)
         return x + y
 
+    def int8_weights(self):
+        """The experts in 8-bit integers, for prefill."""
+        return self.fc1.int8_weight(), self.fc2.int8_weight()
+
     @torch.no_grad()
-    def prefill(self, x):
-        """Serving: x bf16 [tokens, hidden], any number of tokens, 8-bit integers."""
+    def prefill(self, x, weights):
+        """Serving: x bf16 [tokens, hidden], any number of tokens, on int8_weights()."""
         n, _, _ = mxg.layer_norm_fwd(x, self.norm.weight, self.norm.bias, self.norm.eps)
         top, ids = torch.topk(n @ self.gate.t(), self.top_k, dim=1)
         plan = TokenPlan(ids, self.experts)
         splits = plan.m_splits()
-        gate, up = self.fc1.forward_int8(dispatch(n, plan), splits).chunk(2, dim=1)
-        out = self.fc2.forward_int8(torch.nn.functional.silu(gate) * up, splits)
+        gate, up = self.fc1.forward_int8(dispatch(n, plan), splits, weights[0]).chunk(2, dim=1)
+        out = self.fc2.forward_int8(torch.nn.functional.silu(gate) * up, splits, weights[1])
         return x + combine(out, torch.softmax(top.float(), dim=1), plan)
 
     def gradients(self):
@@ -125,7 +129,7 @@ def main(argv=None):
     x = torch.randn((a.tokens, a.hidden), device="cuda", generator=g).bfloat16()
     with torch.no_grad():
         trained = block(x).float()
-    prompt = float((block.prefill(x).float() - trained).norm() / (trained - x.float()).norm())
+    prompt = float((block.prefill(x, block.int8_weights()).float() - trained).norm() / (trained - x.float()).norm())
     print(f"{a.tokens} tokens served in 8-bit integers: {prompt:.4f} of it (whose weights have 4 bits)")
     return history, off
 

@@ -116,7 +116,7 @@ enum Int8Form { kInt8Big, kInt8Small, kInt8Few11, kInt8Few12, kInt8Few21, kInt8F
 //   2048, 8192, 1024                  26*    32      78       119
 //   4096, 4096, 4096                  62*    78
 //   64 of 128 experts, 2048, 7168     171    128     148      141      147      126*     132
-//   256 of 32, 4096, 4096             141    126     128      120      137      109*     132
+//   256 of 32, 4096, 4096             141    126     128      120*     137      110      132
 //   1024 of 32, 4096, 4096            143    125*    144      153      193      191      251
 //   4096 of 32, 4096, 4096            188    153*
 //   8192 of 32, 4096, 4096            204*   221

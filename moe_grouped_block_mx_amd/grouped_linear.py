@@ -173,7 +173,6 @@ class GroupedLinear(torch.nn.Module):
                                             device=device)
         self.weight.overwrite_main_grad = False
         self._cache = _WeightCache()
-        self._int8 = None
         self._pending = []
 
     def forward(self, x, m_splits, is_first_microbatch=None, out=None, dgrad_out=None):
@@ -200,19 +199,17 @@ class GroupedLinear(torch.nn.Module):
         return q, s, L.FORMATS[f] if isinstance(f, str) else f
 
     def int8_weight(self):
-        """(codes, scales) of the weight in 8-bit integers with a scale per output
-        channel, quantized again only when the weight changed."""
-        key = (self.weight.data_ptr(), self.weight._version)
-        if self._int8 is None or self._int8[0] != key:
-            self._int8 = (key, *L.mxgg_quantize_rowwise(self.weight.detach(), L.INT8))
-        return self._int8[1:]
+        """(codes, scales) of the weight as it is now, in 8-bit integers with a scale
+        per output channel: what a server keeps and gives to forward_int8."""
+        return L.mxgg_quantize_rowwise(self.weight.detach(), L.INT8)
 
     @torch.no_grad()
-    def forward_int8(self, x, m_splits):
+    def forward_int8(self, x, m_splits, weight=None):
         """The layer in 8-bit integers, for serving (no gradient): x bf16 [M, K]
-        quantized per token, times int8_weight(). in_features a multiple of 16."""
+        quantized per token, times `weight`, which int8_weight() made (None: made for
+        this call). in_features a multiple of 16."""
         q, scales = L.mxgg_quantize_rowwise(x, L.INT8)
-        w_q, w_s = self.int8_weight()
+        w_q, w_s = self.int8_weight() if weight is None else weight
         return L.mxgg_grouped_fwd(q, scales, w_q, w_s, [int(m) for m in m_splits], self.out_features, self.in_features,
                                   a_fmt=L.INT8, w_fmt=L.INT8)
 

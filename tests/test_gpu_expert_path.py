@@ -180,10 +180,9 @@ def test_layer_in_int8():
         want = ot.grouped_int8(q, s, wq.reshape(3, 72, 160), ws.reshape(3, 72), [20, 0, 30])
         assert (np.abs(f64(got) - want) <= (2.0 ** -8 + 4 * U) * np.abs(want)).all()
         held = layer.int8_weight()
-        assert layer.int8_weight()[0] is held[0]            # quantized once ...
-        with torch.no_grad():
-            layer.weight.mul_(1.5)
-        assert layer.int8_weight()[0] is not held[0]        # ... for each version of the weight
+        layer.weight.data.mul_(-2)                           # nothing is kept that misses this
+        assert torch.equal(layer.forward_int8(x, [20, 0, 30], held), got)
+        assert torch.equal(layer.forward_int8(x, [20, 0, 30]), -2 * got)
 
 
 def test_example_block():
@@ -195,7 +194,7 @@ def test_example_block():
     g = torch.Generator("cuda").manual_seed(1)
     block = m.MoEBlock(256, 128, 6, 2, generator=g).eval()
     x = torch.randn((300, 256), device="cuda", generator=g).bfloat16()
-    out = block.prefill(x)
+    out = block.prefill(x, block.int8_weights())
     n, _, _ = mxg.layer_norm_fwd(x, block.norm.weight, block.norm.bias, block.norm.eps)
     top, ids = torch.topk(n @ block.gate.t(), 2, dim=1)
     rows, choices, counts = mxg.moe_sort(ids, 6)
