@@ -245,7 +245,7 @@ mxgg_status mxgg_mx_scales_relayout(const void* src, mxgg_scale_layout src_layou
  *           MXGG_FP8_1x128: blocks of 128 along cols (cols % 128 == 0).
  *           MXGG_FP8_128x128: 128x128 blocks (rows % 128 == 0, cols % 128 == 0).
  *           MXGG_INT8: whole rows (cols % 16 == 0, cols < 2^17).
- *   flags   MXGG_POW2_SCALES for the blockwise formats (ignored for MX).
+ *   flags   MXGG_POW2_SCALES for the blockwise formats (ignored for MX and INT8).
  *   q       MXFP4: u8 [rows, cols/2]; MXFP8: u8 [rows, cols]; blockwise: E4M3
  *           codes u8 [cols/64, rows, 64] (64-byte blocks along cols).
  *   scales  MX: u8 [cols/32, R4] (block-major, R4 = mxgg_mx_scale_stride(rows)),
@@ -626,6 +626,7 @@ typedef enum mxgg_itype { MXGG_I32 = 0, MXGG_I64 = 1 } mxgg_itype;
  *            the number of choices that were not dropped (on the host they are
  *            the m_splits of the grouped GEMMs).
  *   ws       mxgg_moe_sort_workspace(...) bytes, 16-byte aligned (NULL when 0).
+ * What is written overlaps neither ids nor each other.
  * tokens >= 0, tokens * top_k <= 2^30, top_k in [1, 16], experts in [1, 512].
  * tokens == 0 clears the counts. Errors: NULL, SHAPE, FORMAT, ALIGN, WORKSPACE,
  * DEVICE, ARCH, HIP.
@@ -659,7 +660,8 @@ mxgg_status mxgg_moe_dispatch(const void* x, int64_t ldx, mxgg_dtype dtype, int6
  *   y        [expert_rows, cols] of `dtype`, leading dimension ldy. A place from
  *            expert_rows on counts as dropped.
  *   weights  fp32 [tokens, top_k] or NULL (1).
- *   out      [tokens, cols] of `dtype`, leading dimension ldo; not y.
+ *   out      [tokens, cols] of `dtype`, leading dimension ldo; does not
+ *            overlap y.
  * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
  */
 mxgg_status mxgg_moe_combine(const void* y, int64_t ldy, mxgg_dtype dtype, int64_t expert_rows, int64_t cols,
@@ -671,8 +673,8 @@ mxgg_status mxgg_moe_combine(const void* y, int64_t ldy, mxgg_dtype dtype, int64
  *   dy[rows[t, j]] = weights[t, j] dout[t], zeros at the place of a dropped choice
  *   dweights[t, j] = sum_c dout[t, c] y[rows[t, j], c] in fp32 (one fixed order),
  *                    0 for a dropped choice
- *   dy       [expert_rows, cols] of `dtype`, leading dimension lddy; may be y.
- *            Rows that no place names stay as they were.
+ *   dy       [expert_rows, cols] of `dtype`, leading dimension lddy; may be y
+ *            (else overlaps no input). Rows that no place names stay as they were.
  * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
  */
 mxgg_status mxgg_moe_combine_bwd(const void* dout, int64_t lddo, const void* y, int64_t ldy, mxgg_dtype dtype,

@@ -757,11 +757,12 @@ def _rows_index(rows):
     return shape
 
 
-def _like_rows(t, name, n, cols, x):
+def _like_rows(t, name, n, cols, x, named=None):
     """[n, cols] of x's type, the caller's or a new one, and its leading dimension.
-    (That it is on x's device the library checks, as of every pointer.)"""
+    Of a new one only `named` rows may be written, the others are zeros. (That it
+    is on x's device the library checks, as of every pointer.)"""
     if t is None:
-        return x.new_empty((n, cols)), cols
+        return x.new_empty((n, cols)) if named is None or n <= named else x.new_zeros((n, cols)), cols
     if t.shape != (n, cols) or t.dtype is not x.dtype:
         raise ValueError(f"{name} must be a {str(x.dtype).replace('torch.', '')} tensor [{n}, {cols}], got "
                          f"{str(t.dtype).replace('torch.', '')} {tuple(t.shape)}")
@@ -801,7 +802,8 @@ def mxgg_moe_dispatch(x, rows, expert_rows=None, out=None):
     """Tokens' rows to the places of their choices: out[rows[t, j]] = x[t], zeros
     at the places of dropped ones. x: bf16 or fp32 [tokens, cols] (any row
     stride); rows from moe_sort; expert_rows: the rows of out (tokens * top_k, or
-    sum(m_splits) to leave the dropped ones out)."""
+    sum(m_splits) to leave the dropped ones out; rows behind them are zeros, of a
+    given out left as they were)."""
     dt, ldx = _dtype(x, "x"), _lead(x, "x")
     T, k = _rows_index(rows)
     n, cols = x.shape
@@ -809,7 +811,7 @@ def mxgg_moe_dispatch(x, rows, expert_rows=None, out=None):
         raise ValueError(f"x has {n} rows, rows is of {T} tokens")
     if expert_rows is None:
         expert_rows = T * k if out is None else out.shape[0]
-    out, ldo = _like_rows(out, "out", expert_rows, cols, x)
+    out, ldo = _like_rows(out, "out", expert_rows, cols, x, T * k)
     _check(lib.mxgg_moe_dispatch(x.data_ptr(), ldx, dt, T, cols, rows.data_ptr(), k, out.data_ptr(), ldo, expert_rows,
                                  _stream_of(x)))
     return out
@@ -833,7 +835,8 @@ def mxgg_moe_combine(y, rows, weights=None, out=None):
 
 def mxgg_moe_combine_bwd(dout, y, rows, weights, dy=None, dweights=None):
     """The gradients of moe_combine: (dy, dweights), dy like y (zeros at the
-    places of dropped choices), dweights fp32 [tokens, top_k]."""
+    places of dropped choices and in rows behind all; a given dy keeps those),
+    dweights fp32 [tokens, top_k]."""
     dt, ldy = _dtype(y, "y"), _lead(y, "y")
     T, k = _rows_index(rows)
     if dout is None:
@@ -841,7 +844,7 @@ def mxgg_moe_combine_bwd(dout, y, rows, weights, dy=None, dweights=None):
     n, cols = y.shape
     dout, lddo = _like_rows(dout, "dout", T, cols, y)
     _expect(weights, "weights", (T, k), _f32_t)
-    dy, lddy = _like_rows(dy, "dy", n, cols, y)
+    dy, lddy = _like_rows(dy, "dy", n, cols, y, T * k)
     dweights = y.new_empty((T, k), dtype=_f32_t) if dweights is None else _expect(dweights, "dweights", (T, k), _f32_t)
     _check(lib.mxgg_moe_combine_bwd(dout.data_ptr(), lddo, y.data_ptr(), ldy, dt, n, cols, rows.data_ptr(),
                                     weights.data_ptr(), T, k, dy.data_ptr(), lddy, dweights.data_ptr(), _stream_of(y)))

@@ -60,9 +60,7 @@ class _CombineFn(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dout):
         y, weights, rows = ctx.saved_tensors
-        # rows that no place names (there are more than choices) have no gradient
-        dy = y.new_zeros(y.shape) if y.shape[0] > rows.numel() else None
-        dy, dweights = L.mxgg_moe_combine_bwd(_rows(dout), y, rows, weights, dy=dy)
+        dy, dweights = L.mxgg_moe_combine_bwd(_rows(dout), y, rows, weights)
         return dy, dweights, None
 
 

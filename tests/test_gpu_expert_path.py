@@ -94,6 +94,8 @@ def test_rows_that_no_choice_names():
     y = torch.randn((25, 40), device="cuda", requires_grad=True)
     combine(y, w, plan).backward(d)
     assert not y.grad[18:].any() and y.grad[:18].any(1).all()
+    out = dispatch(x.detach(), plan, 25)
+    assert torch.equal(out[:18], dispatch(x.detach(), plan)) and not out[18:].any()
 
 
 def test_noncontiguous_and_broadcast_gradients():

@@ -156,10 +156,11 @@ def test_offsets_past_32_bits():
     assert torch.equal(back, x) and not buf[:, 200:].any()
 
 
-def test_streams_and_graph():
+@pytest.mark.parametrize("T", [700, 2000])                  # one launch of the sort, and two
+def test_streams_and_graph(T):
     """Another stream, and a captured sort, dispatch, combine and gradient replayed
     on new inputs with eager work between."""
-    T, k, E, C = 700, 4, 24, 513
+    k, E, C = 4, 24, 513
     g = gen(3)
     ids, x = choices(g, T, k, E, 0.2), rows_of(g, T, C, torch.bfloat16)
     w = torch.softmax(torch.randn((T, k), device="cuda", generator=g), 1)
