@@ -24,7 +24,7 @@ typedef int v2i __attribute__((ext_vector_type(2)));
 // two integers is seen as that and goes to the even one (any other is at least
 // 2^-9 away from half way, far more than the approximation is off).
 //
-// What bounds it: the bytes. 65536 x 512 22 us (4.6 TB/s), 16384 x 7168 63 us (5.6),
+// What bounds it: the bytes. 65536 x 512 18 us (5.7 TB/s), 16384 x 7168 63 us (5.6),
 // 4096 x 20480, read twice, 53 us (the second time from cache); 1 x 7168 2.6 us.
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -93,10 +93,8 @@ __global__ __launch_bounds__(THREADS) void quant_int8_kernel(const uint16_t* x, 
     top = max(top, rotate<4>(top));
     top = max(top, rotate<2>(top));
     top = max(top, rotate<1>(top));
-    if constexpr (L >= 64) {
-      top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
-      top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
-    }
+    if constexpr (L >= 32) top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    if constexpr (L >= 64) top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     if constexpr (L > 64) {
       if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = top;
       __syncthreads();
@@ -689,8 +687,12 @@ hipError_t tile_int8(void (*kernel)(Int8Params), const Int8Params& p, int num_cu
 
 hipError_t launch_quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx, int8_t* q, float* scales,
                              hipStream_t st) {
+  // As many lanes as hold the row in two chunks each: with twice as many, half of them
+  // idle, 65536 x 512 took 21 us for 18, 16384 x 1536 19 for 15, 32768 x 2048 37 for 31.
   if (cols <= 16 * 2 * 8) return quant_int8<16, 2>(x, rows, cols, ldx, q, scales, st);
+  if (cols <= 32 * 2 * 8) return quant_int8<32, 2>(x, rows, cols, ldx, q, scales, st);
   if (cols <= 64 * 2 * 8) return quant_int8<64, 2>(x, rows, cols, ldx, q, scales, st);
+  if (cols <= 128 * 2 * 8) return quant_int8<128, 2>(x, rows, cols, ldx, q, scales, st);
   if (cols <= 256 * 2 * 8) return quant_int8<256, 2>(x, rows, cols, ldx, q, scales, st);
   if (cols <= 512 * 2 * 8) return quant_int8<512, 2>(x, rows, cols, ldx, q, scales, st);
   if (cols <= 1024 * 2 * 8) return quant_int8<1024, 2>(x, rows, cols, ldx, q, scales, st);

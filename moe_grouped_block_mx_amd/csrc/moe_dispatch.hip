@@ -28,8 +28,8 @@ namespace {
 //
 // What bounds it: launches and latencies, not the 12 or 16 bytes a choice. 64 choices take
 // 3.2 us, 4096 5.8 - 7.9 (one workgroup, whose LDS counters and ballots are its
-// time), 262144 9 - 13 (two launches, the second waits for the first), 4194304 68
-// (1 TB/s).
+// time), 65536 8 - 10 and 262144 9 - 15 (two launches, the second waits for the
+// first), 4194304 58 (1.2 TB/s).
 
 constexpr int kSortBits = 10;   // experts + 1 <= 513
 
@@ -90,9 +90,8 @@ __device__ __forceinline__ int32_t block_exclusive(int32_t v, int32_t* part) {
   return base + sum - v;
 }
 
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
+constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kSortKeys = kMaxExperts + 1;
-constexpr int kSortPer = kSortChunk / kSortThreads;   // choices of a lane, of several workgroups
 static_assert(kSortKeys <= kSortThreads && kSortKeys <= 1 << kSortBits, "a thread for each key");
 
 // The chunk's choices: keys, and their places among those of the same key in
@@ -152,16 +151,16 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(SortParams p) {
 }
 
 // Several: each one's counts and the places inside it, ...
-template <class I>
+template <class I, int PER>
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams p) {
   __shared__ int32_t cnt[kSortWaves][kSortKeys];
-  int key[kSortPer], place[kSortPer];
-  const int first = (int)blockIdx.x * kSortChunk;
-  const int32_t total = sort_chunk<I, kSortPer>(p, first, cnt, key, place);
+  int key[PER], place[PER];
+  const int first = (int)blockIdx.x * (PER * kSortThreads);
+  const int32_t total = sort_chunk<I, PER>(p, first, cnt, key, place);
   if ((int)threadIdx.x <= p.experts) p.table[(int64_t)blockIdx.x * (p.experts + 1) + threadIdx.x] = total;
 #pragma unroll
-  for (int i = 0; i < kSortPer; ++i) {
-    const int c = first + (int)(threadIdx.x >> 6) * (64 * kSortPer) + i * 64 + (threadIdx.x & 63);
+  for (int i = 0; i < PER; ++i) {
+    const int c = first + (int)(threadIdx.x >> 6) * (64 * PER) + i * 64 + (threadIdx.x & 63);
     if (c < p.n) p.rows[c] = place[i];
   }
 }
@@ -188,14 +187,14 @@ __global__ __launch_bounds__(64) void sort_scan_kernel(SortParams p, int chunks)
 
 // ... and the places of all. SCANNED: the table holds what the launch above made
 // of it; else every workgroup adds its columns up, `parts` threads a column.
-template <class I, bool SCANNED>
+template <class I, int PER, bool SCANNED>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p, int chunks, int parts) {
   __shared__ int32_t base[kSortKeys], part[kSortWaves], sums[2][kSortThreads];
   const int keys = p.experts + 1, t = threadIdx.x, mine = blockIdx.x;
-  const int first = mine * kSortChunk;
-  int key[kSortPer], place[kSortPer];
+  const int first = mine * (PER * kSortThreads);
+  int key[PER], place[PER];
 #pragma unroll
-  for (int i = 0; i < kSortPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int c = first + i * kSortThreads + t;
     if (c < p.n) {
       key[i] = sort_key<I>(p, c);
@@ -233,14 +232,37 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p, 
   if (mine == 0 && t < p.experts) p.counts[t] = total;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSortPer; ++i) {
+  for (int i = 0; i < PER; ++i) {
     const int c = first + i * kSortThreads + t;
     if (c < p.n) store_place(p, c, key[i], base[key[i]] + place[i]);
   }
 }
 
+template <class I, int PER>
+hipError_t sort_chunked(const SortParams& p, int64_t chunks, hipStream_t st) {
+  sort_count_kernel<I, PER><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if constexpr (PER < 4)
+    if (chunks <= kSortDirect) {
+      int parts = 1;
+      while (parts * 2 * (p.experts + 1) <= kSortThreads) parts *= 2;
+      sort_place_kernel<I, PER, false><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, parts);
+      return hipGetLastError();
+    }
+  if constexpr (PER > 1) {
+    sort_scan_kernel<<<(uint32_t)p.experts + 1, 64, 0, st>>>(p, (int)chunks);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    sort_place_kernel<I, PER, true><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, 1);
+    e = hipGetLastError();
+  }
+  return e;
+}
+
 template <class I>
 hipError_t sort_any(const SortParams& p, hipStream_t st) {
+  static_assert(kSortShort / kSortThreads <= kSortDirect && kSortLong / (4 * kSortThreads) > kSortDirect,
+                "chunks of one choice a lane take no scan, those of four always");
   const int64_t chunks = sort_chunks(p.n);
   if (chunks <= 1) {
     if (p.n <= kSortThreads) sort_one_kernel<I, 1><<<1, kSortThreads, 0, st>>>(p);
@@ -248,19 +270,11 @@ hipError_t sort_any(const SortParams& p, hipStream_t st) {
     else sort_one_kernel<I, kSortOne / kSortThreads><<<1, kSortThreads, 0, st>>>(p);
     return hipGetLastError();
   }
-  sort_count_kernel<I><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (chunks <= kSortDirect) {
-    int parts = 1;
-    while (parts * 2 * (p.experts + 1) <= kSortThreads) parts *= 2;
-    sort_place_kernel<I, false><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, parts);
-    return hipGetLastError();
+  switch (sort_lane(p.n)) {
+    case 1: return sort_chunked<I, 1>(p, chunks, st);
+    case 2: return sort_chunked<I, 2>(p, chunks, st);
+    default: return sort_chunked<I, 4>(p, chunks, st);
   }
-  sort_scan_kernel<<<(uint32_t)p.experts + 1, 64, 0, st>>>(p, (int)chunks);
-  if ((e = hipGetLastError()) != hipSuccess) return e;
-  sort_place_kernel<I, true><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, 1);
-  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------

@@ -5,27 +5,41 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "device_common.hpp"
 
 namespace mxgg {
 
 // --- tokens to experts and back ---------------------------------------------
 // Up to kSortOne choices are sorted by one workgroup in one launch. More are cut
-// into chunks of kSortChunk, a workgroup each, that meet in a table (in the
-// workspace): one row of experts + 1 counts a chunk (the last: dropped choices).
-// Measured, us, one launch and chunks: 4096 choices of 8 experts 5.8 and 7.2, of 511
-// 7.9 and 8.2; 8192 of 8 experts 9.6 and 7.3, of 128 12.6 and 7.9.
-constexpr int kSortOne = 4096, kSortChunk = 2048;
+// into chunks, a workgroup each, that meet in a table (in the workspace): one row of
+// experts + 1 counts a chunk (the last: dropped choices).
+// Measured, us, one launch and chunks of 2048: 4096 choices of 8 experts 5.8 and 7.2,
+// of 511 7.9 and 8.2; 8192 of 8 experts 9.6 and 7.3, of 128 12.6 and 7.9.
+constexpr int kSortOne = 4096, kSortThreads = 1024;
+// Choices of a chunk, 1, 2 or 4 a lane: small chunks spread over the card, large ones
+// keep the table short. Measured, us, chunks of 1024, 2048 and 4096: 8192 choices of
+// 128 experts 7.1 8.1 10.4; 65536 of 128 8.3 10.1 11.9, of 511 10.0 10.0 13.6; 131072
+// of 128 9.8 9.7 13.2; 262144 of 128 13.2 11.5 14.3; 524288 of 128 16.7 13.9 15.2;
+// 1048576 of 128 28 21 19; 4194304 of 128 91 68 58.
+constexpr int64_t kSortShort = 65536, kSortLong = 1 << 20;
+inline int sort_lane(int64_t choices) { return choices <= kSortShort ? 1 : choices < kSortLong ? 2 : 4; }
 inline int64_t sort_chunks(int64_t choices) {
-  return choices <= kSortOne ? 1 : (choices + kSortChunk - 1) / kSortChunk;
+  const int64_t chunk = (int64_t)sort_lane(choices) * kSortThreads;
+  return choices <= kSortOne ? 1 : (choices + chunk - 1) / chunk;
 }
 // Up to so many workgroups, each adds up the table's rows before its own
 // itself; beyond, a launch between does it for all. Measured, us, without the launch
-// and with it: 16 chunks of 128 experts 9.0 and 9.7; 64 of 8 experts 8.0 and 8.8; 128
-// of 128 experts 11.5 and 11.6; 256 of 128 experts 15.5 and 14.1, of 511 22 and 17.
+// and with it (chunks of 2048): 16 chunks of 128 experts 9.0 and 9.7; 64 of 8 experts
+// 8.0 and 8.8; 128 of 128 experts 11.5 and 11.6; 256 of 128 experts 15.5 and 14.1, of
+// 511 22 and 17.
 constexpr int64_t kSortDirect = 128;
 inline size_t sort_workspace(int64_t choices, int64_t experts) {
-  const int64_t chunks = sort_chunks(choices);
+  int64_t chunks = sort_chunks(choices);
+  // (no less than fewer choices take, so that the space of the largest call does for all)
+  if (choices > kSortShort) chunks = std::max(chunks, sort_chunks(kSortShort));
+  if (choices >= kSortLong) chunks = std::max(chunks, sort_chunks(kSortLong - 1));
   return chunks <= 1 ? 0 : (size_t)((chunks + 1) * (experts + 1)) * sizeof(int32_t);
 }
 

@@ -33,8 +33,8 @@ def check_codes(x):
     assert np.array_equal(host(s), ws, equal_nan=True)
 
 
-@pytest.mark.parametrize("rows,cols,pad", [(1, 16, 0), (3, 16, 8), (5, 112, 0), (17, 256, 0), (2, 272, 8), (9, 1024, 0),
-                                           (4, 1040, 0), (3, 2000, 16), (2, 4096, 0), (3, 4112, 0), (2, 7168, 0),
+@pytest.mark.parametrize("rows,cols,pad", [(1, 16, 0), (3, 16, 8), (5, 112, 0), (17, 256, 0), (2, 272, 8), (7, 512, 0), (5, 528, 8), (9, 1024, 0),
+                                           (4, 1040, 0), (3, 2000, 16), (5, 2048, 0), (3, 2064, 0), (2, 4096, 0), (3, 4112, 0), (2, 7168, 0),
                                            (2, 8208, 0), (1, 16384, 0), (2, 16400, 0), (2, 70000, 0), (1, 131056, 0),
                                            (0, 64, 0), (100001, 16, 0)])
 def test_quantizer(rows, cols, pad):
@@ -48,7 +48,7 @@ def test_quantizer(rows, cols, pad):
 def test_quantizer_more_rows_than_workgroups():
     """2^20 workgroups at most, which stay for the rows behind."""
     R = (1 << 20) + 700
-    x = torch.empty((R, 1040), dtype=torch.bfloat16, device="cuda").normal_(generator=gen(3))
+    x = torch.empty((R, 2064), dtype=torch.bfloat16, device="cuda").normal_(generator=gen(3))
     q, s = mxg.quantize_rowwise(x, "int8")
     for at in (slice(0, 3), slice((1 << 20) - 2, (1 << 20) + 2), slice(R - 3, R)):
         wq, ws = ot.quantize_int8(f64(x[at]))

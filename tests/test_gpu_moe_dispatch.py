@@ -49,7 +49,8 @@ def check_sort(ids, E):
 # one choice, a wave, one workgroup's chunk and its borders, several chunks, more
 # than one launch adds up, ragged ends
 @pytest.mark.parametrize("T,k,E", [(0, 2, 5), (1, 1, 1), (1, 16, 512), (9, 7, 3), (256, 8, 128), (257, 8, 512), (2048, 1, 1),
-                                   (2049, 1, 64), (5000, 3, 129), (32768, 8, 64), (32769, 8, 511), (100003, 5, 17)])
+                                   (2049, 1, 64), (5000, 3, 129), (8192, 8, 512), (8193, 8, 9), (32768, 8, 64), (32769, 8, 511),
+                                   (100003, 5, 17), (131071, 8, 100), (131072, 8, 3), (140001, 8, 511)])
 @pytest.mark.parametrize("itype", [torch.int32, torch.int64])
 def test_sort(T, k, E, itype):
     check_sort(choices(gen(T), T, k, E, 0.1 if T % 2 else 0.0, itype), E)

@@ -37,6 +37,8 @@ def test_sort_rules():
     assert sort(T=4096, ws=P, ws_bytes=need) == HIP
     assert sort(T=4096, ws=P, ws_bytes=need - 1) == WS and sort(T=4096, ws_bytes=need) == NULL
     assert L.mxgg_moe_sort_workspace(-1, 8, 16) == 0 and L.mxgg_moe_sort_workspace(BIG, 8, 16) == 0
+    sizes = [L.mxgg_moe_sort_workspace(T, 8, 16) for T in (1, 512, 513, 8191, 8192, 8193, 16384, 131071, 131072, 10 ** 6)]
+    assert sizes == sorted(sizes)                          # the largest call's does for all
     assert sort(T=0, ids=None, rows=None, choices=None) == HIP   # clears the counts
 
 
