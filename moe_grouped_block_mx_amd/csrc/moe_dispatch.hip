@@ -28,7 +28,7 @@ namespace {
 //
 // What bounds it: launches and latencies, not the 12 or 16 bytes a choice. 64 choices take
 // 3.2 us, 4096 5.8 - 7.9 (one workgroup, whose LDS counters and ballots are its
-// time), 65536 8 - 10 and 262144 9 - 15 (two launches, the second waits for the
+// time), 65536 7 - 10 and 262144 9 - 13 (two launches, the second waits for the
 // first), 4194304 58 (1.2 TB/s).
 
 constexpr int kSortBits = 10;   // experts + 1 <= 513
@@ -157,7 +157,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams p) 
   int key[PER], place[PER];
   const int first = (int)blockIdx.x * (PER * kSortThreads);
   const int32_t total = sort_chunk<I, PER>(p, first, cnt, key, place);
-  if ((int)threadIdx.x <= p.experts) p.table[(int64_t)blockIdx.x * (p.experts + 1) + threadIdx.x] = total;
+  const int ld = sort_table_row(p.experts);
+  if ((int)threadIdx.x < ld) p.table[(int64_t)blockIdx.x * ld + threadIdx.x] = total;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int c = first + (int)(threadIdx.x >> 6) * (64 * PER) + i * 64 + (threadIdx.x & 63);
@@ -167,30 +168,31 @@ __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(SortParams p) 
 
 // ... the counts before each chunk (the totals behind the last), one wave a key ...
 __global__ __launch_bounds__(64) void sort_scan_kernel(SortParams p, int chunks) {
-  const int keys = p.experts + 1;
+  const int ld = sort_table_row(p.experts);
   int32_t* col = p.table + blockIdx.x;
   int32_t base = 0;
   for (int b0 = 0; b0 < chunks; b0 += 64) {
     const int b = b0 + (int)threadIdx.x;
-    const int32_t v = b < chunks ? col[(int64_t)b * keys] : 0;
+    const int32_t v = b < chunks ? col[(int64_t)b * ld] : 0;
     int32_t sum = v;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int32_t o = __shfl_up(sum, d, 64);
       if ((int)threadIdx.x >= d) sum += o;
     }
-    if (b < chunks) col[(int64_t)b * keys] = base + sum - v;
+    if (b < chunks) col[(int64_t)b * ld] = base + sum - v;
     base += __shfl(sum, 63, 64);
   }
-  if (threadIdx.x == 0) col[(int64_t)chunks * keys] = base;
+  if (threadIdx.x == 0) col[(int64_t)chunks * ld] = base;
 }
 
 // ... and the places of all. SCANNED: the table holds what the launch above made
-// of it; else every workgroup adds its columns up, `parts` threads a column.
+// of it; else every workgroup adds its columns up, `parts` threads each four columns.
 template <class I, int PER, bool SCANNED>
 __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p, int chunks, int parts) {
-  __shared__ int32_t base[kSortKeys], part[kSortWaves], sums[2][kSortThreads];
-  const int keys = p.experts + 1, t = threadIdx.x, mine = blockIdx.x;
+  __shared__ int32_t base[kSortKeys], part[kSortWaves];
+  __shared__ v4i sums[2][SCANNED ? 1 : kSortThreads];
+  const int keys = p.experts + 1, ld = sort_table_row(p.experts), t = threadIdx.x, mine = blockIdx.x;
   const int first = mine * (PER * kSortThreads);
   int key[PER], place[PER];
 #pragma unroll
@@ -204,27 +206,27 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(SortParams p, 
   int32_t before = 0, total = 0;
   if constexpr (SCANNED) {
     if (t < keys) {
-      before = p.table[(int64_t)mine * keys + t];
-      total = p.table[(int64_t)chunks * keys + t];
+      before = p.table[(int64_t)mine * ld + t];
+      total = p.table[(int64_t)chunks * ld + t];
     }
   } else {
-    const int width = kSortThreads / parts, e = t % width;
-    if (e < keys) {
-#pragma unroll 16
+    const int width = kSortThreads / parts, e = t % width * 4;
+    v4i b4{}, t4{};
+    if (e < ld) {
+#pragma unroll 8
       for (int b = t / width; b < chunks; b += parts) {
-        const int32_t v = p.table[(int64_t)b * keys + e];
-        before += b < mine ? v : 0;
-        total += v;
+        const v4i v = *reinterpret_cast<const v4i*>(p.table + (int64_t)b * ld + e);
+        b4 += b < mine ? v : v4i{};
+        t4 += v;
       }
     }
-    sums[0][t] = before;
-    sums[1][t] = total;
+    sums[0][t] = b4;
+    sums[1][t] = t4;
     __syncthreads();
-    before = total = 0;
     if (t < keys)
       for (int q = 0; q < parts; ++q) {
-        before += sums[0][q * width + t];
-        total += sums[1][q * width + t];
+        before += reinterpret_cast<const int32_t*>(sums[0] + q * width)[t];
+        total += reinterpret_cast<const int32_t*>(sums[1] + q * width)[t];
       }
   }
   const int32_t at = block_exclusive<kSortThreads>(total, part);
@@ -246,7 +248,7 @@ hipError_t sort_chunked(const SortParams& p, int64_t chunks, hipStream_t st) {
   if constexpr (PER < 4)
     if (chunks <= kSortDirect) {
       int parts = 1;
-      while (parts * 2 * (p.experts + 1) <= kSortThreads) parts *= 2;
+      while (parts < 32 && parts * 2 * sort_table_row(p.experts) <= kSortThreads * 4) parts *= 2;
       sort_place_kernel<I, PER, false><<<(uint32_t)chunks, kSortThreads, 0, st>>>(p, (int)chunks, parts);
       return hipGetLastError();
     }

@@ -14,15 +14,16 @@ namespace mxgg {
 // --- tokens to experts and back ---------------------------------------------
 // Up to kSortOne choices are sorted by one workgroup in one launch. More are cut
 // into chunks, a workgroup each, that meet in a table (in the workspace): one row of
-// experts + 1 counts a chunk (the last: dropped choices).
-// Measured, us, one launch and chunks of 2048: 4096 choices of 8 experts 5.8 and 7.2,
-// of 511 7.9 and 8.2; 8192 of 8 experts 9.6 and 7.3, of 128 12.6 and 7.9.
+// experts + 1 counts a chunk (the last: dropped choices; padded to whole 16 bytes).
+// Measured, us on the card: 4096 choices in one launch 5.8 (8 experts), 7.3 (128) and
+// 7.9 (511), and 4104 in two 6.7 (128), which costs the host a launch, 3.5, more; 8192
+// in one 9.6 (8) and 12.6 (128), in two 6.4 and 6.8.
 constexpr int kSortOne = 4096, kSortThreads = 1024;
 // Choices of a chunk, 1, 2 or 4 a lane: small chunks spread over the card, large ones
 // keep the table short. Measured, us, chunks of 1024, 2048 and 4096: 8192 choices of
-// 128 experts 7.1 8.1 10.4; 65536 of 128 8.3 10.1 11.9, of 511 10.0 10.0 13.6; 131072
-// of 128 9.8 9.7 13.2; 262144 of 128 13.2 11.5 14.3; 524288 of 128 16.7 13.9 15.2;
-// 1048576 of 128 28 21 19; 4194304 of 128 91 68 58.
+// 128 experts 6.8 8.0 10.5; 65536 of 128 8.4 9.0 11.4, of 511 10.1 10.3 12.5; 131072
+// of 128 9.8 9.9 12.0, of 511 13.2 10.8 13.4; 262144 of 128 11.9 10.8 13.0; 524288 of
+// 128 16.5 14.0 14.4; 1048576 of 128 28 21 19; 4194304 of 128 90 68 58.
 constexpr int64_t kSortShort = 65536, kSortLong = 1 << 20;
 inline int sort_lane(int64_t choices) { return choices <= kSortShort ? 1 : choices < kSortLong ? 2 : 4; }
 inline int64_t sort_chunks(int64_t choices) {
@@ -31,16 +32,18 @@ inline int64_t sort_chunks(int64_t choices) {
 }
 // Up to so many workgroups, each adds up the table's rows before its own
 // itself; beyond, a launch between does it for all. Measured, us, without the launch
-// and with it (chunks of 2048): 16 chunks of 128 experts 9.0 and 9.7; 64 of 8 experts
-// 8.0 and 8.8; 128 of 128 experts 11.5 and 11.6; 256 of 128 experts 15.5 and 14.1, of
-// 511 22 and 17.
+// and with it: 32 chunks of 32 experts 7.0 and 8.0; 64 of 128 8.3 and 8.7, of 511 10.0
+// and 9.4; 128 of 128 10.9 and 11.6, of 511 13.5 and 13.4; 256 of 8 10.0 and 11.3, of
+// 128 13.9 and 14.3, of 511 18.7 and 16.6.
 constexpr int64_t kSortDirect = 128;
+// A row of the table: whole 16 bytes
+__host__ __device__ inline int sort_table_row(int experts) { return (experts + 4) / 4 * 4; }
 inline size_t sort_workspace(int64_t choices, int64_t experts) {
   int64_t chunks = sort_chunks(choices);
   // (no less than fewer choices take, so that the space of the largest call does for all)
   if (choices > kSortShort) chunks = std::max(chunks, sort_chunks(kSortShort));
   if (choices >= kSortLong) chunks = std::max(chunks, sort_chunks(kSortLong - 1));
-  return chunks <= 1 ? 0 : (size_t)((chunks + 1) * (experts + 1)) * sizeof(int32_t);
+  return chunks <= 1 ? 0 : (size_t)((chunks + 1) * sort_table_row((int)experts)) * sizeof(int32_t);
 }
 
 struct SortParams {
@@ -48,7 +51,7 @@ struct SortParams {
   int32_t* rows;      // [choices]
   int32_t* choices;   // [choices]
   int32_t* counts;    // [experts]
-  int32_t* table;     // [chunks + 1][experts + 1]
+  int32_t* table;     // [chunks + 1][sort_table_row(experts)]
   int64_t ldi;
   int32_t n, top_k, experts;
 };
