@@ -288,10 +288,12 @@ hipError_t sort_any(const SortParams& p, hipStream_t st) {
 // Copies with places: nothing is computed that counts, so the design is about bytes in
 // flight. A lane has all loads of its choices on the way before it uses the first, and
 // workgroups that run at the same time have the pieces of the same rows. bf16, eight
-// choices a token, 128 experts: dispatch of 4096 x 4096 51 us (5.9 TB/s, the token's
-// row is read once), combine to 16384 x 7168 450 us (4.7 TB/s; with the rows in the
-// tokens' order 4.9), its gradient at 4096 x 4096 119 us (4.8 TB/s). A plain copy of
-// 2^30 bytes reaches 5.1.
+// choices a token, 128 experts: dispatch of 4096 x 4096 50 us (6.0 TB/s, the token's
+// row is read once), combine to 16384 x 7168 410 us (5.2 TB/s; with the rows in the
+// tokens' order 5.3), its gradient at 4096 x 4096 112 us (5.1 TB/s). A plain copy of
+// 2^30 bytes reaches 5.1. Rows shorter than a chunk have kernels of their own: with a
+// branch at every load for them combine took 450 us, and few tokens, whose time is much
+// that of bringing the code, 9.8 for 6 (8 x 1024, the gradient).
 
 constexpr int kRowThreads = 256;
 constexpr int64_t kRowGrid = 1 << 20;   // workgroups at most; they stay for the rest
@@ -309,93 +311,120 @@ struct RowPlace {
   }
 };
 
-// The chunk at `col`, moved back to end with the row (its first elements are its
-// neighbour's then, and written twice with the same bits); a row shorter than a
-// chunk goes by element.
+// One element, in the place of a chunk where a row is shorter than that.
 template <class E>
-struct RowChunk {
-  static constexpr int N = Chunk<E>::N;
-  int start, size;
-  __device__ __forceinline__ RowChunk(int col, int cols) {
-    start = max(min(col, cols - N), 0);
-    size = min(cols, N);
-  }
-  __device__ __forceinline__ void load(Chunk<E>& c, const E* row) const {
-    if (size < N) c.load_part(row, size);
-    else c.load(row + start);
-  }
-  __device__ __forceinline__ void store(const Chunk<E>& c, E* row) const {
-    if (size < N) c.store_part(row, size);
-    else c.store(row + start);
+struct Single {
+  static constexpr int N = 1;
+  Chunk<E> c;
+  __device__ __forceinline__ void load(const E* p) { c.load_part(p, 1); }
+  __device__ __forceinline__ void store(E* p) const { c.store_part(p, 1); }
+  __device__ __forceinline__ float get(int) const { return c.get(0); }
+  __device__ __forceinline__ void set(const float (&v)[1]) {
+    float all[Chunk<E>::N] = {v[0]};
+    c.set(all);
   }
 };
 
-template <class E>
+// The chunk at `col` begins here, moved back to end with the row (its first
+// elements are its neighbour's then, and written twice with the same bits).
+template <class C>
+__device__ __forceinline__ int chunk_start(int col, int cols) { return min(col, cols - C::N); }
+
+template <class E, class C>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(TokenParams p, int lanes, uint32_t pieces) {
-  constexpr int N = Chunk<E>::N;
+  constexpr int N = C::N;
   const RowPlace pl(lanes, pieces);
   const int col = pl.chunk * N;
   if (col >= p.cols) return;
-  const RowChunk<E> at(col, p.cols);
+  const int at = chunk_start<C>(col, p.cols);
   for (int64_t t = pl.token; t < p.tokens; t += pl.step) {
-    Chunk<E> c, zero{};
-    at.load(c, static_cast<const E*>(p.x) + t * p.ldx);
+    C c, zero{};
+    c.load(static_cast<const E*>(p.x) + t * p.ldx + at);
     for (int j = 0; j < p.top_k; ++j) {
       const int32_t r = p.rows[t * p.top_k + j];
       const int32_t to = r < 0 ? ~r : r;
-      if (to < p.expert_rows) at.store(r < 0 ? zero : c, static_cast<E*>(p.out) + to * p.ldo);
+      if (to < p.expert_rows) (r < 0 ? zero : c).store(static_cast<E*>(p.out) + to * p.ldo + at);
     }
   }
 }
 
-// A token's choices j < K (at least top_k): rows that are kept and their weights. A
-// row that is not has weight 0 and is read at place 0, and what is read there is
-// not used: loads behind a branch would be waited for one after the other.
+// A token's choices j < K (at least top_k): rows and weights. A row that is not kept
+// is read at place 0, and what is read there is not used: loads behind a branch
+// would be waited for one after the other. A choice past top_k has no place.
 template <int K>
 struct Choices {
   int32_t row[K];
   float weight[K];
-  bool kept[K];
-  __device__ __forceinline__ Choices(const TokenParams& p, int64_t t) {
+  uint32_t rows;
+  __device__ __forceinline__ Choices(const TokenParams& p, int64_t t) : rows((uint32_t)p.expert_rows) {
 #pragma unroll
     for (int j = 0; j < K; ++j) row[j] = p.rows[t * p.top_k + (j < p.top_k ? j : 0)];
 #pragma unroll
     for (int j = 0; j < K; ++j) weight[j] = p.weights ? p.weights[t * p.top_k + (j < p.top_k ? j : 0)] : 1.f;
 #pragma unroll
-    for (int j = 0; j < K; ++j) kept[j] = j < p.top_k && row[j] >= 0 && row[j] < p.expert_rows;
+    for (int j = 0; j < K; ++j) row[j] = j < p.top_k ? row[j] : INT32_MIN;
   }
+  __device__ __forceinline__ bool kept(int j) const { return (uint32_t)row[j] < rows; }
+  __device__ __forceinline__ int64_t from(int j) const { return kept(j) ? row[j] : 0; }
 };
 
-template <class E, int K>
+template <class E, class C, int K>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int lanes, uint32_t pieces) {
-  constexpr int N = Chunk<E>::N;
+  constexpr int N = C::N;
   const RowPlace pl(lanes, pieces);
   const int col = pl.chunk * N;
   if (col >= p.cols) return;
-  const RowChunk<E> at(col, p.cols);
+  const int at = chunk_start<C>(col, p.cols);
   for (int64_t t = pl.token; t < p.tokens; t += pl.step) {
     float sum[N] = {};
     if (p.expert_rows > 0) {
       const Choices<K> ch(p, t);
-      Chunk<E> c[K];
+      C c[K], zero{};
 #pragma unroll
-      for (int j = 0; j < K; ++j) at.load(c[j], static_cast<const E*>(p.y) + (ch.kept[j] ? ch.row[j] : 0) * p.ldy);
+      for (int j = 0; j < K; ++j) c[j].load(static_cast<const E*>(p.y) + ch.from(j) * p.ldy + at);
 #pragma unroll
-      for (int j = 0; j < K; ++j)
+      for (int j = 0; j < K; ++j) {
+        const C y = ch.kept(j) ? c[j] : zero;
+        const float w = ch.kept(j) ? ch.weight[j] : 0.f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) sum[i] = ch.kept[j] ? __builtin_fmaf(ch.weight[j], c[j].get(i), sum[i]) : sum[i];
+        for (int i = 0; i < N; ++i) sum[i] = __builtin_fmaf(w, y.get(i), sum[i]);
+      }
     }
-    Chunk<E> o;
+    C o;
     o.set(sum);
-    at.store(o, static_cast<E*>(p.out) + t * p.ldo);
+    o.store(static_cast<E*>(p.out) + t * p.ldo + at);
   }
 }
 
+// The elements of a chunk that are not its neighbour's
+template <class C>
+struct Own {
+  __device__ __forceinline__ Own(int, int) {}
+  __device__ __forceinline__ C of(const C& c) const { return c; }
+};
+template <class E>
+struct Own<Chunk<E>> {
+  uint32_t mask[4];
+  __device__ __forceinline__ Own(int start, int col) {
+    constexpr int EACH = Chunk<E>::N / 4, BITS = 32 / EACH;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int before = min(max(col - start - EACH * i, 0), EACH);
+      mask[i] = before == EACH ? 0 : ~0u << (BITS * before);
+    }
+  }
+  __device__ __forceinline__ Chunk<E> of(Chunk<E> c) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.w[i] &= mask[i];
+    return c;
+  }
+};
+
 // A token belongs to L lanes that go over the whole row: the weights' gradients
 // are sums over it.
-template <class E, int K, int L>
+template <class E, class C, int K, int L>
 __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p) {
-  constexpr int N = Chunk<E>::N, PER = kRowThreads / L;
+  constexpr int N = C::N, PER = kRowThreads / L;
   __shared__ float part[kRowThreads / 64][K];
   const int lane = threadIdx.x % L;
   for (int64_t t0 = (int64_t)blockIdx.x * PER; t0 < p.tokens; t0 += (int64_t)gridDim.x * PER) {
@@ -406,49 +435,50 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p)
       const Choices<K> ch(p, t);
       const E* d = static_cast<const E*>(p.x) + t * p.ldx;
       for (int col = lane * N; col < p.cols; col += L * N) {
-        const RowChunk<E> at(col, p.cols);
-        Chunk<E> c, y[K];
-        at.load(c, d);
+        const int at = chunk_start<C>(col, p.cols);
+        const Own<C> own(at, col);
+        C c, y[K], zero{};
+        c.load(d + at);
 #pragma unroll
-        for (int j = 0; j < K; ++j) at.load(y[j], static_cast<const E*>(p.y) + (ch.kept[j] ? ch.row[j] : 0) * p.ldy);
+        for (int j = 0; j < K; ++j) y[j].load(static_cast<const E*>(p.y) + ch.from(j) * p.ldy + at);
+        const C mine = own.of(c);
 #pragma unroll
         for (int j = 0; j < K; ++j) {
+          const C yj = own.of(y[j]);
           float v[N];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            // a moved chunk's first elements count in their own lane
-            const bool own = at.start + i >= col && i < at.size;
-            dot[j] = own ? __builtin_fmaf(c.get(i), y[j].get(i), dot[j]) : dot[j];
-            v[i] = ch.kept[j] ? ch.weight[j] * c.get(i) : 0.f;
+            dot[j] = __builtin_fmaf(mine.get(i), yj.get(i), dot[j]);
+            v[i] = ch.weight[j] * c.get(i);
           }
-          Chunk<E> o;
+          C o;
           o.set(v);
           const int32_t to = ch.row[j] < 0 ? ~ch.row[j] : ch.row[j];
-          if (j < p.top_k && to < p.expert_rows) at.store(o, static_cast<E*>(p.out) + to * p.ldo);
+          if (to < p.expert_rows) (ch.kept(j) ? o : zero).store(static_cast<E*>(p.out) + to * p.ldo + at);
         }
       }
 #pragma unroll
-      for (int j = 0; j < K; ++j) dot[j] = ch.kept[j] ? dot[j] : 0.f;
+      for (int j = 0; j < K; ++j) dot[j] = ch.kept(j) ? dot[j] : 0.f;
     }
 #pragma unroll
     for (int j = 0; j < K; ++j) dot[j] = lanes_sum<(L < 64 ? L : 64)>(dot[j]);
-    if constexpr (L > 64) {
+    if constexpr (L > 64) {                              // (the workgroup has one token)
       if (threadIdx.x % 64 == 0)
 #pragma unroll
         for (int j = 0; j < K; ++j) part[threadIdx.x / 64][j] = dot[j];
       __syncthreads();
-#pragma unroll
-      for (int j = 0; j < K; ++j)
-        if (lane == j) {
-          float sum = part[threadIdx.x / L * (L / 64)][j];
-          for (int w = 1; w < L / 64; ++w) sum += part[threadIdx.x / L * (L / 64) + w][j];
-          dot[j] = sum;
-        }
+      if (lane < p.top_k) {
+        float sum = part[0][lane];
+        for (int w = 1; w < L / 64; ++w) sum += part[w][lane];
+        p.dweights[t * p.top_k + lane] = sum;
+      }
       __syncthreads();
-    }
+    } else {
+      float mine = dot[0];
 #pragma unroll
-    for (int j = 0; j < K; ++j)
-      if (here && lane == j && j < p.top_k) p.dweights[t * p.top_k + j] = dot[j];
+      for (int j = 1; j < K; ++j) mine = lane == j ? dot[j] : mine;
+      if (here && lane < p.top_k) p.dweights[t * p.top_k + lane] = mine;
+    }
   }
 }
 
@@ -473,36 +503,47 @@ RowGrid row_grid(const TokenParams& p, int n) {
   return g;
 }
 
-template <class E, int K>
+template <class E, class C>
+hipError_t dispatch(const TokenParams& p, hipStream_t st) {
+  const RowGrid g = row_grid(p, C::N);
+  dispatch_kernel<E, C><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
+  return hipGetLastError();
+}
+template <class E, class C, int K>
 hipError_t combine(const TokenParams& p, hipStream_t st) {
-  const RowGrid g = row_grid(p, Chunk<E>::N);
-  combine_kernel<E, K><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
+  const RowGrid g = row_grid(p, C::N);
+  combine_kernel<E, C, K><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
   return hipGetLastError();
 }
-template <class E, int K, int L>
+template <class E, class C, int K, int L>
 hipError_t combine_bwd(const TokenParams& p, hipStream_t st) {
-  const int64_t blocks = (p.tokens + kRowThreads / L - 1) / (kRowThreads / L);
-  combine_bwd_kernel<E, K, L><<<(uint32_t)(blocks < kRowGrid ? blocks : kRowGrid), kRowThreads, 0, st>>>(p);
+  constexpr int PER = kRowThreads / L;
+  const int64_t blocks = (p.tokens + PER - 1) / PER;
+  combine_bwd_kernel<E, C, K, L><<<(uint32_t)(blocks < kRowGrid ? blocks : kRowGrid), kRowThreads, 0, st>>>(p);
   return hipGetLastError();
 }
-template <class E>
+template <class E, class C>
 hipError_t combine_any(const TokenParams& p, hipStream_t st) {
-  if (p.top_k <= 1) return combine<E, 1>(p, st);
-  if (p.top_k <= 2) return combine<E, 2>(p, st);
-  if (p.top_k <= 4) return combine<E, 4>(p, st);
-  if (p.top_k <= 8) return combine<E, 8>(p, st);
-  return combine<E, 16>(p, st);
+  if (p.top_k <= 1) return combine<E, C, 1>(p, st);
+  if (p.top_k <= 2) return combine<E, C, 2>(p, st);
+  if (p.top_k <= 4) return combine<E, C, 4>(p, st);
+  if (p.top_k <= 8) return combine<E, C, 8>(p, st);
+  return combine<E, C, 16>(p, st);
 }
+constexpr int64_t kFewTokens = 256;
 template <class E, int K>
 hipError_t combine_bwd_wide(const TokenParams& p, hipStream_t st) {
-  // Lanes that fit the row: fewer would leave few loads in flight, more would be idle.
-  // Eight choices, us with 16, 32, 64 and 256 lanes: 65536 x 128 63 99 159 531;
-  // 65536 x 256 130 134 195 580; 16384 x 1024 123 125 125 199; 16384 x 2048 321 308
-  // 287 244; 8192 x 4096 331 293 292 238; 64 x 2048 52 29 17 8.7.
+  // Lanes that fit the row: fewer would leave few loads in flight, more would be idle;
+  // but with few tokens, which leave CUs idle, a row's chunks all at once. Eight
+  // choices, us: 65536 x 128, 16 lanes 63, 32 99, 64 159; 65536 x 256, 16 130, 32 127, 64 195;
+  // 16384 x 1024, 64 115, 256 181; 16384 x 2048, 64 287, 256 238; 256 x 1024, 64 8.3, 256
+  // 6.3, and 1024 of them 10 and 15.
+  if (p.cols < Chunk<E>::N) return combine_bwd<E, Single<E>, K, 16>(p, st);
   const int chunks = (p.cols + Chunk<E>::N - 1) / Chunk<E>::N;
-  if (chunks <= 16) return combine_bwd<E, K, 16>(p, st);
-  if (chunks <= 32) return combine_bwd<E, K, 32>(p, st);
-  return chunks <= 128 ? combine_bwd<E, K, 64>(p, st) : combine_bwd<E, K, 256>(p, st);
+  if (chunks <= 16) return combine_bwd<E, Chunk<E>, K, 16>(p, st);
+  if (chunks <= 32) return combine_bwd<E, Chunk<E>, K, 32>(p, st);
+  if (chunks > 64 && p.tokens <= kFewTokens) return combine_bwd<E, Chunk<E>, K, 256>(p, st);
+  return chunks <= 128 ? combine_bwd<E, Chunk<E>, K, 64>(p, st) : combine_bwd<E, Chunk<E>, K, 256>(p, st);
 }
 template <class E>
 hipError_t combine_bwd_any(const TokenParams& p, hipStream_t st) {
@@ -520,14 +561,13 @@ hipError_t launch_moe_sort(const SortParams& p, bool i64, hipStream_t st) {
 }
 
 hipError_t launch_moe_dispatch(const TokenParams& p, bool f32, hipStream_t st) {
-  const RowGrid g = row_grid(p, f32 ? 4 : 8);
-  if (f32) dispatch_kernel<float><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
-  else dispatch_kernel<bf16_t><<<g.grid, kRowThreads, 0, st>>>(p, g.lanes, g.pieces);
-  return hipGetLastError();
+  if (f32) return p.cols < 4 ? dispatch<float, Single<float>>(p, st) : dispatch<float, Chunk<float>>(p, st);
+  return p.cols < 8 ? dispatch<bf16_t, Single<bf16_t>>(p, st) : dispatch<bf16_t, Chunk<bf16_t>>(p, st);
 }
 
 hipError_t launch_moe_combine(const TokenParams& p, bool f32, hipStream_t st) {
-  return f32 ? combine_any<float>(p, st) : combine_any<bf16_t>(p, st);
+  if (f32) return p.cols < 4 ? combine_any<float, Single<float>>(p, st) : combine_any<float, Chunk<float>>(p, st);
+  return p.cols < 8 ? combine_any<bf16_t, Single<bf16_t>>(p, st) : combine_any<bf16_t, Chunk<bf16_t>>(p, st);
 }
 
 hipError_t launch_moe_combine_bwd(const TokenParams& p, bool f32, hipStream_t st) {
