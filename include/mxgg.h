@@ -674,7 +674,8 @@ mxgg_status mxgg_moe_combine(const void* y, int64_t ldy, mxgg_dtype dtype, int64
  *   dweights[t, j] = sum_c dout[t, c] y[rows[t, j], c] in fp32 (one fixed order),
  *                    0 for a dropped choice
  *   dy       [expert_rows, cols] of `dtype`, leading dimension lddy; may be y
- *            (else overlaps no input). Rows that no place names stay as they were.
+ *            (with lddy == ldy; else overlaps no input). Rows that no place names
+ *            stay as they were.
  * Errors: NULL, SHAPE, FORMAT, ALIGN, DEVICE, ARCH, HIP.
  */
 mxgg_status mxgg_moe_combine_bwd(const void* dout, int64_t lddo, const void* y, int64_t ldy, mxgg_dtype dtype,

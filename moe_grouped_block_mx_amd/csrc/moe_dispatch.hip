@@ -325,10 +325,6 @@ struct Single {
   }
 };
 
-// The chunk at `col` begins here, moved back to end with the row (its first
-// elements are its neighbour's then, and written twice with the same bits).
-template <class C>
-__device__ __forceinline__ int chunk_start(int col, int cols) { return min(col, cols - C::N); }
 
 template <class E, class C>
 __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(TokenParams p, int lanes, uint32_t pieces) {
@@ -336,7 +332,7 @@ __global__ __launch_bounds__(kRowThreads) void dispatch_kernel(TokenParams p, in
   const RowPlace pl(lanes, pieces);
   const int col = pl.chunk * N;
   if (col >= p.cols) return;
-  const int at = chunk_start<C>(col, p.cols);
+  const int at = row_chunk(col, p.cols, N).start;   // (its neighbour's elements are written twice with the same bits)
   for (int64_t t = pl.token; t < p.tokens; t += pl.step) {
     C c, zero{};
     c.load(static_cast<const E*>(p.x) + t * p.ldx + at);
@@ -374,7 +370,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int
   const RowPlace pl(lanes, pieces);
   const int col = pl.chunk * N;
   if (col >= p.cols) return;
-  const int at = chunk_start<C>(col, p.cols);
+  const int at = row_chunk(col, p.cols, N).start;   // (as in dispatch)
   for (int64_t t = pl.token; t < p.tokens; t += pl.step) {
     float sum[N] = {};
     if (p.expert_rows > 0) {
@@ -396,20 +392,27 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int
   }
 }
 
-// The elements of a chunk that are not its neighbour's
-template <class C>
+// The elements of a chunk that are the lane's own. In rows of whole chunks (or of
+// single elements) all are; else the last chunk's first `skip` are its neighbour's,
+// and where the gradient goes over y itself they are not to be written: the neighbour
+// may not have read them yet.
+template <class C, bool RAGGED>
 struct Own {
-  __device__ __forceinline__ Own(int, int) {}
+  __device__ __forceinline__ explicit Own(int) {}
   __device__ __forceinline__ C of(const C& c) const { return c; }
+  template <class E>
+  __device__ __forceinline__ void store(C c, E* p) const { c.store(p); }
 };
 template <class E>
-struct Own<Chunk<E>> {
+struct Own<Chunk<E>, true> {
+  static constexpr int N = Chunk<E>::N;
+  int skip;
   uint32_t mask[4];
-  __device__ __forceinline__ Own(int start, int col) {
-    constexpr int EACH = Chunk<E>::N / 4, BITS = 32 / EACH;
+  __device__ __forceinline__ explicit Own(int skipped) : skip(skipped) {
+    constexpr int EACH = N / 4, BITS = 32 / EACH;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int before = min(max(col - start - EACH * i, 0), EACH);
+      const int before = min(max(skip - EACH * i, 0), EACH);
       mask[i] = before == EACH ? 0 : ~0u << (BITS * before);
     }
   }
@@ -418,11 +421,26 @@ struct Own<Chunk<E>> {
     for (int i = 0; i < 4; ++i) c.w[i] &= mask[i];
     return c;
   }
+  // the last N - skip, in 8, 4 and 2 bytes from the chunk's end on
+  __device__ __forceinline__ void store(Chunk<E> c, E* p) const {
+    if (skip == 0) return c.store(p);
+    const int n = N - skip;
+    if constexpr (N == 8) {
+      const uint32_t two = n & 4 ? c.w[1] : c.w[3], one = n & 2 ? (n & 4 ? c.w[0] : c.w[2]) : two;
+      if (n & 4) memcpy(p + 4, c.w + 2, 8);
+      if (n & 2) memcpy(p + (n & 4 ? 2 : 6), &two, 4);
+      if (n & 1) reinterpret_cast<uint16_t*>(p)[skip] = (uint16_t)(one >> 16);
+    } else {
+      const uint32_t one = n & 2 ? c.w[1] : c.w[3];
+      if (n & 2) memcpy(p + 2, c.w + 2, 8);
+      if (n & 1) memcpy(p + skip, &one, 4);
+    }
+  }
 };
 
 // A token belongs to L lanes that go over the whole row: the weights' gradients
 // are sums over it.
-template <class E, class C, int K, int L>
+template <class E, class C, int K, int L, bool RAGGED>
 __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p) {
   constexpr int N = C::N, PER = kRowThreads / L;
   __shared__ float part[kRowThreads / 64][K];
@@ -435,8 +453,9 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p)
       const Choices<K> ch(p, t);
       const E* d = static_cast<const E*>(p.x) + t * p.ldx;
       for (int col = lane * N; col < p.cols; col += L * N) {
-        const int at = chunk_start<C>(col, p.cols);
-        const Own<C> own(at, col);
+        const RowChunk chunk = row_chunk(col, p.cols, N);
+        const int at = chunk.start;
+        const Own<C, RAGGED> own(chunk.skip);
         C c, y[K], zero{};
         c.load(d + at);
 #pragma unroll
@@ -454,7 +473,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p)
           C o;
           o.set(v);
           const int32_t to = ch.row[j] < 0 ? ~ch.row[j] : ch.row[j];
-          if (to < p.expert_rows) (ch.kept(j) ? o : zero).store(static_cast<E*>(p.out) + to * p.ldo + at);
+          if (to < p.expert_rows) own.store(ch.kept(j) ? o : zero, static_cast<E*>(p.out) + to * p.ldo + at);
         }
       }
 #pragma unroll
@@ -519,7 +538,13 @@ template <class E, class C, int K, int L>
 hipError_t combine_bwd(const TokenParams& p, hipStream_t st) {
   constexpr int PER = kRowThreads / L;
   const int64_t blocks = (p.tokens + PER - 1) / PER;
-  combine_bwd_kernel<E, C, K, L><<<(uint32_t)(blocks < kRowGrid ? blocks : kRowGrid), kRowThreads, 0, st>>>(p);
+  const uint32_t grid = (uint32_t)(blocks < kRowGrid ? blocks : kRowGrid);
+  if constexpr (C::N > 1)
+    if (p.cols % C::N) {
+      combine_bwd_kernel<E, C, K, L, true><<<grid, kRowThreads, 0, st>>>(p);
+      return hipGetLastError();
+    }
+  combine_bwd_kernel<E, C, K, L, false><<<grid, kRowThreads, 0, st>>>(p);
   return hipGetLastError();
 }
 template <class E, class C>

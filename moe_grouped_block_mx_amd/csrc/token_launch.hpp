@@ -57,6 +57,17 @@ struct SortParams {
 };
 hipError_t launch_moe_sort(const SortParams& p, bool i64, hipStream_t st);
 
+// A lane's chunk of n elements of a row of `cols` (at least n), for the columns from
+// `col` on. A chunk that would pass the row's end begins earlier, to end with the row:
+// its first `skip` elements are then its neighbour's.
+struct RowChunk {
+  int start, skip;
+};
+__host__ __device__ inline RowChunk row_chunk(int col, int cols, int n) {
+  const int start = col < cols - n ? col : cols - n;
+  return RowChunk{start, col - start};
+}
+
 struct TokenParams {
   const void* x;          // tokens' rows: dispatch's input, the gradient of combine's output
   const void* y;          // experts' rows: combine's input

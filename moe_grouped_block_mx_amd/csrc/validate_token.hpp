@@ -80,6 +80,8 @@ inline Check validate_moe_combine_bwd(const void* dout, int64_t lddo, const void
   MXGG_TRY(check_ld(ldy, cols, "ldy"));
   MXGG_TRY(check_ld(lddy, cols, "lddy"));
   if (tokens == 0) return Check{};
+  if (dy && dy == y && lddy != ldy && expert_rows > 1)
+    return fail(MXGG_ERR_SHAPE, "dy is y with another leading dimension (lddy=%lld, ldy=%lld)", lddy, ldy);
   const int size = dtype_size(dtype);
   MXGG_TRY(check_elem_ptr(dout, size, "dout"));
   MXGG_TRY(check_elem_ptr(y, size, "y", expert_rows == 0));

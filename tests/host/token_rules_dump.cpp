@@ -1,0 +1,29 @@
+// Host build of the rules of the token and int8 operators (token_launch.hpp), written
+// out for the CPU tests as rows of int32.
+//   token_rules_dump chunks OUT    n, cols, col, start, skip of every chunk of rows of n to 2100 columns
+#include <cstdint>
+#include <cstdio>
+#include <cstring>
+#include <vector>
+
+#include "../../moe_grouped_block_mx_amd/csrc/token_launch.hpp"
+
+int main(int argc, char** argv) {
+  if (argc < 3) return 2;
+  std::vector<int32_t> out;
+  if (!std::strcmp(argv[1], "chunks")) {
+    for (int n : {4, 8})
+      for (int cols = n; cols <= 2100; ++cols)
+        for (int col = 0; col < cols; col += n) {
+          const mxgg::RowChunk c = mxgg::row_chunk(col, cols, n);
+          for (int v : {n, cols, col, c.start, c.skip}) out.push_back(v);
+        }
+  } else {
+    return 2;
+  }
+  FILE* f = std::fopen(argv[2], "wb");
+  if (!f) return 3;
+  std::fwrite(out.data(), 4, out.size(), f);
+  std::fclose(f);
+  return 0;
+}

@@ -188,3 +188,31 @@ def test_streams_and_graph(T):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), seed
+
+
+# Rows whose last chunk is short, its lane in the wave of its neighbour's, in another
+# one (513 to 519 bf16 columns, 257 fp32, for few tokens), and at the beginning of the
+# next trip over the row (2049); all parts of a chunk are left over once.
+@pytest.mark.parametrize("dt,C", [("bf16", c) for c in (9, 130, 257, 513, 514, 515, 516, 517, 518, 519, 1025, 1027, 1031, 1537,
+                                                         2049, 2052, 4103)]
+                         + [("f32", c) for c in (5, 66, 131, 257, 258, 259, 513, 514, 515, 769, 1025, 2051)])
+@pytest.mark.parametrize("T,k", [(1, 16), (40, 8), (300, 3)])
+def test_gradient_in_place_of_y(dt, C, T, k):
+    """dy over y against the fp64 reference of what y held before: a weight's gradient
+    is a sum of at most 64 products a lane."""
+    g = gen(C * T)
+    rows, _, counts = mxg.moe_sort(choices(g, T, k, 8, 0.1), 8)
+    n = T * k
+    x = rows_of(g, T, C, DT[dt], 3, 1)
+    w = torch.softmax(torch.randn((T, k), device="cuda", generator=g), 1)
+    room = rows_of(g, n + 2, C + 2, DT[dt], 1, 1)
+    before = f64(room)
+    y = room[1:n + 1, 1:C + 1]
+    wy, ww, size = ot.combine_bwd(f64(x), f64(y), host(rows), host(w))
+    dy, dw = mxg.moe_combine_bwd(x, y, rows, w, dy=y)
+    after = f64(room)
+    assert dy.data_ptr() == y.data_ptr() and not np.isnan(wy).any()
+    assert (np.abs(after[1:n + 1, 1:C + 1] - wy) <= (HALF_STEP[dt] + 2 * U) * np.abs(wy)).all()
+    assert (np.abs(f64(dw) - ww) <= 256 * U * size).all()
+    after[1:n + 1, 1:C + 1] = before[1:n + 1, 1:C + 1]
+    assert np.array_equal(after, before)                        # what surrounds the rows stays

@@ -1,0 +1,42 @@
+"""The rules of the token and int8 operators, compiled for the host."""
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    """rules(mode, columns, *args): the rows that a mode writes."""
+    cxx = shutil.which("hipcc")
+    if cxx is None:
+        pytest.skip("hipcc not available")
+    d = tmp_path_factory.mktemp("token")
+    exe, out = str(d / "token_rules_dump"), str(d / "dump.bin")
+    subprocess.run([cxx, "-O2", "-std=c++17", "-o", exe, os.path.join(HERE, "host", "token_rules_dump.cpp")], check=True,
+                   capture_output=True)
+
+    def run(mode, columns, *args):
+        subprocess.run([exe, mode, out, *map(str, args)], check=True)
+        return np.fromfile(out, dtype=np.int32).reshape(-1, columns)
+    return run
+
+
+def test_a_columns_gradient_is_stored_by_one_lane(rules):
+    """What a lane of combine's gradient stores, elements start + skip up to start +
+    n, is no other lane's, and all together are the row. (Where the gradient goes
+    over y, a lane that stored its neighbour's elements would do so before another
+    wave has read them.) What it loads lies inside the row."""
+    n, cols, col, start, skip = rules("chunks", 5).T.astype(np.int64)
+    assert (start >= 0).all() and (start + n <= cols).all() and (skip >= 0).all() and (skip < n).all()
+    first = start + skip
+    assert (first == col).all()
+    last = np.minimum(col + n, cols)
+    assert (start + n == last).all()
+    # chunk after chunk of one row, each begins where the one before it ends
+    same = cols[1:] == cols[:-1]
+    assert (first[1:][same] == last[:-1][same]).all() and (last[:-1][~same] == cols[:-1][~same]).all()

@@ -164,3 +164,10 @@ def test_host_memory_is_refused():
                  lambda: mx.moe_combine_bwd(x, torch.zeros(8, 8), ids, torch.zeros(4, 2)),
                  lambda: mx.dropout(x, 0.1, state)):
         refused(call, "GPU")
+
+
+def test_gradient_over_y_has_its_strides():
+    assert bwd(ldy=8, lddy=9) == SHAPE and "leading dimension" in last()
+    assert bwd(ldy=9, lddy=9) == HIP and bwd(ldy=8, lddy=9, R=1) == HIP
+    other = ctypes.c_void_p(0x900000)
+    assert bwd(ldy=8, lddy=9, dy=other) == HIP
