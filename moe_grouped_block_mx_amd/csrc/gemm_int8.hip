@@ -258,7 +258,7 @@ struct Int8Stream {
     nt = (int)((p.n + T::TN - 1) / T::TN);
     int64_t* both = reinterpret_cast<int64_t*>(smem);     // the ring is not in use yet
     block_prefix64<kThreads>(G, [&](int g) {
-      return (int64_t)((p.sp.m[g] + T::TM - 1) / T::TM) << 32 | p.sp.m[g];
+      return (int64_t)token_pieces(p.sp.m[g], T::TM) << 32 | p.sp.m[g];
     }, both, both + kMaxExperts + 1);
     for (int g = threadIdx.x; g <= G; g += kThreads) {
       rows_at[g] = (int32_t)both[g];
@@ -546,7 +546,7 @@ __device__ __forceinline__ Piece find_piece(const SplitArgs& sp, int seg, int ea
   uint64_t sum = 0;
   for (int i = 0; i < per; ++i) {
     const int e = lane * per + i, m = e < sp.G ? sp.m[e] : 0;
-    sum += (uint64_t)((m + each - 1) / each) << 32 | (uint32_t)m;
+    sum += (uint64_t)token_pieces(m, each) << 32 | (uint32_t)m;
   }
   uint64_t upto = sum;
 #pragma unroll
@@ -560,7 +560,7 @@ __device__ __forceinline__ Piece find_piece(const SplitArgs& sp, int seg, int ea
   int left = uniform(seg - (int)(before >> 32)), row = uniform((int)(uint32_t)before);
   p.g = uniform(owner) * per;
   for (; p.g < sp.G; ++p.g) {
-    const int n = (sp.m[p.g] + each - 1) / each;
+    const int n = token_pieces(sp.m[p.g], each);
     if (left < n) break;
     left -= n;
     row += sp.m[p.g];

@@ -112,10 +112,14 @@ struct Int8Params {
   int32_t k;
   SplitArgs sp;
 };
-// Pieces of at most `each` tokens of one expert
+// Pieces of at most `each` of an expert's m tokens (any m below 2^31: the sum is
+// unsigned)
+__host__ __device__ inline int32_t token_pieces(int32_t m, int each) {
+  return (int32_t)(((uint32_t)m + (uint32_t)each - 1) / (uint32_t)each);
+}
 inline int64_t int8_pieces(const SplitArgs& sp, int each) {
   int64_t n = 0;
-  for (int g = 0; g < sp.G; ++g) n += ((int64_t)sp.m[g] + each - 1) / each;
+  for (int g = 0; g < sp.G; ++g) n += token_pieces(sp.m[g], each);
   return n;
 }
 // The forms of the product: tiles of 256 channels x 256 tokens, of 128 x 128, and

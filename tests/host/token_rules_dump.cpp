@@ -1,8 +1,10 @@
 // Host build of the rules of the token and int8 operators (token_launch.hpp), written
 // out for the CPU tests as rows of int32.
 //   token_rules_dump chunks OUT    n, cols, col, start, skip of every chunk of rows of n to 2100 columns
+//   token_rules_dump pieces OUT M...  m, each, pieces for the heights of the int8 product's tiles
 #include <cstdint>
 #include <cstdio>
+#include <cstdlib>
 #include <cstring>
 #include <vector>
 
@@ -18,6 +20,12 @@ int main(int argc, char** argv) {
           const mxgg::RowChunk c = mxgg::row_chunk(col, cols, n);
           for (int v : {n, cols, col, c.start, c.skip}) out.push_back(v);
         }
+  } else if (!std::strcmp(argv[1], "pieces")) {
+    for (int a = 3; a < argc; ++a)
+      for (int each : {16, 32, 64, 128, 256}) {
+        const int m = (int)std::strtol(argv[a], nullptr, 10);
+        for (int v : {m, each, mxgg::token_pieces(m, each)}) out.push_back(v);
+      }
   } else {
     return 2;
   }

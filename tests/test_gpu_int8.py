@@ -221,3 +221,23 @@ def test_streams_and_graph():
             graph.replay()
             torch.cuda.synchronize()
             assert torch.equal(out, want), seed
+
+
+@pytest.mark.parametrize("splits", [[2 ** 31 - 1], [7, 2 ** 31 - 20, 12]])
+def test_most_rows(splits):
+    """2^31 - 1 rows, nearly all of one expert, whose last tile would end past 2^31."""
+    M, K, G = sum(splits), 16, len(splits)
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("60 GiB of memory are not free")
+    a_q = torch.empty((M, K), dtype=torch.int8, device="cuda").fill_(2)
+    a_q[-300:] = 3
+    w_q = torch.ones((G, K), dtype=torch.int8, device="cuda")
+    w_s = torch.arange(1.0, G + 1, device="cuda")
+    a_s = torch.empty(M, device="cuda").fill_(0.5)
+    out = torch.empty((M, 1), dtype=torch.bfloat16, device="cuda").fill_(-1)
+    mxg.grouped_fwd(a_q, a_s, w_q, w_s, splits, 1, K, "int8", "int8", out=out)
+    at = 0
+    for g, m in enumerate(splits):
+        plain = min(m, max(M - 300 - at, 0))
+        assert bool((out[at:at + plain] == 16 * (g + 1)).all()) and bool((out[at + plain:at + m] == 24 * (g + 1)).all())
+        at += m

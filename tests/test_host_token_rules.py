@@ -40,3 +40,10 @@ def test_a_columns_gradient_is_stored_by_one_lane(rules):
     # chunk after chunk of one row, each begins where the one before it ends
     same = cols[1:] == cols[:-1]
     assert (first[1:][same] == last[:-1][same]).all() and (last[:-1][~same] == cols[:-1][~same]).all()
+
+
+def test_pieces_of_any_number_of_tokens(rules):
+    """Tiles of an expert's tokens, up to the most rows that the product takes."""
+    m, each, pieces = rules("pieces", 3, 0, 1, 15, 16, 17, 255, 256, 257, 10 ** 6, 2 ** 30, 2 ** 31 - 257, 2 ** 31 - 256,
+                            2 ** 31 - 255, 2 ** 31 - 128, 2 ** 31 - 1).T.astype(np.int64)
+    assert (pieces == -(-m // each)).all() and len(m) == 75
