@@ -27,11 +27,12 @@ class TokenPlan:
     def __init__(self, ids, experts):
         self.rows, self.choices, self.counts = L.mxgg_moe_sort(ids, experts)
         self._splits = None
+        self._captured = torch.cuda.is_current_stream_capturing()   # every replay then counts anew
 
     def m_splits(self):
         """counts on the host, what the grouped GEMMs take (the first call waits
-        for the device)."""
-        if self._splits is None:
+        for the device, of a captured plan every call)."""
+        if self._splits is None or self._captured:
             self._splits = self.counts.tolist()
         return self._splits
 

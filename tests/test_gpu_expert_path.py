@@ -220,3 +220,19 @@ def test_example_block():
     want, size = ot.combine(f64(z), host(rows), f64(weights))
     assert (np.abs(f64(back) - want) <= 2.0 ** -8 * np.abs(want) + 8 * U * size).all()
     assert torch.equal(out, x + back)
+
+
+def test_splits_of_a_captured_plan():
+    """Every replay sorts other choices: the counts are read anew."""
+    T, k, E, C = 40, 2, 5, 24
+    ids, x, _, _ = inputs(T, k, E, C, 0.2)
+    TokenPlan(ids, E)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plan = TokenPlan(ids, E)
+    for seed in range(3):
+        ids.copy_(inputs(T, k, E, C, 0.2, seed=seed)[0])
+        graph.replay()
+        want = [int((ids == e).sum()) for e in range(E)]
+        assert plan.m_splits() == want, seed
+        assert dispatch(x, plan).shape == (sum(want), C)
