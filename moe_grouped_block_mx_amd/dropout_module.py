@@ -6,6 +6,12 @@ call and of the element's place, and the backward pass draws it again.
     drop = Dropout(0.1, state, call=0)     # another call number for each place in the model
     y = drop(branch, residual=x)
     state.advance()                        # after each forward pass
+
+A forward that is run again in the backward pass (activation checkpointing) reads the
+state then. Advance after the backward pass, or give the checkpointed function the
+state as an argument, which it gets again:
+
+    y = checkpoint(lambda x, s: drop(x, state=s), x, state.tensor, use_reentrant=False)
 """
 import torch
 from torch.autograd.function import once_differentiable
@@ -24,12 +30,13 @@ class DropoutState:
 
     def advance(self):
         """New masks from here on. A backward pass still to come keeps the step of
-        its forward pass."""
+        its forward pass (one that runs the forward again: see above)."""
         self.tensor = self.tensor + self._one
 
     def advance_(self):
         """The same in place, for a captured graph (each replay then draws new
-        masks). A backward pass still to come of an earlier step raises."""
+        masks). A backward pass still to come of an earlier step raises; one that runs
+        the forward again has to come first."""
         self.tensor[1:].add_(1)
 
 
@@ -55,7 +62,8 @@ class _DropoutFn(torch.autograd.Function):
 class Dropout(torch.nn.Module):
     """residual + x / (1 - p) where kept, residual where dropped; x bf16 or fp32
     [..., features], residual like it or None. p is rounded to a multiple of 2^-16.
-    In eval mode nothing is dropped."""
+    forward's state: the int64 [2] to draw from, by default the DropoutState's. In eval
+    mode nothing is dropped."""
 
     def __init__(self, p, state, call=0):
         super().__init__()
@@ -65,9 +73,9 @@ class Dropout(torch.nn.Module):
             raise ValueError(f"call={call} outside [0, 2^32)")
         self.p, self.state, self.call = p, state, call
 
-    def forward(self, x, residual=None):
+    def forward(self, x, residual=None, state=None):
         if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):
             raise ValueError(f"residual must be {x.dtype} {tuple(x.shape)}, got {residual.dtype} {tuple(residual.shape)}")
         if not self.training or self.p == 0:
             return x if residual is None else residual + x
-        return _DropoutFn.apply(x, residual, self.state.tensor, self.p, self.call)
+        return _DropoutFn.apply(x, residual, self.state.tensor if state is None else state, self.p, self.call)

@@ -236,3 +236,21 @@ def test_splits_of_a_captured_plan():
         want = [int((ids == e).sum()) for e in range(E)]
         assert plan.m_splits() == want, seed
         assert dispatch(x, plan).shape == (sum(want), C)
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_dropout_of_a_recomputed_forward(reentrant):
+    """A forward that runs again in the backward pass, after the step went on, draws
+    the mask of the state that it was given."""
+    from torch.utils.checkpoint import checkpoint
+    state = DropoutState(5)
+    drop = Dropout(0.5, state)
+    x = torch.randn((50, 64), device="cuda", requires_grad=True)
+    d = torch.randn((50, 64), device="cuda")
+    out = checkpoint(lambda x, s: drop(x * 1.0, residual=x, state=s), x, state.tensor, use_reentrant=reentrant,
+                     preserve_rng_state=False)
+    state.advance()
+    out.backward(d)
+    kept = torch.from_numpy(ot.dropout(np.zeros((50, 64)), 0.5, 5, 0, 0)[1]).cuda()
+    assert torch.equal(x.grad, torch.where(kept, 2 * d, 0) + d)
+    assert torch.equal(drop(x, state=torch.tensor([5, 0], device="cuda")) != 0, kept)
