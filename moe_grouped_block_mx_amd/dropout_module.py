@@ -21,7 +21,10 @@ from .layer_norm import _rows
 
 
 class DropoutState:
-    """Seed and step, int64 [2] on the device, shared by a model's dropouts."""
+    """Seed and step, int64 [2] on the device, shared by a model's dropouts. It is no
+    part of the modules' state_dict: a program that goes on from a checkpoint saves
+    and loads it beside the model, as it does an optimizer (else the masks of the first
+    steps come again)."""
 
     def __init__(self, seed, step=0, device=None):
         device = torch.device("cuda") if device is None else torch.device(device)
@@ -38,6 +41,15 @@ class DropoutState:
         masks). A backward pass still to come of an earlier step raises; one that runs
         the forward again has to come first."""
         self.tensor[1:].add_(1)
+
+    def state_dict(self):
+        """{"seed", "step"} as ints (waits for the device)."""
+        seed, step = self.tensor.tolist()
+        return {"seed": seed, "step": step}
+
+    def load_state_dict(self, saved):
+        """In place, as advance_: a captured graph goes on from there."""
+        self.tensor.copy_(torch.tensor([saved["seed"], saved["step"]], dtype=torch.int64))
 
 
 class _DropoutFn(torch.autograd.Function):

@@ -254,3 +254,12 @@ def test_dropout_of_a_recomputed_forward(reentrant):
     kept = torch.from_numpy(ot.dropout(np.zeros((50, 64)), 0.5, 5, 0, 0)[1]).cuda()
     assert torch.equal(x.grad, torch.where(kept, 2 * d, 0) + d)
     assert torch.equal(drop(x, state=torch.tensor([5, 0], device="cuda")) != 0, kept)
+
+
+def test_dropout_goes_on_where_it_was_saved():
+    x, state = torch.ones((64, 64), device="cuda"), DropoutState(2)
+    state.advance()
+    saved, want = state.state_dict(), Dropout(0.5, state)(x)
+    other = DropoutState(9)
+    other.load_state_dict(saved)
+    assert torch.equal(Dropout(0.5, other)(x), want)

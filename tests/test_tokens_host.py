@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import moe_grouped_block_mx_amd as mx
+from moe_grouped_block_mx_amd.dropout_module import DropoutState
 
 L = mx.lib
 P = ctypes.c_void_p(0x100000)      # a fake aligned device address
@@ -171,3 +172,16 @@ def test_gradient_over_y_has_its_strides():
     assert bwd(ldy=9, lddy=9) == HIP and bwd(ldy=8, lddy=9, R=1) == HIP
     other = ctypes.c_void_p(0x900000)
     assert bwd(ldy=8, lddy=9, dy=other) == HIP
+
+
+def test_dropout_state_is_saved_and_loaded():
+    state = DropoutState(-5, step=2, device="cpu")
+    state.advance()
+    saved = state.state_dict()
+    assert saved == {"seed": -5, "step": 3}
+    other = DropoutState(1, device="cpu")
+    held = other.tensor
+    other.load_state_dict(saved)
+    assert other.tensor is held and held.tolist() == [-5, 3]     # in place: a captured graph reads there
+    other.advance_()
+    assert other.state_dict() == {"seed": -5, "step": 4} and saved["step"] == 3
