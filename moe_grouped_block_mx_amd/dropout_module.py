@@ -3,7 +3,7 @@
 call and of the element's place, and the backward pass draws it again.
 
     state = DropoutState(seed=1)
-    drop = Dropout(0.1, state, call=0)     # another call number for each place in the model
+    drop = Dropout(0.1, state)             # one for each place in the model: a call number of its own
     y = drop(branch, residual=x)
     state.advance()                        # after each forward pass
 
@@ -30,6 +30,19 @@ class DropoutState:
         device = torch.device("cuda") if device is None else torch.device(device)
         self.tensor = torch.tensor([seed, step], dtype=torch.int64, device=device)
         self._one = torch.tensor([0, 1], dtype=torch.int64, device=device)
+        self._calls, self._given = set(), set()    # the numbers of its dropouts, and those given out here
+
+    def _number(self, call):
+        """The caller's number, or for None the first that no dropout has."""
+        if call is None:
+            call = next(n for n in range(len(self._calls) + 1) if n not in self._calls)
+            self._given.add(call)
+        elif not 0 <= call < 1 << 32:
+            raise ValueError(f"call={call} outside [0, 2^32)")
+        elif call in self._given:
+            raise ValueError(f"call={call} was given to another dropout of this state, which would draw the same mask")
+        self._calls.add(call)
+        return call
 
     def advance(self):
         """New masks from here on. A backward pass still to come keeps the step of
@@ -74,16 +87,16 @@ class _DropoutFn(torch.autograd.Function):
 class Dropout(torch.nn.Module):
     """residual + x / (1 - p) where kept, residual where dropped; x bf16 or fp32
     [..., features], residual like it or None. p is rounded to a multiple of 2^-16.
-    forward's state: the int64 [2] to draw from, by default the DropoutState's. In eval
-    mode nothing is dropped."""
+    call: the number that tells a state's dropouts apart, by default the first that
+    none of them has (by the order in which they are made); two that were given the
+    same draw the same mask. forward's state: the int64 [2] to draw from, by default the
+    DropoutState's. In eval mode nothing is dropped."""
 
-    def __init__(self, p, state, call=0):
+    def __init__(self, p, state, call=None):
         super().__init__()
         if not 0 <= p <= 1:
             raise ValueError(f"p must be in [0, 1], got {p}")
-        if not 0 <= call < 1 << 32:
-            raise ValueError(f"call={call} outside [0, 2^32)")
-        self.p, self.state, self.call = p, state, call
+        self.p, self.state, self.call = p, state, state._number(call)
 
     def forward(self, x, residual=None, state=None):
         if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype):

@@ -263,3 +263,10 @@ def test_dropout_goes_on_where_it_was_saved():
     other = DropoutState(9)
     other.load_state_dict(saved)
     assert torch.equal(Dropout(0.5, other)(x), want)
+
+
+def test_two_dropouts_of_a_state_draw_two_masks():
+    x, state = torch.ones((64, 64), device="cuda"), DropoutState(2)
+    one, two = Dropout(0.5, state), Dropout(0.5, state)
+    assert 0.3 < float(((one(x) == 0) == (two(x) == 0)).double().mean()) < 0.7
+    assert torch.equal(one(x), mxg.dropout(x, 0.5, state.tensor, 0))

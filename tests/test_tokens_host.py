@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import moe_grouped_block_mx_amd as mx
-from moe_grouped_block_mx_amd.dropout_module import DropoutState
+from moe_grouped_block_mx_amd.dropout_module import Dropout, DropoutState
 
 L = mx.lib
 P = ctypes.c_void_p(0x100000)      # a fake aligned device address
@@ -185,3 +185,14 @@ def test_dropout_state_is_saved_and_loaded():
     assert other.tensor is held and held.tolist() == [-5, 3]     # in place: a captured graph reads there
     other.advance_()
     assert other.state_dict() == {"seed": -5, "step": 4} and saved["step"] == 3
+
+
+def test_dropouts_of_a_state_have_numbers_of_their_own():
+    state = DropoutState(3, device="cpu")
+    assert [Dropout(0.1, state).call for _ in range(3)] == [0, 1, 2]
+    other = DropoutState(3, device="cpu")
+    assert [Dropout(0.1, other, call=c).call for c in (1, 5, 5)] == [1, 5, 5]    # the caller's may meet
+    assert [Dropout(0.1, other).call for _ in range(5)] == [0, 2, 3, 4, 6]
+    refused(lambda: Dropout(0.1, other, call=4), "call=4")                       # ... but not one that was given out
+    assert Dropout(0.1, other, call=7).call == 7 and Dropout(0.1, other).call == 8
+    refused(lambda: Dropout(0.1, other, call=1 << 32), "call")
