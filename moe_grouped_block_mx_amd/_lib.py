@@ -631,8 +631,17 @@ def _quantize_int8(x, flags, q, scales):
     return q, scales
 
 
+def _int8_splits(m_splits):
+    """The array of _splits, faster for a list of ints, and its length."""
+    vals = m_splits if isinstance(m_splits, (list, tuple)) else list(m_splits)
+    try:
+        return _host_array(ctypes.c_int64, "q", vals, len(vals)), len(vals)
+    except TypeError:           # 2.0, as the other formats take it
+        return _splits(vals)
+
+
 def _grouped_fwd_int8(a_q, a_s, w_q, w_s, m_splits, N, K, out, ws):
-    G = len(m_splits)
+    splits, G = _int8_splits(m_splits)
     M = a_q.shape[0] if a_q.dim() else 0
     _expect(a_q, "a_q", (M, K), _i8_t)
     _expect(a_s, "a_s", (M,), _f32_t)
@@ -641,8 +650,7 @@ def _grouped_fwd_int8(a_q, a_s, w_q, w_s, m_splits, N, K, out, ws):
     out = a_q.new_empty((M, N), dtype=_bf16_t) if out is None else _expect(out, "out", (M, N), _bf16_t)
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib.mxgg_grouped_fwd(a_q.data_ptr(), a_s.data_ptr(), INT8, w_q.data_ptr(), w_s.data_ptr(), INT8,
-                                _host_array(ctypes.c_int64, "q", m_splits, G), G, M, N, K, out.data_ptr(), _at(ws),
-                                ws_bytes, _stream_of(a_q)))
+                                splits, G, M, N, K, out.data_ptr(), _at(ws), ws_bytes, _stream_of(a_q)))
     return out
 
 

@@ -3,6 +3,7 @@ refuse bad arguments before any HIP call, and the binding refuses buffers of the
 wrong shape, type or layout before the library sees them."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -196,3 +197,13 @@ def test_dropouts_of_a_state_have_numbers_of_their_own():
     refused(lambda: Dropout(0.1, other, call=4), "call=4")                       # ... but not one that was given out
     assert Dropout(0.1, other, call=7).call == 7 and Dropout(0.1, other).call == 8
     refused(lambda: Dropout(0.1, other, call=1 << 32), "call")
+
+
+def test_int8_splits_are_any_numbers():
+    """Whatever the other formats take: they all get as far as the check of the memory."""
+    q, s = torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    wq, ws = torch.zeros(2 * 8, 64, dtype=torch.int8), torch.zeros(2 * 8)
+    for splits in ([3, 1], (3, 1), [3.0, 1.0], (m for m in (3, 1)), (m for m in (3.0, 1.0)), torch.tensor([3, 1]), torch.tensor([3., 1.]),
+                   np.array([3, 1]), map(int, "31")):
+        refused(lambda: mx.grouped_fwd(q, s, wq, ws, splits, 8, 64, "int8", "int8"), "GPU")
+    refused(lambda: mx.grouped_fwd(q, s, wq, ws, (m for m in (3, 1, 0)), 8, 64, "int8", "int8"), "w_q must be")
