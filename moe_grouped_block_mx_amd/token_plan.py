@@ -16,8 +16,8 @@ from .layer_norm import _rows
 
 
 class TokenPlan:
-    """The choices ids (int32 or int64 [tokens, top_k]) in the order of their
-    experts; a choice outside [0, experts) is dropped.
+    """The choices ids (int32 or int64 [tokens, top_k], any strides) in the order of
+    their experts; a choice outside [0, experts) is dropped.
 
     rows     int32 [tokens, top_k]: the place of each choice, ~place where dropped
     choices  int32 [tokens * top_k]: the choice at each place
@@ -25,6 +25,8 @@ class TokenPlan:
     """
 
     def __init__(self, ids, experts):
+        if ids.dim() == 2 and ids.numel():
+            ids = _rows(ids)
         self.rows, self.choices, self.counts = L.mxgg_moe_sort(ids, experts)
         self._splits = None
         self._captured = torch.cuda.is_current_stream_capturing()   # every replay then counts anew

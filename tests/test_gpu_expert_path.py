@@ -270,3 +270,11 @@ def test_two_dropouts_of_a_state_draw_two_masks():
     one, two = Dropout(0.5, state), Dropout(0.5, state)
     assert 0.3 < float(((one(x) == 0) == (two(x) == 0)).double().mean()) < 0.7
     assert torch.equal(one(x), mxg.dropout(x, 0.5, state.tensor, 0))
+
+
+def test_plan_of_transposed_choices():
+    ids, x, _, _ = inputs(30, 3, 5, 16, 0.1)
+    plan, turned = TokenPlan(ids, 5), TokenPlan(ids.t().contiguous().t(), 5)
+    assert torch.equal(plan.rows, turned.rows) and torch.equal(plan.counts, turned.counts)
+    same = TokenPlan(ids[:1].expand(7, 3), 5)
+    assert torch.equal(same.rows, TokenPlan(ids[:1].expand(7, 3).contiguous(), 5).rows)

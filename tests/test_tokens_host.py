@@ -9,6 +9,7 @@ import torch
 
 import moe_grouped_block_mx_amd as mx
 from moe_grouped_block_mx_amd.dropout_module import Dropout, DropoutState
+from moe_grouped_block_mx_amd.token_plan import TokenPlan
 
 L = mx.lib
 P = ctypes.c_void_p(0x100000)      # a fake aligned device address
@@ -207,3 +208,11 @@ def test_int8_splits_are_any_numbers():
                    np.array([3, 1]), map(int, "31")):
         refused(lambda: mx.grouped_fwd(q, s, wq, ws, splits, 8, 64, "int8", "int8"), "GPU")
     refused(lambda: mx.grouped_fwd(q, s, wq, ws, (m for m in (3, 1, 0)), 8, 64, "int8", "int8"), "w_q must be")
+
+
+def test_plan_takes_any_strides():
+    ids = torch.zeros(4, 6, dtype=torch.int32)
+    for view in (ids.t(), ids[:, ::2], ids[:1].expand(5, 6), ids[:, :1].expand(4, 3)):
+        refused(lambda: TokenPlan(view, 4), "GPU")
+    for bad in (ids[0], ids.float(), ids[None]):
+        refused(lambda: TokenPlan(bad, 4), "^(?!.*GPU)")
