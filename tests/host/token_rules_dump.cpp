@@ -1,6 +1,8 @@
 // Host build of the rules of the token and int8 operators (token_launch.hpp), written
 // out for the CPU tests as rows of int32.
 //   token_rules_dump chunks OUT    n, cols, col, start, skip of every chunk of rows of n to 2100 columns
+//   token_rules_dump form OUT CUS N K M...   the int8 product's form for M... rows of the experts, then how
+//                                            many forms there are
 //   token_rules_dump pieces OUT M...  m, each, pieces for the heights of the int8 product's tiles
 #include <cstdint>
 #include <cstdio>
@@ -20,6 +22,11 @@ int main(int argc, char** argv) {
           const mxgg::RowChunk c = mxgg::row_chunk(col, cols, n);
           for (int v : {n, cols, col, c.start, c.skip}) out.push_back(v);
         }
+  } else if (!std::strcmp(argv[1], "form")) {
+    mxgg::SplitArgs sp{};
+    for (int a = 6; a < argc; ++a) sp.m[sp.G++] = (int)std::strtol(argv[a], nullptr, 10);
+    out.push_back(mxgg::int8_form(sp, std::atoll(argv[4]), std::atoll(argv[5]), std::atoi(argv[3])));
+    out.push_back(mxgg::kInt8Few44 + 1);
   } else if (!std::strcmp(argv[1], "pieces")) {
     for (int a = 3; a < argc; ++a)
       for (int each : {16, 32, 64, 128, 256}) {
