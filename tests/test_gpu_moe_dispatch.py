@@ -216,3 +216,11 @@ def test_gradient_in_place_of_y(dt, C, T, k):
     assert (np.abs(f64(dw) - ww) <= 256 * U * size).all()
     after[1:n + 1, 1:C + 1] = before[1:n + 1, 1:C + 1]
     assert np.array_equal(after, before)                        # what surrounds the rows stays
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("k", [6, 7, 9, 10, 11, 12, 13, 14, 15])
+def test_rows_of_any_top_k(dt, k):
+    """Numbers of choices between the kernels' own."""
+    test_rows(dt, 29, k, 40, 1033, 3, 1, 0.2)
+    test_rows(dt, 50, k, 17, 5, 1, 0, 0.1)
