@@ -393,12 +393,13 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(TokenParams p, int
 }
 
 // The elements of a chunk that are the lane's own. In rows of whole chunks (or of
-// single elements) all are; else the last chunk's first `skip` are its neighbour's,
-// and where the gradient goes over y itself they are not to be written: the neighbour
-// may not have read them yet.
+// single elements) all are; else the last chunk's first `skip` are its neighbour's, and
+// where the gradient goes over y itself (`over`) they are not to be written: the
+// neighbour may not have read them yet. (Elsewhere they get the same bits twice, as in
+// dispatch, which is faster: 65536 x 125 bf16, eight choices, 76 us for 82.)
 template <class C, bool RAGGED>
 struct Own {
-  __device__ __forceinline__ explicit Own(int) {}
+  __device__ __forceinline__ Own(int, bool) {}
   __device__ __forceinline__ C of(const C& c) const { return c; }
   template <class E>
   __device__ __forceinline__ void store(C c, E* p) const { c.store(p); }
@@ -406,9 +407,9 @@ struct Own {
 template <class E>
 struct Own<Chunk<E>, true> {
   static constexpr int N = Chunk<E>::N;
-  int skip;
+  int keep;            // elements that are not written
   uint32_t mask[4];
-  __device__ __forceinline__ explicit Own(int skipped) : skip(skipped) {
+  __device__ __forceinline__ Own(int skip, bool over) : keep(over ? skip : 0) {
     constexpr int EACH = N / 4, BITS = 32 / EACH;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -421,19 +422,19 @@ struct Own<Chunk<E>, true> {
     for (int i = 0; i < 4; ++i) c.w[i] &= mask[i];
     return c;
   }
-  // the last N - skip, in 8, 4 and 2 bytes from the chunk's end on
+  // the last N - keep, in 8, 4 and 2 bytes from the chunk's end on
   __device__ __forceinline__ void store(Chunk<E> c, E* p) const {
-    if (skip == 0) return c.store(p);
-    const int n = N - skip;
+    if (keep == 0) return c.store(p);
+    const int n = N - keep;
     if constexpr (N == 8) {
       const uint32_t two = n & 4 ? c.w[1] : c.w[3], one = n & 2 ? (n & 4 ? c.w[0] : c.w[2]) : two;
       if (n & 4) memcpy(p + 4, c.w + 2, 8);
       if (n & 2) memcpy(p + (n & 4 ? 2 : 6), &two, 4);
-      if (n & 1) reinterpret_cast<uint16_t*>(p)[skip] = (uint16_t)(one >> 16);
+      if (n & 1) reinterpret_cast<uint16_t*>(p)[keep] = (uint16_t)(one >> 16);
     } else {
       const uint32_t one = n & 2 ? c.w[1] : c.w[3];
       if (n & 2) memcpy(p + 2, c.w + 2, 8);
-      if (n & 1) memcpy(p + skip, &one, 4);
+      if (n & 1) memcpy(p + keep, &one, 4);
     }
   }
 };
@@ -455,7 +456,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(TokenParams p)
       for (int col = lane * N; col < p.cols; col += L * N) {
         const RowChunk chunk = row_chunk(col, p.cols, N);
         const int at = chunk.start;
-        const Own<C, RAGGED> own(chunk.skip);
+        const Own<C, RAGGED> own(chunk.skip, p.out == p.y);
         C c, y[K], zero{};
         c.load(d + at);
 #pragma unroll

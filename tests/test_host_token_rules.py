@@ -27,10 +27,10 @@ def rules(tmp_path_factory):
 
 
 def test_a_columns_gradient_is_stored_by_one_lane(rules):
-    """What a lane of combine's gradient stores, elements start + skip up to start +
-    n, is no other lane's, and all together are the row. (Where the gradient goes
-    over y, a lane that stored its neighbour's elements would do so before another
-    wave has read them.) What it loads lies inside the row."""
+    """What a lane of combine's gradient stores where that goes over y, elements start +
+    skip up to start + n, is no other lane's, and all together are the row. (One that
+    stored its neighbour's elements would do so before another wave has read them.)
+    What it loads lies inside the row."""
     n, cols, col, start, skip = rules("chunks", 5).T.astype(np.int64)
     assert (start >= 0).all() and (start + n <= cols).all() and (skip >= 0).all() and (skip < n).all()
     first = start + skip
