@@ -147,18 +147,19 @@ hipError_t quant_int8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ldx
 // buffers that end with the tile's rows, so what lies past an end is zeros without
 // a comparison.
 //
-// 16x16x64 MFMAs, not 32x32x32: both do the same operations a cycle, but a 32x32
-// result moves twice the accumulators, and while one wave's MFMAs ran the other's
-// twelve reads of a turn took 770 cycles of the SIMD's (310 alone), with 16x16 510
-// (8192 x 8192 x 8192: 488 us and 440).
+// 16x16x64 MFMAs, not 32x32x32, whose results move twice the accumulators for the same
+// operations: 8192 x 8192 x 8192 takes 435 - 465 us with them and took 464 - 478 with those,
+// the two run in turns. (Of zeros for codes 346 - 356 and 312: without a limit by power it
+// would be the other way round.)
 //
 // What bounds it: large products of real codes the power of the card. 8192^3 in
-// 440 us is 2500 Tops (a bf16 product reaches half of that); with zeros for codes the
-// same launch takes 319 us, 3450 Tops. Issuing the loads between the MFMAs instead of
-// in the other turn, and letting a tile's stores run on into the next tile, changed
-// nothing (438 -> 444 us). Of 64 experts with 512 rows each on average (32768 x 4096
-// x 7168, 990 us) a quarter of the tiles' rows are past an expert's end. A 128 x 128
-// tile brings a byte for 128 operations and is bound by that: 52 bytes a ns and CU.
+// 435 - 465 us is 2360 - 2530 Tops (a bf16 product reaches half of that); the same launch
+// on zeros, the same instructions, takes 346 - 356, up to 3180 Tops. Issuing the loads
+// between the MFMAs instead of in the other turn, and letting a tile's stores run on into
+// the next tile, changed nothing. Of 64 experts with 512 rows each on average (32768 x
+// 4096 x 7168, 1020 - 1060 us) a quarter of the tiles' rows are past an expert's end. A
+// 128 x 128 tile brings a byte for 128 operations and is bound by that: 4096 x 4096 x
+// 4096, four tiles of 1 MB on every CU, takes 83 us, 51 bytes a ns and CU.
 
 #define MXGG_LDS __attribute__((address_space(3)))
 
@@ -532,8 +533,8 @@ __global__ __launch_bounds__(kThreads, 1) void split_int8_kernel(const Int8Param
 // neighbour does, which takes the address unit a cycle a lane.)
 //
 // What bounds it: reading the weights. 64 rows of 128 experts, 2048 x 7168: 110 us for
-// the 620 MB of the experts that have any (5.7 TB/s, as a plain read); one row, 4096 x
-// 7168: 7 us, of which 5.2 are for the 29 MB.
+// the 620 MB of the experts that have any (5.7 TB/s; a plain read reaches 6.4); one row,
+// 4096 x 7168: 7 us, of which 4.6 are for the 29 MB.
 
 constexpr int kFewWaves = 8;
 constexpr int few_slots(int nf, int mf) { return nf + mf <= 2 ? 4 : nf + mf <= 3 ? 3 : nf + mf <= 4 ? 4 : nf + mf <= 6 ? 3 : 2; }

@@ -288,12 +288,14 @@ hipError_t sort_any(const SortParams& p, hipStream_t st) {
 // Copies with places: nothing is computed that counts, so the design is about bytes in
 // flight. A lane has all loads of its choices on the way before it uses the first, and
 // workgroups that run at the same time have the pieces of the same rows. bf16, eight
-// choices a token, 128 experts: dispatch of 4096 x 4096 50 us (6.0 TB/s, the token's
+// choices a token, 128 experts: dispatch of 4096 x 4096 49 us (6.1 TB/s, the token's
 // row is read once), combine to 16384 x 7168 410 us (5.2 TB/s; with the rows in the
-// tokens' order 5.3), its gradient at 4096 x 4096 112 us (5.1 TB/s). A plain copy of
-// 2^30 bytes reaches 5.1. Rows shorter than a chunk have kernels of their own: with a
-// branch at every load for them combine took 450 us, and few tokens, whose time is much
-// that of bringing the code, 9.8 for 6 (8 x 1024, the gradient).
+// tokens' order 5.3), its gradient at 4096 x 4096 110 us (5.2 TB/s). A plain copy of
+// 2^30 bytes reaches 5.1, a plain read 6.4, a fill 6.9. Rows shorter than a chunk have
+// kernels of their own: with a branch at every load for them combine took 450 us, and
+// few tokens, whose time is much that of bringing the code, 9.8 for 5.7 (8 x 1024, the
+// gradient); so have, in the gradient, rows of whole chunks (then 4.9; 64 x 7168 13.0
+// and 9.1).
 
 constexpr int kRowThreads = 256;
 constexpr int64_t kRowGrid = 1 << 20;   // workgroups at most; they stay for the rest
@@ -561,9 +563,11 @@ template <class E, int K>
 hipError_t combine_bwd_wide(const TokenParams& p, hipStream_t st) {
   // Lanes that fit the row: fewer would leave few loads in flight, more would be idle;
   // but with few tokens, which leave CUs idle, a row's chunks all at once. Eight
-  // choices, us: 65536 x 128, 16 lanes 63, 32 99, 64 159; 65536 x 256, 16 130, 32 127, 64 195;
-  // 16384 x 1024, 64 115, 256 181; 16384 x 2048, 64 287, 256 238; 256 x 1024, 64 8.3, 256
-  // 6.3, and 1024 of them 10 and 15.
+  // choices, us with 16, 32, 64 and 256 lanes, the rule's marked: bf16 65536 x 128 60*, 85,
+  // 138, 407; 65536 x 256 115, 118*, 163, 443; 32768 x 512 118, 115, 117*, 245; 16384 x 1024
+  // 119, 118, 114*, 149; 16384 x 2048 291, 257, 234, 224*; 8192 x 7168 413, 407, 404, 396*;
+  // fp32 65536 x 128 116, 120*, 166, 418; 16384 x 1024 293, 258, 237, 224*; 256 tokens
+  // x 1024, bf16, 13, 8.8, 7.0, 5.5*, and 512 of them 13.9, 9.3, 7.1*, 7.0, 1024 15, 11, 8.4*, 11.
   if (p.cols < Chunk<E>::N) return combine_bwd<E, Single<E>, K, 16>(p, st);
   const int chunks = (p.cols + Chunk<E>::N - 1) / Chunk<E>::N;
   if (chunks <= 16) return combine_bwd<E, Chunk<E>, K, 16>(p, st);

@@ -34,7 +34,8 @@ inline int64_t sort_chunks(int64_t choices) {
 // itself; beyond, a launch between does it for all. Measured, us, without the launch
 // and with it: 32 chunks of 32 experts 7.0 and 8.0; 64 of 128 8.3 and 8.7, of 511 10.0
 // and 9.4; 128 of 128 10.9 and 11.6, of 511 13.5 and 13.4; 256 of 8 10.0 and 11.3, of
-// 128 13.9 and 14.3, of 511 18.7 and 16.6.
+// 128 13.9 and 14.3, of 511 18.7 and 16.6. (One limit for any number of experts costs
+// 0.6 us at 64 chunks of 511, 1.3 at 256 of 8, 0.4 at 256 of 128.)
 constexpr int64_t kSortDirect = 128;
 // A row of the table: whole 16 bytes
 __host__ __device__ inline int sort_table_row(int experts) { return (experts + 4) / 4 * 4; }
@@ -135,25 +136,28 @@ enum Int8Form { kInt8Big, kInt8Small, kInt8Few11, kInt8Few12, kInt8Few21, kInt8F
 // Measured, us (one expert unless said; tokens, channels, K; medians of replays, the
 // weights of several layers in turn; the form that the rule takes is marked):
 //                                    256    128    64 x 64  64 x 32  32 x 32  32 x 16  16 x 16
-//   1, 4096, 7168                     71     32      21       19       12       12       8.2*
-//   1, 8192, 1024                     18     10      6.7      6.0      5.2      4.5*     4.8
-//   32, 4096, 4096                    43     20      12       10       8.2      7.1*     8.3
-//   64, 4096, 4096                    44     20      12       10       9.1*     11       13
-//   256, 4096, 4096                   48     21      15*      21       26       29       38
-//   512, 4096, 4096                   48     22*     27       40       48       53       70
-//   512, 1111, 2000                   36     16      9.9*     13       16       15       17
-//   1024, 1024, 8192                  84     35      23*      32       40       50       63
-//   1024, 8192, 1024                  23     19*     40       60       95       87       140
-//   2048, 4096, 4096                  51     43*     92       148
-//   2048, 8192, 1024                  26*    32      78       119
-//   4096, 4096, 4096                  62*    78
-//   64 of 128 experts, 2048, 7168     171    128     148      141      147      126*     132
-//   256 of 32, 4096, 4096             141    126     128      120*     137      110      132
-//   1024 of 32, 4096, 4096            143    125*    144      153      193      191      251
-//   4096 of 32, 4096, 4096            188    153*
-//   8192 of 32, 4096, 4096            204*   221
-//   8192 of 64, 4096, 7168            520    482*
-//   16384 of 64, 4096, 7168           640*   730
+//   1, 4096, 7168                     71     31      21       20       13       12       8.4*
+//   1, 8192, 1024                     18     10      6.7      6.0      5.1      4.5*     4.8
+//   32, 4096, 4096                    43     20      12       10       8.3      7.2*     8.4
+//   64, 4096, 4096                    44     20      13       10       9.0*     11       13
+//   256, 4096, 4096                   49     21      15*      21       26       30       38
+//   512, 4096, 4096                   49     22*     27       40       49       54       71
+//   512, 1111, 2000                   33     16      9.9*     13       16       15       16
+//   1024, 1024, 8192                  86     35      23*      32       40       51       64
+//   1024, 4096, 4096                  49     24*     49       77       95       102      133
+//   1024, 8192, 1024                  24     19*     40       60       95       87       141
+//   2048, 4096, 4096                  52     41*     91       149
+//   2048, 8192, 1024                  27*    32      77       119
+//   4096, 4096, 4096                  67*    83
+//   64 of 128 experts, 2048, 7168     170    127     148      141      147      126*     132
+//   256 of 32, 4096, 4096             140    125     127      119*     137      110      131
+//   1024 of 32, 4096, 4096            141    125*    148      151      192      191      251
+//   2999 of 5, 1111, 2000             37     18*     39       49       71       71       101
+//   4096 of 32, 4096, 4096            189    149*
+//   8192 of 32, 4096, 4096            204*   219
+//   8192 of 64, 4096, 7168            522    488*
+//   16384 of 64, 4096, 7168           653*   746
+//   32768 of 64, 4096, 7168           1053*  1253
 // (32 x 64 and 16 x 32 are for the tokens in between, as 40 and 20.)
 inline Int8Form int8_form(const SplitArgs& sp, int64_t n, int64_t k, int num_cus) {
   struct Option {
